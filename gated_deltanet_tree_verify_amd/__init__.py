@@ -16,6 +16,19 @@ is no CPU or PyTorch fallback, and a missing library raises.
     accept(parent, draft_tok, verify_tok)           -> (accepted, accept_len, bonus_tok)
     path(parent, accepted, max_path)                -> (path, path_len)
     index(parent)                                   -> (depth, anc)
+
+Serving operators next to the tree calls:
+
+    prefill(q, k, v, alpha, beta, cu, S, src, dst)  -> out   (gdn_prefill)
+    step(q, k, v, alpha, beta, S, src, dst)         -> out   (gdn_step)
+    tree_attention(q, k, v, parent, k_cache, v_cache, pages, length, scale)
+                                                    -> out   (gdn_tree_attention)
+    page_fork(table, length, ref, src, dst, page)   -> copies
+    page_extend(table, length, ref, dst, add, page) -> begin
+    page_free(table, length, ref, done, page)
+    page_compact(table, length, ref, page)          -> (copies, count)
+    page_copy(cache, copies, count)
+    kv_commit(k_cache, v_cache, table, dst, begin, k, v, path, add)
 """
 from __future__ import annotations
 
@@ -24,6 +37,10 @@ import os
 import threading
 
 __all__ = ["load", "lib_path", "verify", "branch_verify", "commit", "commit_verify", "build_tree", "accept", "path", "Launch", "index", "status_string",
+           "prefill", "step", "tree_attention", "page_fork", "page_extend", "page_free",
+           "page_compact", "page_copy", "kv_commit",
+           "FAULT_BAD_SLOT", "FAULT_BAD_LENGTH", "FAULT_BAD_PAGE", "FAULT_BAD_GROUP",
+           "FAULT_NO_PAGE",
            "GdnError", "FAULT_BAD_PARENT", "FAULT_BAD_PATH", "DTYPE_F32", "DTYPE_BF16",
            "MAX_NODES", "MAX_DIM", "ABI_VERSION", "build"]
 
@@ -32,14 +49,19 @@ _LIB_NAME = "libgdntree.so"
 
 FAULT_BAD_PARENT = 1
 FAULT_BAD_PATH = 2
+FAULT_BAD_SLOT = 4
+FAULT_BAD_LENGTH = 8
+FAULT_BAD_PAGE = 16
+FAULT_BAD_GROUP = 32
+FAULT_NO_PAGE = 64
 DTYPE_F32 = 0
 DTYPE_BF16 = 1
-DTYPE_F16 = 2     # pseudo-values of commit_verify only
+DTYPE_F16 = 2     # pseudo-values of commit_verify, tree_attention
 MAX_NODES = 128
 MAX_DIM = 128
 MAX_CANDIDATES = 32
 # GDN_TREE_ABI_VERSION of include/gdn_tree.h that the signatures below follow
-ABI_VERSION = 8
+ABI_VERSION = 9
 
 _lock = threading.Lock()
 _lib = None
@@ -91,6 +113,27 @@ def load() -> ctypes.CDLL:
         lib.gdn_tree_path.restype = I
         lib.gdn_tree_index.argtypes = [P, P, P, I, I, P, P]
         lib.gdn_tree_index.restype = I
+        L, F = ctypes.c_int64, ctypes.c_float
+        lib.gdn_prefill_workspace.argtypes = [I] * 7
+        lib.gdn_prefill_workspace.restype = L
+        lib.gdn_prefill.argtypes = [P, P, P, I, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, P, L,
+                                    P, P]
+        lib.gdn_step.argtypes = [P, P, P, I, P, P, P, P, P, P, I, I, I, I, I, I, I, P, P]
+        lib.gdn_tree_attention_workspace.argtypes = [I] * 8
+        lib.gdn_tree_attention_workspace.restype = L
+        lib.gdn_tree_attention.argtypes = [P, P, P, I, P, P, P, L, P, P, P, P, I, F, P, I, I, I, I,
+                                           I, I, I, I, P, L, P, P]
+        lib.gdn_page_fork.argtypes = [P, P, P, P, P, P, I, I, I, I, I, P, P]
+        lib.gdn_page_extend.argtypes = [P, P, P, P, P, P, I, I, I, I, I, P, P]
+        lib.gdn_page_free.argtypes = [P, P, P, P, I, I, I, I, I, P, P]
+        lib.gdn_page_compact.argtypes = [P, P, P, P, P, P, I, I, I, I, P]
+        lib.gdn_page_copy.argtypes = [P, P, P, I, I, I, L, P]
+        lib.gdn_kv_commit.argtypes = [P, P, L, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I,
+                                      P, P]
+        for fn in (lib.gdn_prefill, lib.gdn_step, lib.gdn_tree_attention, lib.gdn_page_fork,
+                   lib.gdn_page_extend, lib.gdn_page_free, lib.gdn_page_compact,
+                   lib.gdn_page_copy, lib.gdn_kv_commit):
+            fn.restype = I
         lib.gdn_status_string.argtypes = [I]
         lib.gdn_status_string.restype = ctypes.c_char_p
         lib.gdn_tree_abi_version.argtypes = []
@@ -394,3 +437,320 @@ def index(parent, status=None, stream=None):
                             _stream(stream))
     _check("gdn_tree_index", rc)
     return depth, anc
+
+
+# ---------------------------------------------------------------------------
+# serving operators
+# ---------------------------------------------------------------------------
+def _workspace(nbytes, device, stream):
+    """Device memory for one call, from torch's allocator: ordered on the
+    current stream, and kept until `stream` is done with it when that is
+    another one."""
+    torch = _torch()
+    ws = torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=device)
+    if stream is not None:
+        other = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+        # the block may have been used on the current stream just before
+        other.wait_stream(torch.cuda.current_stream(device))
+        ws.record_stream(other)
+    return ws
+
+
+def _rule_shapes(q, k, v, alpha, beta, S, src, dst, out, batch, status):
+    torch = _torch()
+    _need(q, "q", (torch.bfloat16, torch.float32))
+    if q.dim() != 3:
+        raise ValueError("q must be [rows][key heads][d_k]")
+    rows, Hk, dk = q.shape
+    _need(k, "k", (q.dtype,), q.shape)
+    _need(v, "v", (q.dtype,))
+    if v.dim() != 3 or v.shape[0] != rows:
+        raise ValueError("v must be [rows][heads][d_v]")
+    H, dv = v.shape[1], v.shape[2]
+    _need(alpha, "alpha", (torch.float32,), (rows, H))
+    _need(beta, "beta", (torch.float32,), (rows, H))
+    _need(S, "S", (torch.float32,))
+    if S.dim() != 4 or tuple(S.shape[1:]) != (H, dk, dv):
+        raise ValueError("S must be [slots][heads][d_k][d_v]")
+    _need(src, "src", (torch.int32,), (batch,))
+    _need(dst, "dst", (torch.int32,), (batch,))
+    if out is None:
+        out = torch.empty((rows, H, dv), dtype=q.dtype, device=q.device)
+    _need(out, "out", (torch.bfloat16, torch.float32), (rows, H, dv))
+    if status is not None:
+        _need(status, "status", (torch.int32,), (batch,))
+    return rows, Hk, dk, H, dv, out
+
+
+def prefill(q, k, v, alpha, beta, cu, S, src, dst, out=None, status=None, stream=None,
+            workspace=None, prepare=False):
+    """gdn_prefill: the gated delta rule over the prompts of a ragged batch.
+
+    q, k [rows][Hk][d_k], v [rows][H][d_v] (bf16 or fp32), alpha, beta
+    [rows][H] fp32; sequence i owns rows cu[i] .. cu[i+1] (cu int32
+    [batch + 1], on the GPU).  It starts from state slot src[i] of S
+    [slots][H][d_k][d_v] (-1: zero) and leaves its state in slot dst[i].
+    Returns out [rows][H][d_v] (bf16 or fp32, q's type by default); S is
+    updated in place.  workspace: a uint8 tensor of prefill_workspace bytes;
+    one is allocated when None.  prepare=True returns a Launch.
+    """
+    torch = _torch()
+    lib = load()
+    _need(cu, "cu", (torch.int32,))
+    if cu.dim() != 1 or cu.shape[0] < 2:
+        raise ValueError("cu must be [batch + 1]")
+    batch = cu.shape[0] - 1
+    rows, Hk, dk, H, dv, out = _rule_shapes(q, k, v, alpha, beta, S, src, dst, out, batch, status)
+    dt = _qkv_dtype(q)
+    need = lib.gdn_prefill_workspace(dt, batch, rows, H, Hk, dk, dv)
+    if workspace is None:
+        workspace = _workspace(need, q.device, stream)
+    else:
+        _need(workspace, "workspace", (torch.uint8,))
+    args = (_ptr(q), _ptr(k), _ptr(v), dt, _ptr(alpha), _ptr(beta), _ptr(cu), _ptr(S), _ptr(src),
+            _ptr(dst), _ptr(out), _qkv_dtype(out), batch, rows, S.shape[0], H, Hk, dk, dv,
+            _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream))
+    return _issue("gdn_prefill", lib.gdn_prefill, args,
+                  (q, k, v, alpha, beta, cu, S, src, dst, out, workspace, status), out, prepare)
+
+
+def step(q, k, v, alpha, beta, S, src, dst, out=None, status=None, stream=None, prepare=False):
+    """gdn_step: one token for every sequence (row i: sequence i); arguments
+    as for prefill without cu.  Returns out; S is updated in place."""
+    lib = load()
+    rows, Hk, dk, H, dv, out = _rule_shapes(q, k, v, alpha, beta, S, src, dst, out, q.shape[0],
+                                            status)
+    args = (_ptr(q), _ptr(k), _ptr(v), _qkv_dtype(q), _ptr(alpha), _ptr(beta), _ptr(S), _ptr(src),
+            _ptr(dst), _ptr(out), _qkv_dtype(out), rows, S.shape[0], H, Hk, dk, dv, _ptr(status),
+            _stream(stream))
+    return _issue("gdn_step", lib.gdn_step, args,
+                  (q, k, v, alpha, beta, S, src, dst, out, status), out, prepare)
+
+
+def _need_cache(t, name, dtypes, Hkv, page, d):
+    """A cache [pages][Hkv][page][d] whose pages are contiguous (the stride
+    between pages is free); returns (pages, page stride)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if t.dim() != 4 or t.shape[1] != Hkv or t.shape[3] != d or (page and t.shape[2] != page):
+        raise ValueError(f"{name} must be [pages][{Hkv}][page][{d}]")
+    page = t.shape[2]
+    if t.stride()[1:] != (page * d, d, 1):
+        raise ValueError(f"the pages of {name} must be contiguous")
+    return t.shape[0], t.stride(0) if t.shape[0] > 1 else Hkv * page * d
+
+
+def tree_attention(q, k, v, parent, k_cache, v_cache, pages, length, scale, shared=None, out=None,
+                   status=None, stream=None, workspace=None, prepare=False):
+    """gdn_tree_attention: softmax attention of a draft tree (n = 1: one
+    token) over a paged cache and the tree's own ancestors.
+
+    q [batch][n][Hq][d], k, v [batch][n][Hkv][d] (bf16 or fp16); parent int32
+    [batch][n]; k_cache, v_cache [pages][Hkv][page][d]; pages int32
+    [batch][max_pages]; length int32 [batch].  shared = (start [groups + 1],
+    tokens [groups]), int32: sequences start[g] .. start[g+1]-1 have their
+    first tokens[g] tokens in the same pages, which are then read once for
+    all of them.  Returns out [batch][n][Hq][d].  prepare=True: a Launch.
+    """
+    torch = _torch()
+    lib = load()
+    _need(q, "q", (torch.bfloat16, torch.float16))
+    if q.dim() != 4:
+        raise ValueError("q must be [batch][n][Hq][d]")
+    batch, n, Hq, d = q.shape
+    _need(k, "k", (q.dtype,))
+    if k.dim() != 4 or k.shape[0] != batch or k.shape[1] != n or k.shape[3] != d:
+        raise ValueError("k must be [batch][n][Hkv][d]")
+    Hkv = k.shape[2]
+    _need(v, "v", (q.dtype,), k.shape)
+    _need(parent, "parent", (torch.int32,), (batch, n))
+    num, stride = _need_cache(k_cache, "k_cache", (q.dtype,), Hkv, 0, d)
+    page = k_cache.shape[2]
+    if _need_cache(v_cache, "v_cache", (q.dtype,), Hkv, page, d) != (num, stride):
+        raise ValueError("k_cache and v_cache must have the same pages and strides")
+    _need(pages, "pages", (torch.int32,))
+    if pages.dim() != 2 or pages.shape[0] != batch:
+        raise ValueError("pages must be [batch][max_pages]")
+    _need(length, "length", (torch.int32,), (batch,))
+    start = tokens = None
+    groups = 0
+    if shared is not None:
+        start, tokens = shared
+        _need(tokens, "shared tokens", (torch.int32,))
+        groups = tokens.numel()
+        _need(tokens, "shared tokens", (torch.int32,), (groups,))
+        _need(start, "group starts", (torch.int32,), (groups + 1,))
+    if out is None:
+        out = torch.empty_like(q)
+    _need(out, "out", (q.dtype,), q.shape)
+    if status is not None:
+        _need(status, "status", (torch.int32,), (batch,))
+    width = pages.shape[1]
+    need = lib.gdn_tree_attention_workspace(batch, n, Hq, Hkv, d, page, width, groups)
+    if workspace is None:
+        workspace = _workspace(need, q.device, stream)
+    else:
+        _need(workspace, "workspace", (torch.uint8,))
+    args = (_ptr(q), _ptr(k), _ptr(v), DTYPE_BF16 if q.dtype == torch.bfloat16 else DTYPE_F16,
+            _ptr(parent), _ptr(k_cache), _ptr(v_cache), stride, _ptr(pages), _ptr(length),
+            _ptr(start), _ptr(tokens), groups, float(scale), _ptr(out), batch, n, Hq, Hkv, d, page,
+            num, width, _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream))
+    return _issue("gdn_tree_attention", lib.gdn_tree_attention, args,
+                  (q, k, v, parent, k_cache, v_cache, pages, length, start, tokens, out, workspace,
+                   status), out, prepare)
+
+
+def _need_table(table, length, ref):
+    torch = _torch()
+    _need(table, "table", (torch.int32,))
+    if table.dim() != 2:
+        raise ValueError("table must be [seqs][max_pages]")
+    _need(length, "length", (torch.int32,), (table.shape[0],))
+    _need(ref, "ref", (torch.int32,))
+    if ref.dim() != 1:
+        raise ValueError("ref must be [pool]")
+    return table.shape[0], table.shape[1], ref.shape[0]
+
+
+def page_fork(table, length, ref, src, dst, page, copies=None, status=None, stream=None,
+              prepare=False):
+    """gdn_page_fork: the empty rows dst become continuations of the rows src
+    of the page table; returns copies int32 [m][2], the partial pages that
+    page_copy has to move ({-1, -1}: none)."""
+    torch = _torch()
+    lib = load()
+    seqs, width, pool = _need_table(table, length, ref)
+    _need(src, "src", (torch.int32,))
+    m = src.numel()
+    _need(dst, "dst", (torch.int32,), src.shape)
+    if copies is None:
+        copies = torch.empty((m, 2), dtype=torch.int32, device=table.device)
+    _need(copies, "copies", (torch.int32,), (m, 2))
+    if status is not None:
+        _need(status, "status", (torch.int32,), (m,))
+    args = (_ptr(table), _ptr(length), _ptr(ref), _ptr(src), _ptr(dst), _ptr(copies), m, seqs,
+            width, pool, int(page), _ptr(status), _stream(stream))
+    return _issue("gdn_page_fork", lib.gdn_page_fork, args,
+                  (table, length, ref, src, dst, copies, status), copies, prepare)
+
+
+def page_extend(table, length, ref, dst, add, page, begin=None, status=None, stream=None,
+                prepare=False):
+    """gdn_page_extend: room for add[r] more tokens in row dst[r]; returns
+    begin int32 [m], the lengths before (-1: not enough free pages)."""
+    torch = _torch()
+    lib = load()
+    seqs, width, pool = _need_table(table, length, ref)
+    _need(dst, "dst", (torch.int32,))
+    m = dst.numel()
+    _need(add, "add", (torch.int32,), dst.shape)
+    if begin is None:
+        begin = torch.empty_like(dst)
+    _need(begin, "begin", (torch.int32,), dst.shape)
+    if status is not None:
+        _need(status, "status", (torch.int32,), (m,))
+    args = (_ptr(table), _ptr(length), _ptr(ref), _ptr(dst), _ptr(add), _ptr(begin), m, seqs,
+            width, pool, int(page), _ptr(status), _stream(stream))
+    return _issue("gdn_page_extend", lib.gdn_page_extend, args,
+                  (table, length, ref, dst, add, begin, status), begin, prepare)
+
+
+def page_free(table, length, ref, done, page, status=None, stream=None, prepare=False):
+    """gdn_page_free: the rows `done` give their pages back and become empty."""
+    torch = _torch()
+    lib = load()
+    seqs, width, pool = _need_table(table, length, ref)
+    _need(done, "done", (torch.int32,))
+    if status is not None:
+        _need(status, "status", (torch.int32,), (done.numel(),))
+    args = (_ptr(table), _ptr(length), _ptr(ref), _ptr(done), done.numel(), seqs, width, pool,
+            int(page), _ptr(status), _stream(stream))
+    return _issue("gdn_page_free", lib.gdn_page_free, args, (table, length, ref, done, status),
+                  None, prepare)
+
+
+def page_compact(table, length, ref, page, copies=None, count=None, workspace=None, stream=None,
+                 prepare=False):
+    """gdn_page_compact: the used pages become the lowest ids (table and ref
+    follow); returns (copies int32 [pool // 2][2], count int32 []): what
+    page_copy has to move."""
+    torch = _torch()
+    lib = load()
+    seqs, width, pool = _need_table(table, length, ref)
+    if copies is None:
+        copies = torch.empty((pool // 2, 2), dtype=torch.int32, device=table.device)
+    _need(copies, "copies", (torch.int32,), (pool // 2, 2))
+    if count is None:
+        count = torch.empty((), dtype=torch.int32, device=table.device)
+    _need(count, "count", (torch.int32,), ())
+    if workspace is None:
+        workspace = _workspace(4 * pool, table.device, stream)
+    _need(workspace, "workspace", (torch.uint8,))
+    if workspace.numel() < 4 * pool:
+        raise ValueError("workspace must hold 4 bytes for every page of the pool")
+    args = (_ptr(table), _ptr(length), _ptr(ref), _ptr(copies), _ptr(count), _ptr(workspace), seqs,
+            width, pool, int(page), _stream(stream))
+    return _issue("gdn_page_compact", lib.gdn_page_compact, args,
+                  (table, length, ref, copies, count, workspace), (copies, count), prepare)
+
+
+def page_copy(cache, copies, count=None, stream=None, prepare=False):
+    """gdn_page_copy: cache [planes][pool][...], page `to` <- page `from` in
+    every plane for the first count (default: all) of copies [m][2]."""
+    torch = _torch()
+    lib = load()
+    _need(cache, "cache", (torch.bfloat16, torch.float16, torch.float32, torch.uint8))
+    if cache.dim() < 3:
+        raise ValueError("cache must be [planes][pool][...]")
+    _need(copies, "copies", (torch.int32,))
+    if copies.dim() != 2 or copies.shape[1] != 2:
+        raise ValueError("copies must be [m][2]")
+    if count is not None:
+        _need(count, "count", (torch.int32,))
+        if count.numel() != 1:
+            raise ValueError("count must hold one number")
+    planes, pool = cache.shape[0], cache.shape[1]
+    nbytes = cache.stride(1) * cache.element_size()
+    args = (_ptr(cache), _ptr(copies), _ptr(count), copies.shape[0], planes, pool, nbytes,
+            _stream(stream))
+    return _issue("gdn_page_copy", lib.gdn_page_copy, args, (cache, copies, count), cache, prepare)
+
+
+def kv_commit(k_cache, v_cache, table, dst, begin, k, v, path, add, status=None, stream=None,
+              prepare=False):
+    """gdn_kv_commit: the accepted branches' key and value rows (rows
+    path[r][: add[r]] of k, v [m][n][Hkv][d]) become tokens begin[r] .. of the
+    table's rows dst[r]."""
+    torch = _torch()
+    lib = load()
+    kinds = (torch.bfloat16, torch.float16, torch.float32)
+    _need(k, "k", kinds)
+    if k.dim() != 4:
+        raise ValueError("k must be [m][n][Hkv][d]")
+    m, n, Hkv, d = k.shape
+    _need(v, "v", (k.dtype,), k.shape)
+    num, stride = _need_cache(k_cache, "k_cache", (k.dtype,), Hkv, 0, d)
+    page = k_cache.shape[2]
+    if _need_cache(v_cache, "v_cache", (k.dtype,), Hkv, page, d) != (num, stride):
+        raise ValueError("k_cache and v_cache must have the same pages and strides")
+    _need(table, "table", (torch.int32,))
+    if table.dim() != 2:
+        raise ValueError("table must be [seqs][max_pages]")
+    _need(dst, "dst", (torch.int32,), (m,))
+    _need(begin, "begin", (torch.int32,), (m,))
+    _need(add, "add", (torch.int32,), (m,))
+    _need(path, "path", (torch.int32,))
+    if path.dim() != 2 or path.shape[0] != m:
+        raise ValueError("path must be [m][max_path]")
+    if status is not None:
+        _need(status, "status", (torch.int32,), (m,))
+    args = (_ptr(k_cache), _ptr(v_cache), stride, _ptr(table), _ptr(dst), _ptr(begin), _ptr(k),
+            _ptr(v), _ptr(path), _ptr(add), m, n, path.shape[1], Hkv, d, k.element_size(),
+            table.shape[0], table.shape[1], num, page, _ptr(status), _stream(stream))
+    return _issue("gdn_kv_commit", lib.gdn_kv_commit, args,
+                  (k_cache, v_cache, table, dst, begin, k, v, path, add, status), None, prepare)

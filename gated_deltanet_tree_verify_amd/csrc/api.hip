@@ -5,7 +5,7 @@
 
 #include <atomic>
 
-#include "internal.hpp"
+#include "serving.hpp"
 
 namespace {
 
@@ -18,6 +18,41 @@ gdn_status shape_status(int batch, int n, int H, int dk, int dv) {
     if (n > GDN_MAX_NODES || !dim_ok(dk) || !dim_ok(dv)) return GDN_ERR_UNSUPPORTED;
     // element offsets are formed in 64-bit, but grid.x = batch * H must fit
     if ((long long)batch * H > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
+    return GDN_OK;
+}
+
+// log2 of a power of two, -1 for anything else
+int log2_exact(int x) { return x >= 1 && (x & (x - 1)) == 0 ? __builtin_ctz((unsigned)x) : -1; }
+
+template <typename... P>
+bool all_aligned(const P *...p) {
+    return (... && (!p || aligned16(p)));
+}
+
+gdn_status rule_status(const gdn::RuleArgs &a) {
+    if (!a.S || !a.src || !a.dst) return GDN_ERR_INVALID_ARG;
+    if (a.rows > 0 && (!a.q || !a.k || !a.v || !a.alpha || !a.beta || !a.out))
+        return GDN_ERR_INVALID_ARG;
+    if (a.dtype != GDN_DTYPE_F32 && a.dtype != GDN_DTYPE_BF16) return GDN_ERR_INVALID_ARG;
+    if (a.out_dtype != GDN_DTYPE_F32 && a.out_dtype != GDN_DTYPE_BF16) return GDN_ERR_INVALID_ARG;
+    if (!all_aligned((const char *)a.q, (const char *)a.k, (const char *)a.v, a.alpha, a.beta,
+                     a.cu, a.S, a.src, a.dst, (const char *)a.out, (const char *)a.workspace,
+                     a.status))
+        return GDN_ERR_INVALID_ARG;
+    if (a.batch < 1 || a.rows < 0 || a.slots < 1 || a.H < 1 || a.Hk < 1 || a.dk < 1 || a.dv < 1)
+        return GDN_ERR_INVALID_ARG;
+    if (a.H % a.Hk != 0 || !dim_ok(a.dk) || !dim_ok(a.dv)) return GDN_ERR_UNSUPPORTED;
+    // grids of (tokens / 64 + batch) * H workgroups and up to 16 per (sequence, head)
+    if (((long long)a.rows / 64 + a.batch) * a.H > 0x7ffffffLL) return GDN_ERR_UNSUPPORTED;
+    return GDN_OK;
+}
+
+gdn_status page_status(const gdn::PageArgs &a, int m, int page) {
+    if (!a.table || !a.length || !a.ref) return GDN_ERR_INVALID_ARG;
+    if (!all_aligned(a.table, a.length, a.ref, a.status)) return GDN_ERR_INVALID_ARG;
+    if (m < 0 || a.seqs < 1 || a.width < 1 || a.pool < 1 || page < 1) return GDN_ERR_INVALID_ARG;
+    // a row's tokens are counted in 32 bits
+    if (a.page_log < 0 || (long long)a.width * page > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }
 
@@ -208,6 +243,177 @@ gdn_status gdn_tree_index(const int32_t *parent, int32_t *depth, uint32_t *anc, 
         if (p && !aligned16(p)) return GDN_ERR_INVALID_ARG;
     return from_hip(gdn::launch_index(parent, depth, anc, batch, n, status,
                                       static_cast<hipStream_t>(stream)));
+}
+
+int64_t gdn_prefill_workspace(gdn_dtype qkv_dtype, int batch, int rows, int H, int Hk, int d_k,
+                              int d_v) {
+    if (batch < 1 || rows < 0 || H < 1 || Hk < 1 || H % Hk != 0 || !dim_ok(d_k) || !dim_ok(d_v))
+        return 0;
+    gdn::RuleArgs a{};
+    a.dtype = qkv_dtype;
+    a.batch = batch, a.rows = rows, a.H = H, a.Hk = Hk, a.dk = d_k, a.dv = d_v;
+    return gdn::prefill_workspace(a);
+}
+
+gdn_status gdn_prefill(const void *q, const void *k, const void *v, gdn_dtype qkv_dtype,
+                       const float *alpha, const float *beta, const int32_t *cu, float *S,
+                       const int32_t *src, const int32_t *dst, void *out, gdn_dtype out_dtype,
+                       int batch, int rows, int slots, int H, int Hk, int d_k, int d_v,
+                       void *workspace, int64_t workspace_bytes, int32_t *status, void *stream) {
+    gdn::RuleArgs a{q,   k,         v,     qkv_dtype, alpha, beta, cu, S,   src,  dst,
+                    out, out_dtype, batch, rows,      slots, H,    Hk, d_k, d_v,  workspace,
+                    status};
+    if (!cu) return GDN_ERR_INVALID_ARG;
+    const gdn_status st = rule_status(a);
+    if (st != GDN_OK) return st;
+    const int64_t need = gdn::prefill_workspace(a);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return GDN_ERR_INVALID_ARG;
+    return from_hip(gdn::launch_prefill(a, static_cast<hipStream_t>(stream)));
+}
+
+gdn_status gdn_step(const void *q, const void *k, const void *v, gdn_dtype qkv_dtype,
+                    const float *alpha, const float *beta, float *S, const int32_t *src,
+                    const int32_t *dst, void *out, gdn_dtype out_dtype, int batch, int slots,
+                    int H, int Hk, int d_k, int d_v, int32_t *status, void *stream) {
+    gdn::RuleArgs a{q,   k,         v,     qkv_dtype, alpha, beta, nullptr, S,   src,  dst,
+                    out, out_dtype, batch, batch,     slots, H,    Hk,      d_k, d_v,  nullptr,
+                    status};
+    const gdn_status st = rule_status(a);
+    if (st != GDN_OK) return st;
+    return from_hip(gdn::launch_step(a, static_cast<hipStream_t>(stream)));
+}
+
+int64_t gdn_tree_attention_workspace(int batch, int n, int Hq, int Hkv, int d, int page,
+                                     int max_pages, int groups) {
+    if (batch < 1 || n < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || d < 1 || max_pages < 1 ||
+        log2_exact(page) < 0)
+        return 0;
+    gdn::AttentionArgs a{};
+    a.batch = batch, a.n = n, a.Hq = Hq, a.Hkv = Hkv, a.d = d, a.page_log = log2_exact(page);
+    a.max_pages = max_pages, a.groups = groups;
+    return gdn::attention_workspace(a);
+}
+
+gdn_status gdn_tree_attention(const void *q, const void *k, const void *v, gdn_dtype dtype,
+                              const int32_t *parent, const void *k_cache, const void *v_cache,
+                              int64_t page_stride, const int32_t *pages, const int32_t *length,
+                              const int32_t *group_start, const int32_t *group_shared, int groups,
+                              float scale, void *out, int batch, int n, int Hq, int Hkv, int d,
+                              int page, int num_pages, int max_pages, void *workspace,
+                              int64_t workspace_bytes, int32_t *status, void *stream) {
+    if (!q || !k || !v || !parent || !k_cache || !v_cache || !pages || !length || !out)
+        return GDN_ERR_INVALID_ARG;
+    if (dtype != GDN_DTYPE_BF16 && dtype != GDN_DTYPE_F16) return GDN_ERR_INVALID_ARG;
+    if (groups < 0 || (groups > 0 && (!group_start || !group_shared))) return GDN_ERR_INVALID_ARG;
+    if (!all_aligned((const char *)q, (const char *)k, (const char *)v, parent,
+                     (const char *)k_cache, (const char *)v_cache, pages, length, group_start,
+                     group_shared, (const char *)out, (const char *)workspace, status))
+        return GDN_ERR_INVALID_ARG;
+    if (batch < 1 || n < 1 || Hq < 1 || Hkv < 1 || d < 1 || page < 1 || num_pages < 1 ||
+        max_pages < 1)
+        return GDN_ERR_INVALID_ARG;
+    const int page_log = log2_exact(page);
+    if (n > GDN_MAX_NODES || Hq % Hkv != 0 || d % 8 != 0 || d > GDN_MAX_HEAD_DIM || page_log < 0 ||
+        batch > GDN_MAX_SEQUENCES || groups > GDN_MAX_SEQUENCES)
+        return GDN_ERR_UNSUPPORTED;
+    // tokens, and the query rows of a group, are counted in 32 bits
+    if ((long long)max_pages * page > 0x3fffffffLL ||
+        (long long)batch * n * Hq > 0x3fffffffLL)
+        return GDN_ERR_UNSUPPORTED;
+    if (page_stride % 8 != 0 || page_stride < (int64_t)Hkv * page * d) return GDN_ERR_INVALID_ARG;
+    gdn::AttentionArgs a{q,      k,      v,           dtype,        parent, k_cache, v_cache,
+                         page_stride, pages, length,  group_start,  group_shared, groups,
+                         scale,  out,    batch,       n,            Hq,     Hkv,     d,
+                         page_log, num_pages, max_pages, workspace, status};
+    if (!workspace || workspace_bytes < gdn::attention_workspace(a)) return GDN_ERR_INVALID_ARG;
+    return from_hip(gdn::launch_tree_attention(a, static_cast<hipStream_t>(stream)));
+}
+
+gdn_status gdn_page_fork(int32_t *table, int32_t *length, int32_t *ref, const int32_t *src,
+                         const int32_t *dst, int32_t *copies, int m, int seqs, int max_pages,
+                         int pool, int page, int32_t *status, void *stream) {
+    const gdn::PageArgs a{table, length, ref, seqs, max_pages, pool, log2_exact(page), status};
+    const gdn_status st = page_status(a, m, page);
+    if (st != GDN_OK) return st;
+    if (m == 0) return GDN_OK;
+    if (!src || !dst || !copies || !all_aligned(src, dst, copies)) return GDN_ERR_INVALID_ARG;
+    if (m > GDN_MAX_REQUESTS) return GDN_ERR_UNSUPPORTED;
+    return from_hip(
+        gdn::launch_page_fork(a, src, dst, copies, m, static_cast<hipStream_t>(stream)));
+}
+
+gdn_status gdn_page_extend(int32_t *table, int32_t *length, int32_t *ref, const int32_t *dst,
+                           const int32_t *add, int32_t *begin, int m, int seqs, int max_pages,
+                           int pool, int page, int32_t *status, void *stream) {
+    const gdn::PageArgs a{table, length, ref, seqs, max_pages, pool, log2_exact(page), status};
+    const gdn_status st = page_status(a, m, page);
+    if (st != GDN_OK) return st;
+    if (m == 0) return GDN_OK;
+    if (!dst || !add || !begin || !all_aligned(dst, add, begin)) return GDN_ERR_INVALID_ARG;
+    if (m > GDN_MAX_REQUESTS) return GDN_ERR_UNSUPPORTED;
+    return from_hip(
+        gdn::launch_page_extend(a, dst, add, begin, m, static_cast<hipStream_t>(stream)));
+}
+
+gdn_status gdn_page_free(int32_t *table, int32_t *length, int32_t *ref, const int32_t *done, int m,
+                         int seqs, int max_pages, int pool, int page, int32_t *status,
+                         void *stream) {
+    const gdn::PageArgs a{table, length, ref, seqs, max_pages, pool, log2_exact(page), status};
+    const gdn_status st = page_status(a, m, page);
+    if (st != GDN_OK) return st;
+    if (m == 0) return GDN_OK;
+    if (!done || !all_aligned(done)) return GDN_ERR_INVALID_ARG;
+    return from_hip(gdn::launch_page_free(a, done, m, static_cast<hipStream_t>(stream)));
+}
+
+gdn_status gdn_page_compact(int32_t *table, const int32_t *length, int32_t *ref, int32_t *copies,
+                            int32_t *count, int32_t *workspace, int seqs, int max_pages, int pool,
+                            int page, void *stream) {
+    const gdn::PageArgs a{table, const_cast<int32_t *>(length), ref,    seqs, max_pages,
+                          pool,  log2_exact(page),              nullptr};
+    const gdn_status st = page_status(a, 0, page);
+    if (st != GDN_OK) return st;
+    if ((pool > 1 && !copies) || !count || !workspace) return GDN_ERR_INVALID_ARG;
+    if (!all_aligned(copies, count, workspace)) return GDN_ERR_INVALID_ARG;
+    return from_hip(
+        gdn::launch_page_compact(a, copies, count, workspace, static_cast<hipStream_t>(stream)));
+}
+
+gdn_status gdn_page_copy(void *cache, const int32_t *copies, const int32_t *count, int m,
+                         int planes, int pool, int64_t page_bytes, void *stream) {
+    if (m < 0 || planes < 1 || pool < 1 || page_bytes < 16) return GDN_ERR_INVALID_ARG;
+    if (m == 0) return GDN_OK;
+    if (!cache || !copies || !all_aligned((const char *)cache, copies, count) ||
+        page_bytes % 16 != 0)
+        return GDN_ERR_INVALID_ARG;
+    if (planes > 65535) return GDN_ERR_UNSUPPORTED;
+    return from_hip(gdn::launch_page_copy(cache, copies, count, m, planes, pool, page_bytes,
+                                          static_cast<hipStream_t>(stream)));
+}
+
+gdn_status gdn_kv_commit(void *k_cache, void *v_cache, int64_t page_stride, const int32_t *table,
+                         const int32_t *dst, const int32_t *begin, const void *k, const void *v,
+                         const int32_t *path, const int32_t *add, int m, int n, int max_path,
+                         int Hkv, int d, int elem_bytes, int seqs, int max_pages, int pool,
+                         int page, int32_t *status, void *stream) {
+    if (m < 0 || n < 1 || max_path < 1 || Hkv < 1 || d < 1 || seqs < 1 || max_pages < 1 ||
+        pool < 1 || page < 1 || (elem_bytes != 2 && elem_bytes != 4))
+        return GDN_ERR_INVALID_ARG;
+    if (m == 0) return GDN_OK;
+    if (!k_cache || !v_cache || !table || !dst || !begin || !k || !v || !path || !add)
+        return GDN_ERR_INVALID_ARG;
+    if (!all_aligned((const char *)k_cache, (const char *)v_cache, table, dst, begin,
+                     (const char *)k, (const char *)v, path, add, status))
+        return GDN_ERR_INVALID_ARG;
+    const int page_log = log2_exact(page);
+    // rows are moved in 16-byte pieces; a row's tokens are counted in 32 bits
+    if (page_log < 0 || d % 8 != 0 || (long long)max_pages * page > 0x7fffffffLL)
+        return GDN_ERR_UNSUPPORTED;
+    if (page_stride % 8 != 0 || page_stride < (int64_t)Hkv * page * d) return GDN_ERR_INVALID_ARG;
+    const gdn::KvCommitArgs a{k_cache, v_cache, page_stride, table, dst,        begin, k,
+                              v,       path,    add,         m,     n,          max_path, Hkv,
+                              d,       elem_bytes, seqs,     max_pages, pool,   page_log, status};
+    return from_hip(gdn::launch_kv_commit(a, static_cast<hipStream_t>(stream)));
 }
 
 const char *gdn_status_string(int status) {

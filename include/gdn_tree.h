@@ -53,10 +53,13 @@
 extern "C" {
 #endif
 
-#define GDN_TREE_ABI_VERSION 8
+#define GDN_TREE_ABI_VERSION 9
 #define GDN_MAX_NODES 128
 #define GDN_MAX_DIM 128
 #define GDN_MAX_CANDIDATES 32   /* child candidates per node, gdn_tree_build */
+#define GDN_MAX_HEAD_DIM 256    /* head size of gdn_tree_attention */
+#define GDN_MAX_SEQUENCES 1024  /* batch and groups of gdn_tree_attention */
+#define GDN_MAX_REQUESTS 4096   /* requests of one page_fork / page_extend call */
 
 typedef enum {
     GDN_OK = 0,
@@ -74,6 +77,14 @@ typedef enum { GDN_DTYPE_F32 = 0, GDN_DTYPE_BF16 = 1, GDN_DTYPE_F16 = 2 } gdn_dt
 #define GDN_FAULT_BAD_PATH 2   /* path not a root-connected increasing chain,
                                   an id outside [0, n), or a length outside
                                   [0, max_path]                             */
+/* flags of the serving operators (prefill, step, attention, pages) */
+#define GDN_FAULT_BAD_SLOT 4   /* a state slot or table row outside its pool */
+#define GDN_FAULT_BAD_LENGTH 8 /* row offsets or a length that do not fit    */
+#define GDN_FAULT_BAD_PAGE 16  /* a page id in use outside the cache         */
+#define GDN_FAULT_BAD_GROUP 32 /* group offsets not ascending over the batch,
+                                  or a member's page row that differs from
+                                  its group's within the shared tokens       */
+#define GDN_FAULT_NO_PAGE 64   /* not enough free pages for the request      */
 
 /*
  * Tree verify (the rollback-free verification of the section above).
@@ -259,6 +270,161 @@ gdn_status gdn_tree_path(const int32_t *parent, const int32_t *accepted,
 gdn_status gdn_tree_index(const int32_t *parent, int32_t *depth,
                           uint32_t *anc, int batch, int n, int32_t *status,
                           void *stream);
+
+/* ------------------------------------------------------------------------
+ * Serving operators: what a program that serves a model with Gated DeltaNet
+ * and softmax-attention layers needs next to the tree calls above.  Sizes
+ * that the host cannot know without a synchronisation (sequence lengths,
+ * page ids, slots) are device arrays; the kernels check them before any
+ * access and report through status.  Conventions as above, unless stated.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * Prompt prefill of the gated delta rule, a ragged batch:
+ *   S_t = alpha_t S_{t-1} + k_t u_t^T, u_t = beta_t (v_t - alpha_t S_{t-1}^T k_t),
+ *   o_t = S_t^T q_t
+ * over the tokens of every sequence in order.  Sequence i owns the rows
+ * [cu[i], cu[i+1]) of
+ *   q, k  [rows][Hk][d_k], v [rows][H][d_v]   bf16 or fp32 (qkv_dtype)
+ *   alpha, beta [rows][H]                     fp32, alpha >= 0
+ *   out   [rows][H][d_v]                      bf16 or fp32 (out_dtype)
+ * (cu int32 [batch + 1]; a sequence may be empty).  H is a multiple of Hk:
+ * head h reads key head h / (H / Hk).  The state pool S is fp32
+ * [slots][H][d_k][d_v]: sequence i starts from slot src[i], or from zero
+ * where src[i] = -1, and leaves its state in slot dst[i].  dst[i] may be
+ * src[i]; otherwise the dst slots must be distinct and no other sequence's
+ * src.  An empty sequence copies its state.  alpha = 0 clears the state.
+ * Faults, per sequence: GDN_FAULT_BAD_LENGTH (cu not ascending within
+ * [0, rows]: nothing of it is written) and GDN_FAULT_BAD_SLOT (src or dst:
+ * its out rows are NaN, no state is written).
+ * workspace: device memory of at least gdn_prefill_workspace(...) bytes,
+ * contents ignored; one call at a time may use it.
+ * Arithmetic: products, sums and the state in fp32.
+ */
+int64_t gdn_prefill_workspace(gdn_dtype qkv_dtype, int batch, int rows, int H,
+                              int Hk, int d_k, int d_v);
+gdn_status gdn_prefill(const void *q, const void *k, const void *v,
+                       gdn_dtype qkv_dtype, const float *alpha,
+                       const float *beta, const int32_t *cu, float *S,
+                       const int32_t *src, const int32_t *dst, void *out,
+                       gdn_dtype out_dtype, int batch, int rows, int slots,
+                       int H, int Hk, int d_k, int d_v, void *workspace,
+                       int64_t workspace_bytes, int32_t *status,
+                       void *stream);
+
+/*
+ * One token for every sequence: gdn_prefill for lengths of one, with row i
+ * belonging to sequence i (no cu).  A state may be the source of several
+ * sequences as long as no dst slot is another sequence's src.
+ */
+gdn_status gdn_step(const void *q, const void *k, const void *v,
+                    gdn_dtype qkv_dtype, const float *alpha, const float *beta,
+                    float *S, const int32_t *src, const int32_t *dst, void *out,
+                    gdn_dtype out_dtype, int batch, int slots, int H, int Hk,
+                    int d_k, int d_v, int32_t *status, void *stream);
+
+/*
+ * Softmax attention of a draft tree (n = 1: one decoded token) over a paged
+ * cache.  For sequence b, node i and query head h (key head h / (Hq / Hkv)),
+ *   out = softmax(scale q . K) V
+ * over the length[b] cached tokens and those tree nodes that are i or an
+ * ancestor of i.
+ *   q, out [batch][n][Hq][d], k, v [batch][n][Hkv][d], bf16 or fp16 (dtype)
+ *   parent [batch][n] int32 as above
+ *   k_cache, v_cache: page p, key head h, token t at element
+ *     p * page_stride + (h * page + t) * d; num_pages pages
+ *   pages [batch][max_pages] int32: the page of token t of sequence b is
+ *     pages[b][t / page]; entries past the length are not read
+ *   length [batch] int32, 0 <= length <= max_pages * page
+ * Groups (optional, groups = 0 for none): sequences group_start[g] ..
+ * group_start[g+1]-1 have their first group_shared[g] tokens in the same
+ * pages; that part of the cache is read once for all of them.  The result
+ * does not depend on the grouping.  Sequences before group_start[0] and from
+ * group_start[groups] on share nothing; members shorter than the shared part
+ * use what they have.
+ * Faults, per sequence (its out rows are NaN): GDN_FAULT_BAD_PARENT,
+ * _BAD_LENGTH, _BAD_PAGE, _BAD_GROUP.
+ * page is a power of two, d a multiple of 8 up to GDN_MAX_HEAD_DIM,
+ * page_stride a multiple of 8, batch and groups at most GDN_MAX_SEQUENCES.
+ * Arithmetic: products of dtype operands summed in fp32, maxima and sums in
+ * fp32, weights rounded to dtype for the product with V, one rounding of out.
+ */
+int64_t gdn_tree_attention_workspace(int batch, int n, int Hq, int Hkv, int d,
+                                     int page, int max_pages, int groups);
+gdn_status gdn_tree_attention(const void *q, const void *k, const void *v,
+                              gdn_dtype dtype, const int32_t *parent,
+                              const void *k_cache, const void *v_cache,
+                              int64_t page_stride, const int32_t *pages,
+                              const int32_t *length,
+                              const int32_t *group_start,
+                              const int32_t *group_shared, int groups,
+                              float scale, void *out, int batch, int n, int Hq,
+                              int Hkv, int d, int page, int num_pages,
+                              int max_pages, void *workspace,
+                              int64_t workspace_bytes, int32_t *status,
+                              void *stream);
+
+/*
+ * Pages of a cache.  table [seqs][max_pages] int32 (page ids, -1 where
+ * none), length [seqs] int32 tokens, ref [pool] int32: rows that hold a page,
+ * 0 = free.  page (a power of two) tokens per page.  Free pages are handed
+ * out lowest id first, requests are served in order.
+ *
+ * gdn_page_fork: row dst[r] (empty: length 0) becomes a continuation of row
+ * src[r]: its whole pages are shared (ref + 1), a last partial page gets a
+ * page of its own.  copies[r] = {from, to} of that page, {-1, -1} where
+ * there is none; gdn_page_copy moves the bytes.  Without a free page the row
+ * stays empty (GDN_FAULT_NO_PAGE).
+ * gdn_page_extend: room for add[r] more tokens in row dst[r]; begin[r] is
+ * its length before, or -1 where the pages did not suffice: from the first
+ * request on whose pages, with those before it, pass the free ones, none is
+ * served (GDN_FAULT_NO_PAGE).  Where fork or extend name a dst row twice,
+ * the first request has it and the others fail (GDN_FAULT_BAD_SLOT).
+ * gdn_page_free: the rows done[r] give their pages back and become empty; a
+ * row that is named twice is freed once.
+ * gdn_page_compact: the used pages with ids >= (number of used pages) move,
+ * in order, into the free ones below; table (entries of the lengths' tokens)
+ * and ref follow.  copies [pool / 2][2] lists {from, to}, count[0] their
+ * number.  workspace: int32 [pool].
+ * gdn_page_copy: for every listed copy and plane, page `to` <- page `from`
+ * of cache [planes][pool] pages of page_bytes (a multiple of 16); entries
+ * with an id outside the pool are skipped, count[0] (may be NULL: m) bounds
+ * the list.  No page may be both a from and another copy's to.
+ * gdn_kv_commit: rows path[r][0 .. add[r]) of k, v [m][n][Hkv][d] (elements
+ * of elem_bytes, 2 or 4) become tokens begin[r] .. of row dst[r]: page
+ * layout as for gdn_tree_attention, page_stride in elements.  begin = -1
+ * writes nothing.
+ * status (optional, [m]) receives GDN_FAULT_BAD_SLOT (a row outside the
+ * table; fork onto a row in use or onto itself), _BAD_LENGTH, _BAD_PAGE,
+ * _BAD_PATH (kv_commit: a node outside [0, n) or add outside [0, max_path]);
+ * a request with such a fault changes nothing.  m <= GDN_MAX_REQUESTS for
+ * fork and extend.
+ */
+gdn_status gdn_page_fork(int32_t *table, int32_t *length, int32_t *ref,
+                         const int32_t *src, const int32_t *dst,
+                         int32_t *copies, int m, int seqs, int max_pages,
+                         int pool, int page, int32_t *status, void *stream);
+gdn_status gdn_page_extend(int32_t *table, int32_t *length, int32_t *ref,
+                           const int32_t *dst, const int32_t *add,
+                           int32_t *begin, int m, int seqs, int max_pages,
+                           int pool, int page, int32_t *status, void *stream);
+gdn_status gdn_page_free(int32_t *table, int32_t *length, int32_t *ref,
+                         const int32_t *done, int m, int seqs, int max_pages,
+                         int pool, int page, int32_t *status, void *stream);
+gdn_status gdn_page_compact(int32_t *table, const int32_t *length,
+                            int32_t *ref, int32_t *copies, int32_t *count,
+                            int32_t *workspace, int seqs, int max_pages,
+                            int pool, int page, void *stream);
+gdn_status gdn_page_copy(void *cache, const int32_t *copies,
+                         const int32_t *count, int m, int planes, int pool,
+                         int64_t page_bytes, void *stream);
+gdn_status gdn_kv_commit(void *k_cache, void *v_cache, int64_t page_stride,
+                         const int32_t *table, const int32_t *dst,
+                         const int32_t *begin, const void *k, const void *v,
+                         const int32_t *path, const int32_t *add, int m, int n,
+                         int max_path, int Hkv, int d, int elem_bytes,
+                         int seqs, int max_pages, int pool, int page,
+                         int32_t *status, void *stream);
 
 /* human-readable text for a gdn_status value (never NULL) */
 const char *gdn_status_string(int status);

@@ -1,0 +1,163 @@
+"""Refusals of the serving operators: arguments that the C entry points and
+the binding turn down before any launch.  Nothing here reaches a GPU."""
+import os
+
+import pytest
+
+import gated_deltanet_tree_verify_amd as g
+
+FAKE = 0x10000          # an aligned address that is never dereferenced
+ODD = 0x10004
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(g.lib_path()):
+        g.build()
+    return g.load()
+
+
+def prefill(lib, null=None, odd=None, dtype=1, out_dtype=0, batch=1, rows=64, slots=2, H=4, Hk=2,
+            dk=64, dv=64, ws=FAKE, ws_bytes=1 << 40):
+    p = [FAKE] * 10      # q k v alpha beta cu S src dst out
+    if null is not None:
+        p[null] = None
+    if odd is not None:
+        p[odd] = ODD
+    q, k, v, al, be, cu, S, src, dst, out = p
+    return lib.gdn_prefill(q, k, v, dtype, al, be, cu, S, src, dst, out, out_dtype, batch, rows,
+                           slots, H, Hk, dk, dv, ws, ws_bytes, None, None)
+
+
+@pytest.mark.parametrize("i", range(10))
+def test_prefill_pointers(lib, i):
+    assert prefill(lib, null=i) == -1
+    assert prefill(lib, odd=i) == -1
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dtype=2), -1), (dict(out_dtype=2), -1), (dict(batch=0), -1), (dict(rows=-1), -1),
+    (dict(slots=0), -1), (dict(H=3), -2), (dict(Hk=0), -1), (dict(dk=12), -2), (dict(dk=136), -2),
+    (dict(dv=0), -1), (dict(dv=4), -2), (dict(ws=ODD), -1), (dict(rows=1 << 30, H=64), -2),
+])
+def test_prefill_refuses(lib, kw, code):
+    assert prefill(lib, **kw) == code
+
+
+def test_prefill_workspace(lib):
+    need = lib.gdn_prefill_workspace(1, 3, 1000, 4, 2, 128, 128)
+    assert need >= 0
+    if need > 0:
+        assert prefill(lib, rows=1000, batch=3, dk=128, dv=128, ws_bytes=need - 1) == -1
+        assert prefill(lib, rows=1000, batch=3, dk=128, dv=128, ws=None) == -1
+    assert lib.gdn_prefill_workspace(1, 0, 10, 4, 2, 128, 128) == 0
+    assert lib.gdn_prefill_workspace(1, 1, 10, 4, 3, 128, 128) == 0
+
+
+def test_step_refuses(lib):
+    def step(q=FAKE, S=FAKE, dtype=1, batch=2, slots=2, H=4, Hk=2, dk=64, dv=64, status=None):
+        return lib.gdn_step(q, FAKE, FAKE, dtype, FAKE, FAKE, S, FAKE, FAKE, FAKE, 0, batch, slots,
+                            H, Hk, dk, dv, status, None)
+    assert step(q=None) == -1 and step(S=ODD) == -1 and step(status=ODD) == -1
+    assert step(batch=0) == -1 and step(slots=0) == -1 and step(dtype=5) == -1
+    assert step(Hk=3) == -2 and step(dk=20) == -2 and step(dv=256) == -2
+
+
+def attention(lib, null=None, odd=None, dtype=1, groups=0, start=None, shared=None, stride=None,
+              batch=1, n=4, Hq=4, Hkv=2, d=64, page=16, num=8, width=4, ws=FAKE, ws_bytes=1 << 40,
+              status=None):
+    p = [FAKE] * 9       # q k v parent kc vc pages length out
+    if null is not None:
+        p[null] = None
+    if odd is not None:
+        p[odd] = ODD
+    q, k, v, par, kc, vc, pages, length, out = p
+    return lib.gdn_tree_attention(q, k, v, dtype, par, kc, vc,
+                                  Hkv * page * d if stride is None else stride, pages, length,
+                                  start, shared, groups, 0.1, out, batch, n, Hq, Hkv, d, page, num,
+                                  width, ws, ws_bytes, status, None)
+
+
+@pytest.mark.parametrize("i", range(9))
+def test_attention_pointers(lib, i):
+    assert attention(lib, null=i) == -1
+    assert attention(lib, odd=i) == -1
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dtype=0), -1), (dict(dtype=3), -1), (dict(groups=-1), -1), (dict(groups=1), -1),
+    (dict(groups=1, start=FAKE), -1), (dict(groups=1, start=FAKE, shared=ODD), -1),
+    (dict(batch=0), -1), (dict(n=0), -1), (dict(n=129), -2), (dict(Hq=3), -2), (dict(d=60), -2),
+    (dict(d=264), -2), (dict(page=0), -1), (dict(page=24), -2), (dict(num=0), -1),
+    (dict(width=0), -1), (dict(stride=8), -1), (dict(stride=2 * 16 * 64 + 4), -1),
+    (dict(batch=1025), -2), (dict(groups=1025, start=FAKE, shared=FAKE), -2),
+    (dict(width=1 << 27), -2), (dict(ws=None), -1), (dict(ws_bytes=16), -1), (dict(ws=ODD), -1),
+    (dict(status=ODD), -1),
+])
+def test_attention_refuses(lib, kw, code):
+    assert attention(lib, **kw) == code
+
+
+def test_attention_workspace(lib):
+    size = lib.gdn_tree_attention_workspace
+    need = size(2, 4, 8, 2, 64, 16, 10, 0)
+    assert need > 0 and size(2, 4, 8, 2, 64, 16, 10, 1) > need
+    assert attention(lib, batch=2, Hq=8, width=10, ws_bytes=need - 1) == -1
+    assert size(0, 4, 8, 2, 64, 16, 10, 0) == 0 and size(2, 4, 8, 2, 64, 24, 10, 0) == 0
+
+
+def test_pages_refuse(lib):
+    P = FAKE
+
+    def table(fn, a=P, b=P, c=P, t=P, m=2, seqs=4, width=4, pool=8, page=16, status=None):
+        return fn(t, P, P, a, b, c, m, seqs, width, pool, page, status, None)
+    for fn in (lib.gdn_page_fork, lib.gdn_page_extend):
+        assert table(fn, a=None) == -1 and table(fn, b=None) == -1 and table(fn, c=None) == -1
+        assert table(fn, t=None) == -1 and table(fn, t=ODD) == -1 and table(fn, c=ODD) == -1
+        assert table(fn, m=-1) == -1 and table(fn, m=4097) == -2 and table(fn, page=24) == -2
+        assert table(fn, page=0) == -1 and table(fn, seqs=0) == -1 and table(fn, pool=0) == -1
+        assert table(fn, width=1 << 28) == -2 and table(fn, status=ODD) == -1
+        assert table(fn, m=0) == 0                     # nothing to do, nothing launched
+    free = lambda t=P, done=P, m=1, page=16: lib.gdn_page_free(t, P, P, done, m, 4, 4, 8, page,
+                                                               None, None)
+    assert free(t=None) == -1 and free(done=None) == -1 and free(done=ODD) == -1
+    assert free(page=3) == -2 and free(m=0) == 0
+    pack = lambda copies=P, count=P, ws=P, pool=8: lib.gdn_page_compact(P, P, P, copies, count, ws,
+                                                                        4, 4, pool, 16, None)
+    assert pack(copies=None) == -1 and pack(count=None) == -1 and pack(ws=None) == -1
+    assert pack(ws=ODD) == -1 and pack(pool=0) == -1
+    copy = lambda cache=P, copies=P, m=1, planes=2, pool=8, size=64: lib.gdn_page_copy(
+        cache, copies, None, m, planes, pool, size, None)
+    assert copy(cache=None) == -1 and copy(copies=None) == -1 and copy(size=24) == -1
+    assert copy(planes=0) == -1 and copy(pool=0) == -1 and copy(planes=1 << 20) == -2
+    assert copy(m=0) == 0 and copy(cache=ODD) == -1
+
+    def rows(kc=P, k=P, stride=2 * 16 * 64, m=1, n=4, max_path=4, Hkv=2, d=64, size=2, page=16):
+        return lib.gdn_kv_commit(kc, P, stride, P, P, P, k, P, P, P, m, n, max_path, Hkv, d, size,
+                                 4, 4, 8, page, None, None)
+    assert rows(kc=None) == -1 and rows(k=ODD) == -1 and rows(size=3) == -1 and rows(n=0) == -1
+    assert rows(d=60) == -2 and rows(page=24) == -2 and rows(stride=64) == -1 and rows(m=0) == 0
+
+
+def test_binding_refuses_what_the_gpu_calls_cannot_take():
+    torch = pytest.importorskip("torch")
+    z = torch.zeros
+    i = lambda *s: z(*s, dtype=torch.int32)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        g.step(z(1, 2, 64), z(1, 2, 64), z(1, 2, 64), z(1, 2), z(1, 2), z(2, 2, 64, 64), i(1), i(1))
+    with pytest.raises(ValueError, match="GPU tensor"):
+        g.prefill(z(1, 2, 64), z(1, 2, 64), z(1, 2, 64), z(1, 2), z(1, 2), i(2), z(2, 2, 64, 64),
+                  i(1), i(1))
+    h = lambda *s: z(*s, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        g.tree_attention(h(1, 1, 2, 64), h(1, 1, 1, 64), h(1, 1, 1, 64), i(1, 1), h(4, 1, 16, 64),
+                         h(4, 1, 16, 64), i(1, 2), i(1), 0.1)
+    with pytest.raises(TypeError):
+        g.page_fork(None, i(4), i(8), i(1), i(1), 16)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        g.page_free(i(4, 4), i(4), i(8), i(1), 16)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        g.page_copy(h(2, 8, 64), i(1, 2))
+    with pytest.raises(ValueError, match="GPU tensor"):
+        g.kv_commit(h(8, 1, 16, 64), h(8, 1, 16, 64), i(4, 4), i(1), i(1), h(1, 1, 1, 64),
+                    h(1, 1, 1, 64), i(1, 1), i(1))
