@@ -136,8 +136,4 @@ hipError_t launch_step(const RuleArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
-int64_t prefill_workspace(const RuleArgs &) { return 0; }
-
-hipError_t launch_prefill(const RuleArgs &a, hipStream_t s) { return launch_step(a, s); }
-
 }  // namespace gdn

@@ -299,7 +299,9 @@ gdn_status gdn_tree_index(const int32_t *parent, int32_t *depth,
  * its out rows are NaN, no state is written).
  * workspace: device memory of at least gdn_prefill_workspace(...) bytes,
  * contents ignored; one call at a time may use it.
- * Arithmetic: products, sums and the state in fp32.
+ * Arithmetic: products, sums and the state to fp32's precision (on the bf16
+ * matrix unit the fp32 factors enter as three bf16 parts); decays from a
+ * 64-bit sum of logarithms.
  */
 int64_t gdn_prefill_workspace(gdn_dtype qkv_dtype, int batch, int rows, int H,
                               int Hk, int d_k, int d_v);
