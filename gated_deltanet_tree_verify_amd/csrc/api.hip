@@ -42,6 +42,8 @@ gdn_status rule_status(const gdn::RuleArgs &a) {
     if (a.batch < 1 || a.rows < 0 || a.slots < 1 || a.H < 1 || a.Hk < 1 || a.dk < 1 || a.dv < 1)
         return GDN_ERR_INVALID_ARG;
     if (a.H % a.Hk != 0 || !dim_ok(a.dk) || !dim_ok(a.dv)) return GDN_ERR_UNSUPPORTED;
+    // a chunk's rows are addressed with 32-bit byte offsets
+    if (a.H > 16384) return GDN_ERR_UNSUPPORTED;
     // grids of (tokens / 64 + batch) * H workgroups and up to 16 per (sequence, head)
     if (((long long)a.rows / 64 + a.batch) * a.H > 0x7ffffffLL) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;

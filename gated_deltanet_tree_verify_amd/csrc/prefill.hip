@@ -83,11 +83,15 @@ struct Half {
     static __device__ __forceinline__ f32x4 gram(const Raw8 &x, const Raw8 &y, f32x4 c) {
         return mma(v(x.p[0]), v(y.p[0]), c);
     }
-    // exact . fp32, smallest part first
-    static __device__ __forceinline__ f32x4 mul(const Raw8 &x, const Raw8 &y, f32x4 c) {
-        c = mma(v(x.p[0]), v(y.p[2]), c);
-        c = mma(v(x.p[0]), v(y.p[1]), c);
-        return mma(v(x.p[0]), v(y.p[0]), c);
+    // exact . fp32, two operands x at once: the instructions of one sum wait
+    // for each other, those of the two alternate.  Smallest part first.
+    static __device__ __forceinline__ void mul(const Raw8 &x0, const Raw8 &x1, const Raw8 &y,
+                                               f32x4 &c0, f32x4 &c1) {
+#pragma unroll
+        for (int p = 2; p >= 0; --p) {
+            c0 = mma(v(x0.p[0]), v(y.p[p]), c0);
+            c1 = mma(v(x1.p[0]), v(y.p[p]), c1);
+        }
     }
     // fp32 . fp32
     static __device__ __forceinline__ f32x4 mul2(const Raw8 &x, const Raw8 &y, f32x4 c) {
@@ -134,6 +138,15 @@ struct Half {
         if (ok) x.p[0] = *reinterpret_cast<const uint4 *>(p);
         return x;
     }
+    static __device__ __forceinline__ Raw8 load8(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+        Raw8 x;
+        x.p[0] = tile::load16<0>(r, off);
+        return x;
+    }
+    static __device__ __forceinline__ uint32_t load1(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+        return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)off, 0, 0);
+    }
+    static __device__ __forceinline__ float widen(uint32_t x) { return __uint_as_float(x << 16); }
 };
 
 // fp32 q, k: the fp32 matrix instruction, eight per 32 indices
@@ -152,8 +165,10 @@ struct Full {
                                                      __uint_as_float(ys[e]), c, 0, 0, 0);
         return c;
     }
-    static __device__ __forceinline__ f32x4 mul(const Raw8 &x, const Raw8 &y, f32x4 c) {
-        return gram(x, y, c);
+    static __device__ __forceinline__ void mul(const Raw8 &x0, const Raw8 &x1, const Raw8 &y,
+                                               f32x4 &c0, f32x4 &c1) {
+        c0 = gram(x0, y, c0);
+        c1 = gram(x1, y, c1);
     }
     static __device__ __forceinline__ f32x4 mul2(const Raw8 &x, const Raw8 &y, f32x4 c) {
         return gram(x, y, c);
@@ -173,7 +188,27 @@ struct Full {
         }
         return x;
     }
+    static __device__ __forceinline__ Raw8 load8(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+        Raw8 x;
+        x.p[0] = tile::load16<0>(r, off);
+        x.p[1] = tile::load16<0>(r, off + 16);
+        return x;
+    }
+    static __device__ __forceinline__ uint32_t load1(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+        return __builtin_amdgcn_raw_buffer_load_b32(r, (int)off, 0, 0);
+    }
+    static __device__ __forceinline__ float widen(uint32_t x) { return __uint_as_float(x); }
 };
+
+__device__ __forceinline__ void store1(__amdgpu_buffer_rsrc_t r, uint32_t off, float x, uint16_t) {
+    __builtin_amdgcn_raw_buffer_store_b16(tile::bf16_bits(x), r, (int)off, 0, 0);
+}
+__device__ __forceinline__ void store1(__amdgpu_buffer_rsrc_t r, uint32_t off, float x, float) {
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), r, (int)off, 0, 0);
+}
+
+// an offset past the end of any buffer: loads give zero, stores do nothing
+constexpr uint32_t kNowhere = 0x80000000u;
 
 // one (chunk, head) of the workspace
 template <typename M>
@@ -442,9 +477,9 @@ __global__ __launch_bounds__(kThreads) void prefill_scan_kernel(RuleArgs a, Layo
     rule::Sequence sq = rule::sequence(a, i);
     if (pre < 0) sq.fault = kFaultBadLength;
     if (a.status && h == 0 && ct == 0 && tid == 0) a.status[i] = sq.fault;
-    OT *out = static_cast<OT *>(a.out) + (size_t)h * a.dv + col;
     const size_t ostride = (size_t)a.H * a.dv;
     if (sq.fault) {
+        OT *out = static_cast<OT *>(a.out) + (size_t)h * a.dv + col;
         if (!(sq.fault & kFaultBadLength) && clive)
             for (int t = tid >> 4; t < sq.len; t += kThreads / 16)
                 rule::put(&out[((size_t)sq.first + t) * ostride], __builtin_nanf(""));
@@ -472,8 +507,8 @@ __global__ __launch_bounds__(kThreads) void prefill_scan_kernel(RuleArgs a, Layo
 
     const T *kp = static_cast<const T *>(a.k) + ((size_t)sq.first * a.Hk + hk) * a.dk;
     const T *qp = static_cast<const T *>(a.q) + ((size_t)sq.first * a.Hk + hk) * a.dk;
-    const T *vp = static_cast<const T *>(a.v) + (size_t)sq.first * ostride + (size_t)h * a.dv + col;
-    out += (size_t)sq.first * ostride;
+    const T *vp = static_cast<const T *>(a.v) + (size_t)sq.first * ostride + (size_t)h * a.dv;
+    const OT *op = static_cast<const OT *>(a.out) + (size_t)sq.first * ostride + (size_t)h * a.dv;
     const size_t kstride = (size_t)a.Hk * a.dk;
     const ChunkData<M> *data =
         reinterpret_cast<const ChunkData<M> *>(ws + y.off_data) + (size_t)pre * a.H + h;
@@ -483,22 +518,42 @@ __global__ __launch_bounds__(kThreads) void prefill_scan_kernel(RuleArgs a, Layo
 
     const int tok = rho(w, m);                      // this lane's row of K, Q
     const int tok4 = 32 * (w >> 1) + 8 * qd + 4 * (w & 1);   // its four tokens of R, U, O
+    // rows of a chunk are addressed from its first: 32-bit offsets, and what
+    // lies past the chunk's tokens reads as zero with no branch, so that a
+    // load is waited for where it is used
+    uint32_t koff[J], voff[4], ooff[4];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        const int d0 = 32 * j + 8 * qd;
+        koff[j] = d0 < a.dk ? (uint32_t)((tok * kstride + d0) * sizeof(T)) : kNowhere;
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const size_t e = (tok4 + r) * ostride + col;
+        voff[r] = clive ? (uint32_t)(e * sizeof(T)) : kNowhere;
+        ooff[r] = clive ? (uint32_t)(e * sizeof(OT)) : kNowhere;
+    }
+    auto tokens = [&](int c) { return min(kC, sq.len - kC * c); };
+    auto rsrc = [&](const void *p, size_t row, size_t width, size_t size, int c) {
+        return tile::make_rsrc(static_cast<const char *>(p) + (size_t)kC * c * row * size,
+                               (uint32_t)(((tokens(c) - 1) * row + width) * size));
+    };
     Raw8 kf[J], qf[J], tf[2], yf[2], kt[2][2];
     float4 vec[4];
-    float vv[4], egl = 0.f;
+    uint32_t vv[4];
+    float egl = 0.f;
     auto load_kqv = [&](int c) {
-        const int t = kC * c + tok;
+        const __amdgpu_buffer_rsrc_t rk = rsrc(kp, kstride, a.dk, sizeof(T), c);
+        const __amdgpu_buffer_rsrc_t rq = rsrc(qp, kstride, a.dk, sizeof(T), c);
+        const __amdgpu_buffer_rsrc_t rv = rsrc(vp, ostride, a.dv, sizeof(T), c);
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            const int d0 = 32 * j + 8 * qd;
-            const bool ok = t < sq.len && d0 < a.dk;
-            kf[j] = M::load8(kp + (size_t)t * kstride + d0, ok);
-            qf[j] = M::load8(qp + (size_t)t * kstride + d0, ok);
+            kf[j] = M::load8(rk, koff[j]);
+            qf[j] = M::load8(rq, koff[j]);
         }
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const int tv = kC * c + tok4 + r;
-            vv[r] = tv < sq.len && clive ? to_f32(vp[(size_t)tv * ostride]) : 0.f;
+            vv[r] = M::load1(rv, voff[r]);
             vec[r] = data[(size_t)c * a.H].vec[tok4 + r];
         }
     };
@@ -555,14 +610,13 @@ __global__ __launch_bounds__(kThreads) void prefill_scan_kernel(RuleArgs a, Layo
 #pragma unroll
         for (int j = 0; j < J; ++j) {
             const Raw8 b = read(s_s, j);
-            ks = M::mul(kf[j], b, ks);
-            qs = M::mul(qf[j], b, qs);
+            M::mul(kf[j], qf[j], b, ks, qs);
         }
         f32x4 u;
         float wl[4];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            u[r] = vec[r].x * vv[r] - vec[r].y * ks[r];
+            u[r] = vec[r].x * M::widen(vv[r]) - vec[r].y * ks[r];
             qs[r] *= vec[r].z;
             wl[r] = vec[r].w;
         }
@@ -589,19 +643,16 @@ __global__ __launch_bounds__(kThreads) void prefill_scan_kernel(RuleArgs a, Layo
 #pragma unroll
             for (int jt = 0; jt < 2; ++jt) {
                 const Raw8 b = read(s_w, jt);
-                st[0] = M::mul(kt[0][jt], b, st[0]);
-                st[1] = M::mul(kt[1][jt], b, st[1]);
+                M::mul(kt[0][jt], kt[1][jt], b, st[0], st[1]);
             }
             put_state();
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j)
             if (j <= w >> 1) qs = M::mul2(yf[j], read(s_u, j), qs);
+        const __amdgpu_buffer_rsrc_t ro = rsrc(op, ostride, a.dv, sizeof(OT), c);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int t = kC * c + tok4 + r;
-            if (t < sq.len && clive) rule::put(&out[(size_t)t * ostride], qs[r]);
-        }
+        for (int r = 0; r < 4; ++r) store1(ro, ooff[r], qs[r], OT{});
         load_yk(next);
         lds_barrier();
     }
