@@ -30,9 +30,9 @@
 // and results feed the next product with no exchange inside the wave.
 //
 // Precision.  bf16 q, k are exact operands.  fp32 factors (S, R, U, W, T - I, Y)
-// enter as three bf16 parts, x = hi + mid + lo to 2^-27 |x|, and products of
-// two of them keep the six part products down to 2^-18: the result is that of
-// fp32 products.  Two parts were off by 2e-6 each (measured: 4.6e-6 in the
+// enter as three bf16 parts, x = hi + mid + lo exactly, and products of two of
+// them keep the six part products down to 2^-16 (those left out are below
+// 2^-23): the result is that of fp32 products.  Two parts were off by 2e-6 each (measured: 4.6e-6 in the
 // output's 2-norm), more than fp32 sums are.  fp32 q, k take the fp32 matrix
 // instruction.  g is summed in 64 bits: decays of late tokens are differences
 // of large sums.
@@ -93,26 +93,29 @@ struct Half {
             c1 = mma(v(x1.p[0]), v(y.p[p]), c1);
         }
     }
-    // fp32 . fp32
-    static __device__ __forceinline__ f32x4 mul2(const Raw8 &x, const Raw8 &y, f32x4 c) {
+    // fp32 . fp32 into c + d: two sums that alternate
+    static __device__ __forceinline__ void mul2(const Raw8 &x, const Raw8 &y, f32x4 &c, f32x4 &d) {
+        d = mma(v(x.p[1]), v(y.p[1]), d);
         c = mma(v(x.p[2]), v(y.p[0]), c);
-        c = mma(v(x.p[1]), v(y.p[1]), c);
-        c = mma(v(x.p[0]), v(y.p[2]), c);
+        d = mma(v(x.p[0]), v(y.p[2]), d);
         c = mma(v(x.p[1]), v(y.p[0]), c);
-        c = mma(v(x.p[0]), v(y.p[1]), c);
-        return mma(v(x.p[0]), v(y.p[0]), c);
+        d = mma(v(x.p[0]), v(y.p[1]), d);
+        c = mma(v(x.p[0]), v(y.p[0]), c);
     }
+    // by truncation: the upper halves of x, of what is left and of what is
+    // left then are 8 bits each, 24 together, so the parts sum to x exactly
     static __device__ __forceinline__ void split(const float *x, uint2 *part) {
         float r[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
         for (int p = 0; p < 3; ++p) {
-            bf16x4 h;
+            uint32_t u[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                h[i] = static_cast<__bf16>(r[i]);
-                r[i] -= static_cast<float>(h[i]);      // exact
-            }
-            part[p] = __builtin_bit_cast(uint2, h);
+            for (int i = 0; i < 4; ++i) u[i] = __float_as_uint(r[i]);
+            part[p].x = __builtin_amdgcn_perm(u[1], u[0], 0x07060302u);
+            part[p].y = __builtin_amdgcn_perm(u[3], u[2], 0x07060302u);
+            if (p < 2)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) r[i] -= __uint_as_float(u[i] & 0xffff0000u);
         }
     }
     // registers of tile 2 j + s as half of pair j's operand
@@ -170,8 +173,8 @@ struct Full {
         c0 = gram(x0, y, c0);
         c1 = gram(x1, y, c1);
     }
-    static __device__ __forceinline__ f32x4 mul2(const Raw8 &x, const Raw8 &y, f32x4 c) {
-        return gram(x, y, c);
+    static __device__ __forceinline__ void mul2(const Raw8 &x, const Raw8 &y, f32x4 &c, f32x4 &) {
+        c = gram(x, y, c);
     }
     static __device__ __forceinline__ void put_tile(uint4 (*buf)[kParts][64], int j, int s, int l,
                                                     const f32x4 &x) {
@@ -448,12 +451,13 @@ __global__ __launch_bounds__(kThreads) void prefill_chunk_kernel(RuleArgs a, Lay
 // ---------------------------------------------------------------------------
 // scan: the state through a sequence's chunks
 // ---------------------------------------------------------------------------
-template <typename M, int DK, typename OT>
-__global__ __launch_bounds__(kThreads) void prefill_scan_kernel(RuleArgs a, Layout y, int tiles) {
+template <typename M, int DK, typename OT, int G>
+__global__ __launch_bounds__(kThreads, 2) void prefill_scan_kernel(RuleArgs a, Layout y,
+                                                                   int tiles) {
     typedef typename M::elem T;
     constexpr int J = DK / 32;
     constexpr int N = M::kParts;
-    __shared__ uint4 s_s[J][N][64], s_r[2][N][64], s_u[2][N][64], s_w[2][N][64];
+    __shared__ uint4 s_s[G][J][N][64], s_r[G][2][N][64], s_u[G][2][N][64], s_w[G][2][N][64];
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
     const int m = l & 15, qd = l >> 4;
     char *ws = static_cast<char *>(a.workspace);
@@ -471,37 +475,46 @@ __global__ __launch_bounds__(kThreads) void prefill_scan_kernel(RuleArgs a, Layo
     }
     const int i = reinterpret_cast<const int *>(ws + y.off_order)[u / a.H], h = u % a.H;
     const int hk = h / (a.H / a.Hk);
-    const int col = kCols * ct + m;
-    const bool clive = col < a.dv;
+    const int col0 = kCols * G * ct + m;              // and kCols further on for each group
     const int pre = reinterpret_cast<const int *>(ws + y.off_pre)[i];
     rule::Sequence sq = rule::sequence(a, i);
     if (pre < 0) sq.fault = kFaultBadLength;
     if (a.status && h == 0 && ct == 0 && tid == 0) a.status[i] = sq.fault;
     const size_t ostride = (size_t)a.H * a.dv;
     if (sq.fault) {
-        OT *out = static_cast<OT *>(a.out) + (size_t)h * a.dv + col;
-        if (!(sq.fault & kFaultBadLength) && clive)
+        OT *out = static_cast<OT *>(a.out) + (size_t)h * a.dv + col0;
+        if (!(sq.fault & kFaultBadLength))
             for (int t = tid >> 4; t < sq.len; t += kThreads / 16)
-                rule::put(&out[((size_t)sq.first + t) * ostride], __builtin_nanf(""));
+#pragma unroll
+                for (int g = 0; g < G; ++g)
+                    if (col0 + kCols * g < a.dv)
+                        rule::put(&out[((size_t)sq.first + t) * ostride + kCols * g],
+                                  __builtin_nanf(""));
         return;
     }
 
-    // ---- rows rho(2 w, .) and rho(2 w + 1, .) of the state's 16 columns
+    // ---- rows rho(2 w, .) and rho(2 w + 1, .) of the state's columns
     const size_t slab = (size_t)a.H * a.dk * a.dv;
-    const size_t sat = (size_t)h * a.dk * a.dv + col;
+    const size_t sat = (size_t)h * a.dk * a.dv + col0;
     const int sr = 32 * w + 8 * qd;                 // the lane's eight rows
-    const bool slive = w < J && sr < a.dk && clive;
-    f32x4 st[2] = {};
+    const bool slive = w < J && sr < a.dk;
+    f32x4 st[G][2] = {};
     if (slive && sq.src >= 0) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            st[e >> 2][e & 3] = a.S[sq.src * slab + sat + (size_t)(sr + e) * a.dv];
+        for (int g = 0; g < G; ++g)
+            if (col0 + kCols * g < a.dv)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    st[g][e >> 2][e & 3] =
+                        a.S[sq.src * slab + sat + (size_t)(sr + e) * a.dv + kCols * g];
     }
     auto put_state = [&]() {
-        if (w < J) {
-            M::put_tile(s_s, w, 0, l, st[0]);
-            M::put_tile(s_s, w, 1, l, st[1]);
-        }
+        if (w < J)
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                M::put_tile(s_s[g], w, 0, l, st[g][0]);
+                M::put_tile(s_s[g], w, 1, l, st[g][1]);
+            }
     };
     put_state();
 
@@ -521,61 +534,56 @@ __global__ __launch_bounds__(kThreads) void prefill_scan_kernel(RuleArgs a, Layo
     // rows of a chunk are addressed from its first: 32-bit offsets, and what
     // lies past the chunk's tokens reads as zero with no branch, so that a
     // load is waited for where it is used
-    uint32_t koff[J], voff[4], ooff[4];
+    uint32_t koff[J], voff[G];
 #pragma unroll
     for (int j = 0; j < J; ++j) {
         const int d0 = 32 * j + 8 * qd;
         koff[j] = d0 < a.dk ? (uint32_t)((tok * kstride + d0) * sizeof(T)) : kNowhere;
     }
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const size_t e = (tok4 + r) * ostride + col;
-        voff[r] = clive ? (uint32_t)(e * sizeof(T)) : kNowhere;
-        ooff[r] = clive ? (uint32_t)(e * sizeof(OT)) : kNowhere;
-    }
+    for (int g = 0; g < G; ++g)
+        voff[g] = col0 + kCols * g < a.dv ? (uint32_t)(tok4 * ostride + col0 + kCols * g) : kNowhere;
     auto tokens = [&](int c) { return min(kC, sq.len - kC * c); };
     auto rsrc = [&](const void *p, size_t row, size_t width, size_t size, int c) {
         return tile::make_rsrc(static_cast<const char *>(p) + (size_t)kC * c * row * size,
                                (uint32_t)(((tokens(c) - 1) * row + width) * size));
     };
+    // an element offset of kNowhere stays past the end in bytes
+    auto bytes = [&](uint32_t off, int r, uint32_t size) {
+        return off == kNowhere ? kNowhere : (off + (uint32_t)(r * ostride)) * size;
+    };
     Raw8 kf[J], qf[J], tf[2], yf[2], kt[2][2];
     float4 vec[4];
-    uint32_t vv[4];
+    uint32_t vv[G][4];
     float egl = 0.f;
-    auto load_kqv = [&](int c) {
+    auto load_kq = [&](int c) {
         const __amdgpu_buffer_rsrc_t rk = rsrc(kp, kstride, a.dk, sizeof(T), c);
         const __amdgpu_buffer_rsrc_t rq = rsrc(qp, kstride, a.dk, sizeof(T), c);
-        const __amdgpu_buffer_rsrc_t rv = rsrc(vp, ostride, a.dv, sizeof(T), c);
 #pragma unroll
         for (int j = 0; j < J; ++j) {
             kf[j] = M::load8(rk, koff[j]);
             qf[j] = M::load8(rq, koff[j]);
         }
+    };
+    auto load_tv = [&](int c) {
+        const ChunkData<M> *p = data + (size_t)c * a.H;
+        const __amdgpu_buffer_rsrc_t rv = rsrc(vp, ostride, a.dv, sizeof(T), c);
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            vv[r] = M::load1(rv, voff[r]);
-            vec[r] = data[(size_t)c * a.H].vec[tok4 + r];
+#pragma unroll
+            for (int g = 0; g < G; ++g) vv[g][r] = M::load1(rv, bytes(voff[g], r, sizeof(T)));
+            vec[r] = p->vec[tok4 + r];
         }
-    };
-    auto load_t = [&](int c) {
-        const ChunkData<M> *p = data + (size_t)c * a.H;
 #pragma unroll
         for (int j = 0; j < 2; ++j)
             if (j <= w >> 1) {
                 const int f = frag_of(w, j);
 #pragma unroll
-                for (int i = 0; i < N; ++i) tf[j].p[i] = p->t[f][i][l];
+                for (int n = 0; n < N; ++n) tf[j].p[n] = p->t[f][n][l];
             }
     };
     auto load_yk = [&](int c) {
         const ChunkData<M> *p = data + (size_t)c * a.H;
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            if (j <= w >> 1) {
-                const int f = frag_of(w, j);
-#pragma unroll
-                for (int i = 0; i < N; ++i) yf[j].p[i] = p->y[f][i][l];
-            }
         egl = p->vec[kC - 1].z;
         if (w < J) {
             const uint4 *q = ktp + (size_t)c * a.Hk * ktsize;
@@ -585,81 +593,113 @@ __global__ __launch_bounds__(kThreads) void prefill_scan_kernel(RuleArgs a, Layo
                 for (int jt = 0; jt < 2; ++jt) {
                     const int f = ((2 * w + s) * 2 + jt) * M::kExact;
 #pragma unroll
-                    for (int i = 0; i < M::kExact; ++i) kt[s][jt].p[i] = q[(f + i) * 64 + l];
+                    for (int n = 0; n < M::kExact; ++n) kt[s][jt].p[n] = q[(f + n) * 64 + l];
                 }
         }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            if (j <= w >> 1) {
+                const int f = frag_of(w, j);
+#pragma unroll
+                for (int n = 0; n < N; ++n) yf[j].p[n] = p->y[f][n][l];
+            }
     };
     auto read = [&](uint4(*buf)[N][64], int j) {
-        Raw8 x;
+        Raw8 b;
 #pragma unroll
-        for (int i = 0; i < N; ++i) x.p[i] = buf[j][i][l];
-        return x;
+        for (int n = 0; n < N; ++n)
+            b.p[n] = buf[j][n][l];
+        return b;
     };
 
+    // Each phase first reads the operands that the barrier before it made
+    // good, then issues the loads whose registers the last phase set free (a
+    // chunk ahead of their use, a third of them in each phase), then
+    // multiplies.
     const int chunks = (sq.len + kC - 1) / kC;
     if (chunks > 0) {
-        load_kqv(0);
-        load_t(0);
-        load_yk(0);
+        load_kq(0);
+        load_tv(0);
     }
     lds_barrier();
     for (int c = 0; c < chunks; ++c) {
         const int next = min(c + 1, chunks - 1);
         // ---- R of 16 tokens (and Q S)
-        f32x4 ks = {}, qs = {};
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const Raw8 b = read(s_s, j);
-            M::mul(kf[j], qf[j], b, ks, qs);
-        }
-        f32x4 u;
+        f32x4 ks[G] = {}, qs[G] = {}, uu[G];
         float wl[4];
+        load_yk(c);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            u[r] = vec[r].x * M::widen(vv[r]) - vec[r].y * ks[r];
-            qs[r] *= vec[r].z;
-            wl[r] = vec[r].w;
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const Raw8 b = read(s_s[g], j);
+                M::mul(kf[j], qf[j], b, ks[g], qs[g]);
+            }
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                uu[g][r] = vec[r].x * M::widen(vv[g][r]) - vec[r].y * ks[g][r];
+                qs[g][r] *= vec[r].z;
+            }
+            M::put_tile(s_r[g], w >> 1, w & 1, l, uu[g]);
         }
-        M::put_tile(s_r, w >> 1, w & 1, l, u);
-        load_kqv(next);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) wl[r] = vec[r].w;
         lds_barrier();
 
         // ---- U = R + (T - I) R, W
+        load_kq(next);
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-            if (j <= w >> 1) u = M::mul2(tf[j], read(s_r, j), u);
-        M::put_tile(s_u, w >> 1, w & 1, l, u);
-        f32x4 wv;
+        for (int g = 0; g < G; ++g) {
+            f32x4 more = {};
 #pragma unroll
-        for (int r = 0; r < 4; ++r) wv[r] = wl[r] * u[r];
-        M::put_tile(s_w, w >> 1, w & 1, l, wv);
-        load_t(next);
+            for (int j = 0; j < 2; ++j)
+                if (j <= w >> 1) M::mul2(tf[j], read(s_r[g], j), uu[g], more);
+            uu[g] += more;
+            f32x4 wv;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) wv[r] = wl[r] * uu[g][r];
+            M::put_tile(s_w[g], w >> 1, w & 1, l, wv);
+            M::put_tile(s_u[g], w >> 1, w & 1, l, uu[g]);
+        }
         lds_barrier();
 
         // ---- S <- e^{g_l} S + K^T W, O = e^g Q S + Y U
+        load_tv(next);
         if (w < J) {
-            st[0] *= egl;
-            st[1] *= egl;
 #pragma unroll
-            for (int jt = 0; jt < 2; ++jt) {
-                const Raw8 b = read(s_w, jt);
-                M::mul(kt[0][jt], kt[1][jt], b, st[0], st[1]);
+            for (int g = 0; g < G; ++g) {
+                st[g][0] *= egl;
+                st[g][1] *= egl;
+#pragma unroll
+                for (int jt = 0; jt < 2; ++jt)
+                    M::mul(kt[0][jt], kt[1][jt], read(s_w[g], jt), st[g][0], st[g][1]);
             }
             put_state();
         }
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            if (j <= w >> 1) qs = M::mul2(yf[j], read(s_u, j), qs);
         const __amdgpu_buffer_rsrc_t ro = rsrc(op, ostride, a.dv, sizeof(OT), c);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) store1(ro, ooff[r], qs[r], OT{});
-        load_yk(next);
+        for (int g = 0; g < G; ++g) {
+            f32x4 more = {};
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                if (j <= w >> 1) M::mul2(yf[j], read(s_u[g], j), qs[g], more);
+            qs[g] += more;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                store1(ro, bytes(voff[g], r, sizeof(OT)), qs[g][r], OT{});
+        }
         lds_barrier();
     }
     if (slive) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            a.S[sq.dst * slab + sat + (size_t)(sr + e) * a.dv] = st[e >> 2][e & 3];
+        for (int g = 0; g < G; ++g)
+            if (col0 + kCols * g < a.dv)
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    a.S[sq.dst * slab + sat + (size_t)(sr + e) * a.dv + kCols * g] =
+                        st[g][e >> 2][e & 3];
     }
 }
 
@@ -681,6 +721,21 @@ Layout layout(const RuleArgs &a) {
     return y;
 }
 
+// Two column groups a wave load the chunk's operands once for 32 columns; one
+// group gives twice the workgroups.
+bool wide_scan(const RuleArgs &a) {
+    const long long wide = (long long)a.batch * a.H * ((a.dv + 2 * kCols - 1) / (2 * kCols));
+    return wide >= device_cu_count();
+}
+
+template <typename M, int DK, typename OT, int G>
+hipError_t launch_scan(const RuleArgs &a, const Layout &y, hipStream_t s) {
+    const int tiles = (a.dv + kCols * G - 1) / (kCols * G);
+    hipLaunchKernelGGL((prefill_scan_kernel<M, DK, OT, G>),
+                       dim3((unsigned)a.batch * a.H * tiles), dim3(kThreads), 0, s, a, y, tiles);
+    return hipGetLastError();
+}
+
 template <typename M, int DK>
 hipError_t launch(const RuleArgs &a, hipStream_t s) {
     const Layout y = layout(a);
@@ -691,15 +746,10 @@ hipError_t launch(const RuleArgs &a, hipStream_t s) {
                        dim3(kThreads), 0, s, a, y);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int tiles = (a.dv + kCols - 1) / kCols;
-    const dim3 grid((unsigned)a.batch * a.H * tiles);
-    if (a.out_dtype == GDN_DTYPE_BF16)
-        hipLaunchKernelGGL((prefill_scan_kernel<M, DK, uint16_t>), grid, dim3(kThreads), 0, s, a,
-                           y, tiles);
-    else
-        hipLaunchKernelGGL((prefill_scan_kernel<M, DK, float>), grid, dim3(kThreads), 0, s, a, y,
-                           tiles);
-    return hipGetLastError();
+    const bool half = a.out_dtype == GDN_DTYPE_BF16;
+    if (wide_scan(a)) return half ? launch_scan<M, DK, uint16_t, 2>(a, y, s)
+                                  : launch_scan<M, DK, float, 2>(a, y, s);
+    return half ? launch_scan<M, DK, uint16_t, 1>(a, y, s) : launch_scan<M, DK, float, 1>(a, y, s);
 }
 
 }  // namespace
