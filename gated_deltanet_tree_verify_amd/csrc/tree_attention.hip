@@ -22,9 +22,13 @@
 // Tile: Z^T = K Q^T puts a query row into a lane's column and its keys into
 // the lane's registers, so maxima and sums are in-register plus one exchange
 // between the wave's halves, and e^{z - m} is, rounded, the B operand of
-// O^T += V^T P^T as it stands (mfma_tile.hpp).  A unit of up to 32 rows has
-// its four waves take different keys of the tile (merged through LDS at the
-// unit's end), one of more rows has them take 32 rows each.
+// O^T += V^T P^T as it stands (mfma_tile.hpp).  Keys and values go from memory
+// to LDS directly (no registers), the next tile while this one is computed;
+// the values' transpose is the LDS read's (ds_read_b64_tr_b16).  A unit of more
+// than 64 rows gives each of its four waves 32 of them and all keys; up to 64
+// rows, two waves and half the keys each; up to 32 rows (decoding), a wave has
+// half the keys and half the value columns, and the halves merge through LDS
+// at the unit's end.
 #include "device_common.hpp"
 #include "serving.hpp"
 #include "mfma_tile.hpp"
@@ -36,7 +40,7 @@ using namespace tile;
 
 constexpr int kThreads = 256;
 constexpr int kWaves = 4;
-constexpr int kKeys = 128;                // keys of a tile
+constexpr int kKeys = 64;                 // keys of a tile
 constexpr int kRows = 128;                // rows of a unit at most
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -171,40 +175,144 @@ __device__ __forceinline__ long long wave_inclusive64(long long x) {
 }
 
 template <int D>
+struct Tile {
+    uint16_t k[kKeys * D];               // rows of keys, 16-byte pieces turned (k_piece)
+    uint16_t v[kKeys * D];               // rows of values (v_piece)
+};
+
 struct Smem {
-    uint16_t k[kKeys * D];               // rows of keys, 16-byte pieces swizzled
-    uint16_t vt[D * kKeys];              // values transposed, 8-byte pieces swizzled
-    long long off[2][kKeys];             // element offset of a key's row, by tile parity
+    float ml[2][2][32];                  // m and l of the waves that are merged
     uint32_t anc[GDN_MAX_NODES][4];      // ancestor-or-self bits
     int up[GDN_MAX_NODES];
     int start[GDN_MAX_SEQUENCES + 1];
     long long part[kWaves];
-    long long total, first_off;
+    long long first_off;
     int first_entry, max_own, max_shared, bad;
     int lim[kWaves];                     // fewest cached keys seen, over a wave's rows
-    int odd[2];                          // a masked tile has values that are not finite
 };
 
 // Offsets carry their source: cache rows as they are, tree rows with kTree
 // set, keys that are not there -1.
 constexpr long long kTree = 1LL << 62;
 
-// 16-byte piece c (8 elements) of a key row: rows of D elements, the piece's
-// place turned by the key so that 32 keys read at one piece spread over all
-// banks
+// Place of 16-byte piece c (8 elements) in a row: turned by the key, so that
+// 32 keys read at one piece (keys) and 8 keys at four neighbouring pieces
+// (values) spread over the 256 bytes that LDS serves at once.
 template <int D>
-__device__ __forceinline__ int k_at(int key, int c) {
-    constexpr int P = D / 8;                       // pieces of a row
-    const int turn = D >= 128 ? key & 15 : (key >> 1) & 7;
-    return key * D + 8 * ((c & ~15) | ((c ^ turn) & (P < 16 ? P - 1 : 15)));
+__device__ __forceinline__ int k_piece(int key, int c) {
+    return D >= 128 ? c ^ (key & 15) : c ^ ((key >> 1) & 7);
+}
+template <int D>
+__device__ __forceinline__ int v_piece(int key, int c) {
+    return D >= 128 ? c ^ (4 * (key & 3)) : c ^ (4 * ((key >> 1) & 1));
 }
 
-// four keys (8 bytes, quad = place in contraction order) of value column d:
-// the place turned by d so that both the transposing stores (lanes 8 columns
-// apart) and the reads (lanes one column apart) spread over the banks
-__device__ __forceinline__ int v_at(int d, int quad) {
-    const int turn = 2 * (((d >> 3) ^ (2 * (d & 7))) & 15);
-    return d * kKeys + 4 * (quad ^ turn);
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// four elements of a column: lane i of 16 gives the address of piece i % 4 (4
+// elements) of row i / 4 and receives column i of the four rows
+__device__ __forceinline__ uint2 lds_transposed(const uint16_t *p) {
+    return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                         (__attribute__((address_space(3))) s16x4 *)(p)));
+}
+
+// 16 bytes from memory to LDS, lane l to base + 16 l; counted by vmcnt
+__device__ __forceinline__ void load_to_lds(const void *from, uint16_t *base) {
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
+                                     (__attribute__((address_space(3))) void *)base, 16, 0, 0);
+}
+
+// Values that are not finite, in a tile where some rows do not see some keys.
+// They are cleared in v; the result holds, for every row and column, what
+// those with a weight add up to: an infinity, NaN, or 0 where there are none.
+// With a = sum p [not finite] and s = sum p [+inf] - sum p [-inf], formed in
+// the same order, |s| = a exactly when only infinities of one sign were met.
+template <typename E, typename F>
+__device__ __forceinline__ f32x16 odd_values(uint32_t (&v)[8], F times) {
+    uint32_t any[8], sign[8];
+    const uint32_t one = E::bits(1.f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        any[i] = sign[i] = 0;
+#pragma unroll
+        for (int hw = 0; hw < 32; hw += 16) {
+            const uint32_t x = (v[i] >> hw) & 0xffffu;
+            if ((x & E::kExponent) == E::kExponent) {
+                any[i] |= one << hw;
+                if ((x & 0x7fffu) == E::kExponent) sign[i] |= (one | (x & 0x8000u)) << hw;
+                v[i] &= 0xffff0000u >> hw;
+            }
+        }
+    }
+    const f32x16 a = times(any, f32x16{});
+    __builtin_amdgcn_sched_barrier(0);
+    const f32x16 s = times(sign, f32x16{});
+    f32x16 r;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        r[i] = !(a[i] > 0.f) ? 0.f
+               : fabsf(s[i]) == a[i] ? copysignf(__builtin_inff(), s[i]) : __builtin_nanf("");
+    return r;
+}
+
+// x, but not a constant of the loop around: what is computed from it is
+// computed again, a few instructions, instead of held in registers throughout
+__device__ __forceinline__ int keep_in_loop(int x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
+// a value that all lanes share, where the compiler cannot know: into a scalar
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ long long uniform(long long x) {
+    const uint32_t lo = uniform((int)(uint32_t)x), hi = uniform((int)(x >> 32));
+    return (long long)((uint64_t)hi << 32 | lo);
+}
+
+// a tile of the line
+struct Cursor {
+    int e;               // entry
+    int tile, rt, hk;    // tile of the unit, unit of the entry
+    Entry x;
+};
+
+__device__ __forceinline__ void seek(const AttentionArgs &a, const int *start, int groups,
+                                     int entries, Cursor &c, int e) {
+    c.tile = c.rt = c.hk = 0;
+    for (c.e = e; c.e < entries; ++c.e) {
+        const Entry x = entry(a, start, groups, c.e);
+        c.x = {uniform(x.first), uniform(x.rows),  uniform(x.pos0),     uniform(x.cached),
+               uniform(x.keys),  uniform(x.tiles), uniform(x.row_tiles)};
+        if (c.x.tiles > 0 && c.x.row_tiles > 0) return;
+    }
+}
+
+__device__ __forceinline__ void advance(const AttentionArgs &a, const int *start, int groups,
+                                        int entries, Cursor &c) {
+    if (c.e >= entries || ++c.tile < c.x.tiles) return;
+    c.tile = 0;
+    if (++c.rt < c.x.row_tiles) return;
+    c.rt = 0;
+    if (++c.hk < a.Hkv) return;
+    seek(a, start, groups, entries, c, c.e + 1);
+}
+
+// Element offset of key `key` of the cursor's tile, in two steps: the page
+// id's load is issued first and used a tile later.
+__device__ __forceinline__ int key_page(const AttentionArgs &a, const Cursor &c, int key) {
+    const int pos = c.x.pos0 + c.tile * kKeys + key;
+    return a.pages[(size_t)c.x.first * a.max_pages + min(pos >> a.page_log, a.max_pages - 1)];
+}
+__device__ __forceinline__ long long key_offset(const AttentionArgs &a, const Cursor &c, int key,
+                                                int page) {
+    const int j = c.tile * kKeys + key, pos = c.x.pos0 + j;
+    const long long cached =
+        (long long)page * a.page_stride +
+        (((long long)c.hk << a.page_log) + (pos & ((1 << a.page_log) - 1))) * a.d;
+    const long long tree =
+        kTree | ((((long long)c.x.first * a.n + (j - c.x.cached)) * a.Hkv + c.hk) * a.d);
+    if (j >= c.x.cached) return j < c.x.keys ? tree : -1;
+    return page >= 0 && page < a.num_pages ? cached : -1;
 }
 
 template <typename E, int D>
@@ -212,10 +320,14 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
                                                                              Layout lay) {
     typedef typename E::vec vec;
     constexpr int P = D / 8;                       // 16-byte pieces of a row
-    constexpr int kQuads = kKeys / 4;
-    constexpr int kStep = kThreads / P;            // key quads staged at once
-    constexpr int kPasses = kQuads / kStep;
-    __shared__ Smem<D> sm;
+    constexpr int kLoads = kKeys * P / kThreads;   // pieces a thread loads of K, and of V
+    constexpr int DT = D / 32;                     // 32-column tiles of the values
+    // The two tiles and their offsets are objects of their own, and the code
+    // names which one it reads: the compiler then knows that the loads into
+    // the other one need no wait.
+    __shared__ __attribute__((aligned(16))) Tile<D> tile_0, tile_1;
+    __shared__ long long off_0[kKeys], off_1[kKeys];   // element offsets of the keys' rows
+    __shared__ Smem sm;
 
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
     const int m = l & 31, h = l >> 5;
@@ -229,12 +341,18 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
     int groups = a.groups;
     if (tid == 0) sm.bad = 0, sm.max_own = 0, sm.max_shared = 0;
     for (int g = tid; g <= groups && groups > 0; g += kThreads) sm.start[g] = a.gstart[g];
+    // pieces past the head size are never loaded: zero for good
+    if (a.d != D)
+        for (int i = tid; i < (int)sizeof(Tile<D>) / 16; i += kThreads) {
+            reinterpret_cast<uint4 *>(&tile_0)[i] = make_uint4(0, 0, 0, 0);
+            reinterpret_cast<uint4 *>(&tile_1)[i] = make_uint4(0, 0, 0, 0);
+        }
     __syncthreads();
     for (int g = tid; g < groups; g += kThreads)
         if (sm.start[g] < 0 || sm.start[g + 1] < sm.start[g] || sm.start[g + 1] > a.batch)
             sm.bad = 1;
     __syncthreads();
-    if (sm.bad) groups = 0;
+    if (uniform(sm.bad)) groups = 0;
     const int entries = groups + a.batch;
 
     // ---- length of the line and of its longest units
@@ -258,12 +376,13 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
         atomicMax(&sm.max_shared, shared);
     }
     __syncthreads();
-    const long long total = (sm.part[0] + sm.part[1]) + (sm.part[2] + sm.part[3]);
+    const long long total =
+        uniform((sm.part[0] + sm.part[1]) + (sm.part[2] + sm.part[3]));
     // a unit of T tiles meets at most (T - 2) / c + 2 workgroups: c keeps
     // that within the partials there is room for
     long long c = (total + grid - 1) / grid;
-    c = max(c, (long long)(sm.max_own + lay.slots.own - 3) / (lay.slots.own - 1));
-    c = max(c, (long long)(sm.max_shared + lay.slots.shared - 3) / (lay.slots.shared - 1));
+    c = max(c, (long long)(uniform(sm.max_own) + lay.slots.own - 3) / (lay.slots.own - 1));
+    c = max(c, (long long)(uniform(sm.max_shared) + lay.slots.shared - 3) / (lay.slots.shared - 1));
     c = max(c, 1LL);
     const long long t0 = wg * c, t1 = min(total, t0 + c);
     if (t0 >= t1 && wg != 0) return;
@@ -312,61 +431,80 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
     const bool flip = sc < 0.f;        // z = scale q.k: the sign goes into q, exactly
     const uint32_t keep = sc == 0.f ? 0u : ~0u;   // and a scale of zero: masked scores stay -inf
     sc = sc == 0.f ? 1.f : fabsf(sc);
-    const int d8 = tid % P, qd0 = tid / P;        // staging: this thread's piece and first quad
-    const bool dlive = 8 * d8 < a.d;
-    const uint16_t *kc = static_cast<const uint16_t *>(a.kc);
-    const uint16_t *vc = static_cast<const uint16_t *>(a.vc);
-    const uint16_t *kt = static_cast<const uint16_t *>(a.k);
-    const uint16_t *vtree = static_cast<const uint16_t *>(a.v);
+    const char *kc = static_cast<const char *>(a.kc), *vc = static_cast<const char *>(a.vc);
+    const char *kt = static_cast<const char *>(a.k), *vt = static_cast<const char *>(a.v);
 
-    int e = sm.first_entry;
-    long long off = sm.first_off;
+    // the tile that is computed, and the one whose row offsets are looked up
+    Cursor cur, ahead;
+    {
+        seek(a, sm.start, groups, entries, cur, uniform(sm.first_entry));
+        const long long off = uniform(sm.first_off), unit = off / cur.x.tiles;
+        cur.tile = (int)(off - unit * cur.x.tiles);
+        cur.hk = (int)(unit / cur.x.row_tiles);
+        cur.rt = (int)(unit % cur.x.row_tiles);
+        ahead = cur;
+    }
+    auto fetch = [&](Tile<D> &to, const long long *offs) {
+        const int lane = keep_in_loop(l);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int s0 = (w * kLoads + i) * 64;          // the wave's first piece
+            const int key = (s0 + lane) / P, c1 = lane % P;
+            const long long o = offs[key];
+            const size_t at = o >= 0 ? (size_t)(o & ~kTree) * 2 : 0;
+            const bool tr = o >= 0 && (o & kTree);
+            const int ck = k_piece<D>(key, c1), cv = v_piece<D>(key, c1);
+            // a key that is not there: any row (its scores are masked, its
+            // values are cleared before use)
+            if (8 * ck < a.d) load_to_lds((tr ? kt : kc) + at + 16 * ck, &to.k[8 * s0]);
+            if (8 * cv < a.d) load_to_lds((tr ? vt : vc) + at + 16 * cv, &to.v[8 * s0]);
+        }
+    };
+
+    // ---- pipeline: row offsets two tiles ahead, rows one tile ahead
+    if (w == 0) {
+        off_0[l] = key_offset(a, ahead, l, key_page(a, ahead, l));
+    }
+    advance(a, sm.start, groups, entries, ahead);
+    if (w == 0 && ahead.e < entries) off_1[l] = key_offset(a, ahead, l, key_page(a, ahead, l));
+    lds_barrier();
+    fetch(tile_0, off_0);
+
     int anc_of = -1;
     long long t = t0;
     while (t < t1) {
-        const Entry x = entry(a, sm.start, groups, e);
-        const long long in_entry = line_tiles(a, x);
-        if (off >= in_entry) {
-            ++e;
-            off = 0;
-            continue;
-        }
-        const long long unit = off / x.tiles;
-        const int tile0 = (int)(off - unit * x.tiles);
+        const Entry x = cur.x;
+        const int tile0 = cur.tile, hk = cur.hk, r0 = cur.rt * kRows;
         const int count = (int)min((long long)(x.tiles - tile0), t1 - t);
-        const int hk = (int)(unit / x.row_tiles), r0 = (int)(unit % x.row_tiles) * kRows;
         const int slot = wg - (int)((t - tile0) / c);
-        const bool is_own = e >= groups;
+        const bool is_own = cur.e >= groups;
         const int nrows = min(kRows, x.rows - r0);
         const int row_waves = nrows <= 32 ? 1 : nrows <= 64 ? 2 : 4;
-        const int key_waves = kWaves / row_waves;
-        const int wr = w & (row_waves - 1), wk = w / row_waves;
-        const int32_t *prow = a.pages + (size_t)x.first * a.max_pages;
-        const bool tree = is_own && (tile0 + count) * kKeys > x.cached;
+        const int wr = w & (row_waves - 1);
+        const int part = row_waves == 1 ? w & 1 : w >> 1;  // its keys (fewer than 4 row waves)
+        const int half = w >> 1;                           // its columns (1 row wave)
 
         // ---- the tree's ancestor bits, once per sequence: after step i
         // every node knows its 2^i nearest ancestors and jumps that far
-        if (tree && anc_of != x.first) {
+        if (is_own && (tile0 + count) * kKeys > x.cached && anc_of != x.first) {
             anc_of = x.first;
-            __syncthreads();
+            lds_barrier();
             int up = -1;
-            uint32_t bits[4] = {};
             if (tid < a.n) {
                 up = a.parent[(size_t)x.first * a.n + tid];
                 if (!parent_ok(up, tid)) up = -1;
-                bits[tid >> 5] = 1u << (tid & 31);
                 sm.up[tid] = up;
                 for (int i = 0; i < 4; ++i) sm.anc[tid][i] = i == tid >> 5 ? 1u << (tid & 31) : 0u;
             }
             for (int far = 1; far < a.n; far <<= 1) {
-                __syncthreads();
+                lds_barrier();
                 uint32_t more[4] = {};
                 int next = -1;
                 if (tid < a.n && up >= 0) {
                     for (int i = 0; i < 4; ++i) more[i] = sm.anc[up][i];
                     next = sm.up[up];
                 }
-                __syncthreads();
+                lds_barrier();
                 if (tid < a.n && up >= 0) {
                     for (int i = 0; i < 4; ++i) sm.anc[tid][i] |= more[i];
                     sm.up[tid] = up = next;
@@ -378,7 +516,8 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
         const int lr = r0 + 32 * wr + m;                       // row within the entry
         const bool rlive = 32 * wr + m < nrows;
         const int rr = rlive ? lr : r0;
-        const size_t qrow = ((size_t)x.first * a.n + rr / heads) * a.Hq + (size_t)hk * heads + rr % heads;
+        const size_t qrow =
+            ((size_t)x.first * a.n + rr / heads) * a.Hq + (size_t)hk * heads + rr % heads;
         const int node = is_own ? rr / heads : 0;
         const int len_b = clamp_length(a, x.first + rr / heads / a.n);
         const int lim = is_own ? x.cached : min(x.cached, len_b);   // cached keys it sees
@@ -395,126 +534,68 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
             q4.z = (q4.z ^ sign) & keep, q4.w = (q4.w ^ sign) & keep;
             qf[kk] = __builtin_bit_cast(vec, q4);
         }
-        int lim_min = lim;                                     // over the unit's rows
+        int lim_min = lim;                                     // over the wave's rows
         if (!is_own) {
             for (int o = 1; o < 32; o <<= 1) lim_min = min(lim_min, __shfl_xor(lim_min, o));
+            if (l == 0) sm.lim[w] = lim_min;
+            lds_barrier();
         }
-        __syncthreads();
-        if (l == 0) sm.lim[w] = lim_min;
-        if (tid < 2) sm.odd[tid] = 0;
+        const int lim_unit =
+            uniform(is_own ? lim_min : min(min(sm.lim[0], sm.lim[1]), min(sm.lim[2], sm.lim[3])));
 
-        // element offset of a key's row (thread tid < kKeys: key tid of the tile)
-        auto key_offset = [&](int tl) -> long long {
-            const int j = tl * kKeys + tid;
-            if (tid >= kKeys || j >= x.keys) return -1;
-            if (j < x.cached) {
-                const int pos = x.pos0 + j;
-                const int p = prow[pos >> a.page_log];
-                if (p < 0 || p >= a.num_pages) return -1;
-                return (long long)p * a.page_stride +
-                       (((long long)hk << a.page_log) + (pos & ((1 << a.page_log) - 1))) * a.d;
-            }
-            return kTree | ((((long long)x.first * a.n + (j - x.cached)) * a.Hkv + hk) * a.d);
-        };
-        uint4 kx[kPasses][4], vx[kPasses][4];
-        auto fetch = [&](int tl) {
+        f32x16 O[DT];
 #pragma unroll
-            for (int p = 0; p < kPasses; ++p)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const long long o = sm.off[tl & 1][4 * (qd0 + p * kStep) + i];
-                    const bool ok = o >= 0 && dlive, tr = ok && (o & kTree);
-                    const size_t at = ok ? (size_t)(o & ~kTree) + 8 * d8 : 0;
-                    const uint4 zero = make_uint4(0, 0, 0, 0);
-                    const uint4 kv = *reinterpret_cast<const uint4 *>((tr ? kt : kc) + at);
-                    const uint4 vv = *reinterpret_cast<const uint4 *>((tr ? vtree : vc) + at);
-                    kx[p][i] = ok ? kv : zero;
-                    vx[p][i] = ok ? vv : zero;
-                }
-        };
-
-        f32x16 O[D / 32];
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) O[i] = f32x16{};
+        for (int i = 0; i < DT; ++i) O[i] = f32x16{};
         float mx = -__builtin_inff(), ls = 0.f;
 
-        // ---- pipeline: row offsets two tiles ahead, rows one tile ahead
-        if (tid < kKeys) sm.off[tile0 & 1][tid] = key_offset(tile0);
-        long long next_off = key_offset(tile0 + 1);
-        if (tid < kKeys) sm.off[(tile0 + 1) & 1][tid] = next_off;
-        __syncthreads();
-        fetch(tile0);
-        const int lim_unit = min(min(sm.lim[0], sm.lim[1]), min(sm.lim[2], sm.lim[3]));
-
-        for (int tl = tile0; tl < tile0 + count; ++tl) {
-            __syncthreads();                      // the last tile's readers are done
-#pragma unroll
-            for (int p = 0; p < kPasses; ++p) {
-                const int quad = qd0 + p * kStep;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    *reinterpret_cast<uint4 *>(&sm.k[k_at<D>(4 * quad + i, d8)]) = kx[p][i];
-                // place of the quad in contraction order: bits 0, 1 swap
-                const int place = (quad & ~3) | ((quad & 1) << 1) | ((quad >> 1) & 1);
-                const uint32_t *a0 = reinterpret_cast<const uint32_t *>(&vx[p][0]);
-                const uint32_t *a1 = reinterpret_cast<const uint32_t *>(&vx[p][1]);
-                const uint32_t *a2 = reinterpret_cast<const uint32_t *>(&vx[p][2]);
-                const uint32_t *a3 = reinterpret_cast<const uint32_t *>(&vx[p][3]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {     // columns 2 i, 2 i + 1 of the piece
-                    const uint2 even = make_uint2(__builtin_amdgcn_perm(a1[i], a0[i], 0x05040100u),
-                                                  __builtin_amdgcn_perm(a3[i], a2[i], 0x05040100u));
-                    const uint2 odd = make_uint2(__builtin_amdgcn_perm(a1[i], a0[i], 0x07060302u),
-                                                 __builtin_amdgcn_perm(a3[i], a2[i], 0x07060302u));
-                    *reinterpret_cast<uint2 *>(&sm.vt[v_at(8 * d8 + 2 * i, place)]) = even;
-                    *reinterpret_cast<uint2 *>(&sm.vt[v_at(8 * d8 + 2 * i + 1, place)]) = odd;
-                }
-            }
-            // a key that only some rows see may hold anything: weights of zero
-            // do not keep an infinity or a NaN out of the matrix product
-            if ((tl + 1) * kKeys > lim_unit) {
-                bool odd = false;
-#pragma unroll
-                for (int p = 0; p < kPasses; ++p)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t *x4 = reinterpret_cast<const uint32_t *>(&vx[p][i]);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint32_t lo = E::kExponent, hi = E::kExponent << 16;
+        auto one_tile = [&](Tile<D> &tile, Tile<D> &other, long long *offs,
+                            const long long *other_offs, int tl) {
+            // this tile has arrived, and everyone is done with the other one
+            __builtin_amdgcn_s_waitcnt(kVmcntZero);
+            lds_barrier();
+            // ---- a tile that not all rows see whole (the last ones): clear
+            // the values of keys that are not there, and look for infinities
+            // and NaN, which weights of zero do not keep out of the product
+            bool odd = false;
+            if (__builtin_expect((tl + 1) * kKeys > lim_unit, 0)) {
+                for (int i = tid; i < kKeys * P; i += kThreads) {
+                    uint4 *p = reinterpret_cast<uint4 *>(&tile.v[8 * i]);
+                    if (offs[i / P] < 0) {
+                        *p = make_uint4(0, 0, 0, 0);
+                    } else {
+                        const uint32_t x4[4] = {p->x, p->y, p->z, p->w};
+                        const uint32_t lo = E::kExponent, hi = E::kExponent << 16;
+                        for (int j = 0; j < 4; ++j)
                             odd |= (x4[j] & lo) == lo || (x4[j] & hi) == hi;
-                        }
                     }
-                if (odd) sm.odd[tl & 1] = 1;
-            }
-            const bool more = tl + 1 < tile0 + count;
-            if (more) {
-                fetch(tl + 1);
-                next_off = key_offset(tl + 2);
-            }
-            __syncthreads();
-            // readers of this parity's offsets fetched before the barrier above
-            if (more && tid < kKeys) sm.off[tl & 1][tid] = next_off;
-            const bool odd = __builtin_amdgcn_readfirstlane(sm.odd[tl & 1]) != 0;
-            if (tid == 0) sm.odd[(tl + 1) & 1] = 0;
-
-            const int keys = min(kKeys, x.keys - tl * kKeys);
-            for (int st = wk; 32 * st < keys; st += key_waves) {
-                f32x16 z = {};
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const vec ka = *reinterpret_cast<const vec *>(
-                        &sm.k[k_at<D>(32 * st + m, 2 * kk + h)]);
-                    z = E::mma(ka, qf[kk], z);
                 }
+                odd = __syncthreads_or(odd);
+            }
+            const bool more = t + 1 < t1;
+            int page = 0;
+            if (more) {
+                advance(a, sm.start, groups, entries, ahead);
+                if (w == 0 && ahead.e < entries) page = key_page(a, ahead, l);
+                fetch(other, other_offs);
+            }
+
+#pragma unroll 1
+            for (int st = 0; st < kKeys / 32; ++st) {
+                if ((row_waves < 4 && st != part) || tl * kKeys + 32 * st >= x.keys) continue;
+                f32x16 z = {};
+                // piece 2 kk + h of row m, turned: one exclusive or from the first
+                const int ka = (32 * st + keep_in_loop(m)) * D + 8 * k_piece<D>(m, h);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    z = E::mma(*reinterpret_cast<const vec *>(&tile.k[ka ^ (16 * kk)]), qf[kk], z);
                 const int j0 = tl * kKeys + 32 * st;
-                if (j0 + 32 > lim_min) {
+                if (__builtin_expect(j0 + 32 > lim_unit, 0)) {
 #pragma unroll
                     for (int r = 0; r < 16; ++r) {
                         const int j = j0 + crow(r, h), tj = j - x.cached;
-                        bool see = j < lim;
-                        if (is_own && tj >= 0 && tj < a.n)
-                            see = (sm.anc[node][tj >> 5] >> (tj & 31)) & 1u;
+                        const uint32_t up = sm.anc[node][min(max(tj, 0) >> 5, 3)] >> (tj & 31);
+                        const bool see = ((j < lim) & (tj < 0)) |
+                                         (is_own & (tj >= 0) & (tj < a.n) & ((up & 1u) != 0));
                         z[r] = see ? z[r] : -__builtin_inff();
                     }
                 }
@@ -525,11 +606,11 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
                 const float mn = fmaxf(mx, top);
                 // a row that has seen no key yet keeps -inf; its weights are zero
                 const float base = mn == -__builtin_inff() ? 0.f : mn;
-                if (__any(mn > mx)) {
+                if (__builtin_expect(__any(mn > mx), 0)) {
                     const float f = __builtin_amdgcn_exp2f(mx - base);
                     ls *= f;
 #pragma unroll
-                    for (int i = 0; i < D / 32; ++i) O[i] *= f;
+                    for (int i = 0; i < DT; ++i) O[i] *= f;
                     mx = mn;
                 }
                 float p[16];
@@ -538,96 +619,110 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
                     p[r] = __builtin_amdgcn_exp2f(fmaf(z[r], sc, -base));
                     ls += p[r];
                 }
-                if (odd) {
-                    // key by key, leaving out what has no weight (rare)
-                    for (int key = 0; key < 32; ++key) {
-                        float pk = 0.f;
-                        // register of the key in either half's lanes
-                        const int rk = 4 * (key >> 3) + (key & 3);
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) pk = r == rk ? p[r] : pk;
-                        pk = E::widen(E::bits(__shfl(pk, m + 32 * ((key >> 2) & 1))));
-                        const int quad = 8 * st + (key >> 2);
-                        const int place =
-                            (quad & ~3) | ((quad & 1) << 1) | ((quad >> 1) & 1);
-#pragma unroll
-                        for (int i = 0; i < D / 32; ++i)
-#pragma unroll
-                            for (int r = 0; r < 16; ++r) {
-                                const float x1 = E::widen(
-                                    sm.vt[v_at(32 * i + crow(r, h), place) + (key & 3)]);
-                                O[i][r] = pk != 0.f ? fmaf(pk, x1, O[i][r]) : O[i][r];
-                            }
-                    }
-                    continue;
-                }
+                // columns 32 i + (m & 16) + 4 (l & 3) of key 4 h + (l >> 2) & 3,
+                // turned: one exclusive or from i = 0
+                const int vkey = 4 * h + ((keep_in_loop(l) >> 2) & 3);
+                const int vcol = (m & 16) + 4 * (l & 3);
+                const int va = (32 * st + vkey) * D + 8 * v_piece<D>(vkey, vcol >> 3) + (vcol & 7);
                 // weights rounded to the operand type: half a step each
                 // (2^-9 or 2^-12 of a weight), independent over the keys
                 const vec p0 = E::round8(p), p1 = E::round8(p + 8);
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    const int d = 32 * i + m;
-                    const vec v0 = *reinterpret_cast<const vec *>(&sm.vt[v_at(d, 8 * st + 2 * h)]);
-                    const vec v1 =
-                        *reinterpret_cast<const vec *>(&sm.vt[v_at(d, 8 * st + 4 + 2 * h)]);
-                    O[i] = E::mma(v0, p0, O[i]);
-                    O[i] = E::mma(v1, p1, O[i]);
+                for (int i = 0; i < DT; ++i) {
+                    if (row_waves == 1 && i / (DT / 2) != half) continue;
+                    // this lane's column 32 i + m, keys 16 kk + 8 s + 4 h + (0..3)
+                    uint32_t vv[8];
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        const uint2 y = lds_transposed(&tile.v[(va ^ (32 * i)) + 8 * s * D]);
+                        vv[2 * s] = y.x, vv[2 * s + 1] = y.y;
+                    }
+                    auto times = [&](const uint32_t *y, f32x16 o) {
+                        o = E::mma(__builtin_bit_cast(vec, make_uint4(y[0], y[1], y[2], y[3])), p0,
+                                   o);
+                        return E::mma(__builtin_bit_cast(vec, make_uint4(y[4], y[5], y[6], y[7])),
+                                      p1, o);
+                    };
+                    if (__builtin_expect(odd, 0)) O[i] += odd_values<E>(vv, times);
+                    O[i] = times(vv, O[i]);
                 }
             }
+            // the offsets of this parity were last read before the barrier above
+            if (more && w == 0 && ahead.e < entries) offs[l] = key_offset(a, ahead, l, page);
+        };
+        for (int tl = tile0; tl < tile0 + count; ++tl, ++t) {
+            if ((t - t0) & 1) one_tile(tile_1, tile_0, off_1, off_0, tl);
+            else one_tile(tile_0, tile_1, off_0, off_1, tl);
         }
         ls += __shfl_xor(ls, 32);
 
-        // ---- join the key waves of a row through LDS, in wave order
-        if (key_waves > 1) {
-            float *buf = reinterpret_cast<float *>(&sm);       // [wave][D/32][16][64], then m, l
-            static_assert(sizeof(sm.k) + sizeof(sm.vt) >= 4u * (kWaves - 1) * (32 * D + 64), "");
-            __syncthreads();
-            if (wk > 0) {
-                float *o = buf + (size_t)(w - row_waves) * (32 * D + 64);
+        // ---- join the two halves of the keys through the last tile's LDS
+        bool writes = true;
+        auto join_keys = [&](Tile<D> &tile) {
+            float *buf = reinterpret_cast<float *>(&tile);
+            const int which = row_waves == 1 ? half : wr;
+            static_assert(sizeof(Tile<D>) >= 4u * 2 * 32 * D, "");
+            float *o = buf + (size_t)which * (32 * D);
+            writes = part == 0;
+            lds_barrier();
+            if (!writes) {
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i)
+                for (int i = 0; i < DT; ++i) {
+                    if (row_waves == 1 && i / (DT / 2) != half) continue;
 #pragma unroll
                     for (int r = 0; r < 16; ++r) o[(i * 16 + r) * 64 + l] = O[i][r];
+                }
                 if (h == 0) {
-                    o[32 * D + m] = mx;
-                    o[32 * D + 32 + m] = ls;
+                    sm.ml[which][0][m] = mx;
+                    sm.ml[which][1][m] = ls;
                 }
             }
-            __syncthreads();
-            if (wk == 0) {
-                for (int k2 = 1; k2 < key_waves; ++k2) {
-                    const float *o = buf + (size_t)(k2 * row_waves + wr - row_waves) * (32 * D + 64);
-                    const float mo = o[32 * D + m], lo = o[32 * D + 32 + m];
-                    const float mn = fmaxf(mx, mo), base = mn == -__builtin_inff() ? 0.f : mn;
-                    const float f = __builtin_amdgcn_exp2f(mx - base);
-                    const float g = __builtin_amdgcn_exp2f(mo - base);
-                    ls = ls * f + lo * g;
-                    mx = mn;
+            lds_barrier();
+            if (writes) {
+                const float mo = sm.ml[which][0][m], lo = sm.ml[which][1][m];
+                const float mn = fmaxf(mx, mo), base = mn == -__builtin_inff() ? 0.f : mn;
+                const float f = __builtin_amdgcn_exp2f(mx - base);
+                const float g = __builtin_amdgcn_exp2f(mo - base);
+                ls = ls * f + lo * g;
+                mx = mn;
 #pragma unroll
-                    for (int i = 0; i < D / 32; ++i)
+                for (int i = 0; i < DT; ++i) {
+                    if (row_waves == 1 && i / (DT / 2) != half) continue;
 #pragma unroll
-                        for (int r = 0; r < 16; ++r)
-                            O[i][r] = O[i][r] * f + o[(i * 16 + r) * 64 + l] * g;
+                    for (int r = 0; r < 16; ++r)
+                        O[i][r] = O[i][r] * f + o[(i * 16 + r) * 64 + l] * g;
                 }
             }
+            if (a.d != D) {
+                lds_barrier();
+                for (int i = tid; i < (int)sizeof(Tile<D>) / 16; i += kThreads)
+                    reinterpret_cast<uint4 *>(buf)[i] = make_uint4(0, 0, 0, 0);
+            }
+        };
+        if (row_waves < 4) {
+            if ((t - 1 - t0) & 1) join_keys(tile_1);
+            else join_keys(tile_0);
         }
         // ---- the partial: m, l and o of the unit's rows
-        if (wk == 0 && rlive) {
+        if (writes && rlive) {
             const int s = is_own ? slot : lay.slots.own + slot;
             const size_t at = (size_t)s * lay.slots.rows + qrow;
-            if (h == 0)
+            if (h == 0 && (row_waves > 1 || half == 0))
                 reinterpret_cast<float2 *>(ws + lay.off_ml)[at] = make_float2(mx, ls);
             float *o = reinterpret_cast<float *>(ws + lay.off_o) + at * D;
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i)
+            for (int i = 0; i < DT; ++i) {
+                if (row_waves == 1 && i / (DT / 2) != half) continue;
 #pragma unroll
                 for (int r4 = 0; r4 < 4; ++r4)
                     *reinterpret_cast<float4 *>(&o[32 * i + 8 * r4 + 4 * h]) =
                         make_float4(O[i][4 * r4], O[i][4 * r4 + 1], O[i][4 * r4 + 2],
                                     O[i][4 * r4 + 3]);
+            }
         }
-        t += count;
-        off += count;
+        // on to the next unit
+        cur.tile = x.tiles - 1;
+        advance(a, sm.start, groups, entries, cur);
     }
 }
 
