@@ -323,6 +323,8 @@ gdn_status gdn_tree_attention(const void *q, const void *k, const void *v, gdn_d
         (long long)batch * n * Hq > 0x3fffffffLL)
         return GDN_ERR_UNSUPPORTED;
     if (page_stride % 8 != 0 || page_stride < (int64_t)Hkv * page * d) return GDN_ERR_INVALID_ARG;
+    // rows inside a page, or inside a tree, are addressed with 32-bit byte offsets
+    if (page_stride > 0x7fffffffLL || (long long)Hkv * d > 0xffffffLL) return GDN_ERR_UNSUPPORTED;
     gdn::AttentionArgs a{q,      k,      v,           dtype,        parent, k_cache, v_cache,
                          page_stride, pages, length,  group_start,  group_shared, groups,
                          scale,  out,    batch,       n,            Hq,     Hkv,     d,

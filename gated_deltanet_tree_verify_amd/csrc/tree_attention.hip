@@ -29,6 +29,8 @@
 // rows, two waves and half the keys each; up to 32 rows (decoding), a wave has
 // half the keys and half the value columns, and the halves merge through LDS
 // at the unit's end.
+#include <type_traits>
+
 #include "device_common.hpp"
 #include "serving.hpp"
 #include "mfma_tile.hpp"
@@ -111,9 +113,22 @@ struct Layout {
     int64_t off_gpre, off_bpre, off_group, off_ml, off_o, bytes;
 };
 
-__device__ __forceinline__ int clamp_length(const AttentionArgs &a, int b) {
-    const int len = a.length[b];
+// The lengths and groups, as every workgroup keeps them in LDS: lengths that
+// do not fit count as 0, and without sound groups there are none.
+struct Batch {
+    int length[GDN_MAX_SEQUENCES];
+    int start[GDN_MAX_SEQUENCES + 1];
+    int shared[GDN_MAX_SEQUENCES];     // tokens computed once for a group
+};
+
+__device__ __forceinline__ int fit_length(const AttentionArgs &a, int len) {
     return len < 0 || len > (a.max_pages << a.page_log) ? 0 : len;
+}
+
+// tokens computed once for a group that says it shares `said`: none for a
+// group of one sequence (its own part covers them)
+__device__ __forceinline__ int fit_shared(const AttentionArgs &a, int members, int said) {
+    return members < 2 ? 0 : max(0, min(said, a.max_pages << a.page_log));
 }
 
 // group of sequence b, or -1.  start ascends within [0, batch] (checked).
@@ -128,30 +143,21 @@ __device__ __forceinline__ int group_of(const int *start, int groups, int b) {
     return lo;
 }
 
-// tokens computed once for the group: none for a group of one sequence (its
-// own part covers them)
-__device__ __forceinline__ int shared_tokens(const AttentionArgs &a, const int *start, int g) {
-    if (start[g + 1] - start[g] < 2) return 0;
-    const int sh = a.gshared[g];
-    return max(0, min(sh, a.max_pages << a.page_log));
-}
-
-__device__ __forceinline__ Entry entry(const AttentionArgs &a, const int *start, int groups,
-                                       int e) {
+__device__ __forceinline__ Entry entry(const AttentionArgs &a, const Batch &y, int groups, int e) {
     Entry x;
     const int heads = a.Hq / a.Hkv;
     if (e < groups) {
-        x.first = start[e];
-        x.rows = (start[e + 1] - start[e]) * a.n * heads;
+        x.first = y.start[e];
+        x.rows = (y.start[e + 1] - y.start[e]) * a.n * heads;
         x.pos0 = 0;
-        x.cached = shared_tokens(a, start, e);
+        x.cached = y.shared[e];
         x.keys = x.cached;
     } else {
-        const int b = e - groups, g = group_of(start, groups, b);
-        const int len = clamp_length(a, b);
+        const int b = e - groups, g = group_of(y.start, groups, b);
+        const int len = y.length[b];
         x.first = b;
         x.rows = a.n * heads;
-        x.pos0 = g < 0 ? 0 : min(len, shared_tokens(a, start, g));
+        x.pos0 = g < 0 ? 0 : min(len, y.shared[g]);
         x.cached = len - x.pos0;
         x.keys = x.cached + a.n;
     }
@@ -184,16 +190,12 @@ struct Smem {
     float ml[2][2][32];                  // m and l of the waves that are merged
     uint32_t anc[GDN_MAX_NODES][4];      // ancestor-or-self bits
     int up[GDN_MAX_NODES];
-    int start[GDN_MAX_SEQUENCES + 1];
+    Batch batch;
     long long part[kWaves];
     long long first_off;
-    int first_entry, max_own, max_shared, bad;
+    int first_entry, max_own, max_shared;
     int lim[kWaves];                     // fewest cached keys seen, over a wave's rows
 };
-
-// Offsets carry their source: cache rows as they are, tree rows with kTree
-// set, keys that are not there -1.
-constexpr long long kTree = 1LL << 62;
 
 // Place of 16-byte piece c (8 elements) in a row: turned by the key, so that
 // 32 keys read at one piece (keys) and 8 keys at four neighbouring pieces
@@ -222,37 +224,11 @@ __device__ __forceinline__ void load_to_lds(const void *from, uint16_t *base) {
                                      (__attribute__((address_space(3))) void *)base, 16, 0, 0);
 }
 
-// Values that are not finite, in a tile where some rows do not see some keys.
-// They are cleared in v; the result holds, for every row and column, what
-// those with a weight add up to: an infinity, NaN, or 0 where there are none.
-// With a = sum p [not finite] and s = sum p [+inf] - sum p [-inf], formed in
-// the same order, |s| = a exactly when only infinities of one sign were met.
-template <typename E, typename F>
-__device__ __forceinline__ f32x16 odd_values(uint32_t (&v)[8], F times) {
-    uint32_t any[8], sign[8];
-    const uint32_t one = E::bits(1.f);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        any[i] = sign[i] = 0;
-#pragma unroll
-        for (int hw = 0; hw < 32; hw += 16) {
-            const uint32_t x = (v[i] >> hw) & 0xffffu;
-            if ((x & E::kExponent) == E::kExponent) {
-                any[i] |= one << hw;
-                if ((x & 0x7fffu) == E::kExponent) sign[i] |= (one | (x & 0x8000u)) << hw;
-                v[i] &= 0xffff0000u >> hw;
-            }
-        }
-    }
-    const f32x16 a = times(any, f32x16{});
-    __builtin_amdgcn_sched_barrier(0);
-    const f32x16 s = times(sign, f32x16{});
-    f32x16 r;
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        r[i] = !(a[i] > 0.f) ? 0.f
-               : fabsf(s[i]) == a[i] ? copysignf(__builtin_inff(), s[i]) : __builtin_nanf("");
-    return r;
+// the larger of lane l's and lane l ^ 32's
+__device__ __forceinline__ float max_of_halves(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false,
+                                                    false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
 // x, but not a constant of the loop around: what is computed from it is
@@ -276,43 +252,77 @@ struct Cursor {
     Entry x;
 };
 
-__device__ __forceinline__ void seek(const AttentionArgs &a, const int *start, int groups,
+__device__ __forceinline__ void seek(const AttentionArgs &a, const Batch &y, int groups,
                                      int entries, Cursor &c, int e) {
     c.tile = c.rt = c.hk = 0;
     for (c.e = e; c.e < entries; ++c.e) {
-        const Entry x = entry(a, start, groups, c.e);
+        const Entry x = entry(a, y, groups, c.e);
         c.x = {uniform(x.first), uniform(x.rows),  uniform(x.pos0),     uniform(x.cached),
                uniform(x.keys),  uniform(x.tiles), uniform(x.row_tiles)};
         if (c.x.tiles > 0 && c.x.row_tiles > 0) return;
     }
 }
 
-__device__ __forceinline__ void advance(const AttentionArgs &a, const int *start, int groups,
+__device__ __forceinline__ void advance(const AttentionArgs &a, const Batch &y, int groups,
                                         int entries, Cursor &c) {
     if (c.e >= entries || ++c.tile < c.x.tiles) return;
     c.tile = 0;
     if (++c.rt < c.x.row_tiles) return;
     c.rt = 0;
     if (++c.hk < a.Hkv) return;
-    seek(a, start, groups, entries, c, c.e + 1);
+    seek(a, y, groups, entries, c, c.e + 1);
 }
 
-// Element offset of key `key` of the cursor's tile, in two steps: the page
-// id's load is issued first and used a tile later.
-__device__ __forceinline__ int key_page(const AttentionArgs &a, const Cursor &c, int key) {
-    const int pos = c.x.pos0 + c.tile * kKeys + key;
-    return a.pages[(size_t)c.x.first * a.max_pages + min(pos >> a.page_log, a.max_pages - 1)];
+// Where the rows of a tile's keys are, lane l of a wave for key l.  Four tiles
+// at once, one by each wave, every fourth tile; their page ids have been
+// loaded (to LDS) four tiles before.  The value row is as far from the key row
+// as the caches (or the tree's tensors) are from each other.
+constexpr int kAhead = 4;                // kWaves
+constexpr int kRing = 2 * kAhead;
+constexpr unsigned long long kAbsent = 1;    // the key is not there: any row will do (its
+                                             // score is masked, its value cleared)
+constexpr unsigned long long kTree = 2;      // a row of the tree
+struct Rows {
+    unsigned long long k[kKeys];         // the key row's address and its flags
+};
+
+// Address of the tree's keys, and how far the cache's lie from them: added or
+// not, where a choice between two kernel arguments would be compiled into a
+// load of the chosen one, waiting for all loads before it.
+struct Bases {
+    unsigned long long k, to_kc;
+};
+__device__ __forceinline__ unsigned long long address(const void *p) {
+    return reinterpret_cast<unsigned long long>(p);
 }
-__device__ __forceinline__ long long key_offset(const AttentionArgs &a, const Cursor &c, int key,
-                                                int page) {
-    const int j = c.tile * kKeys + key, pos = c.x.pos0 + j;
-    const long long cached =
-        (long long)page * a.page_stride +
-        (((long long)c.hk << a.page_log) + (pos & ((1 << a.page_log) - 1))) * a.d;
-    const long long tree =
-        kTree | ((((long long)c.x.first * a.n + (j - c.x.cached)) * a.Hkv + c.hk) * a.d);
-    if (j >= c.x.cached) return j < c.x.keys ? tree : -1;
-    return page >= 0 && page < a.num_pages ? cached : -1;
+
+__device__ __forceinline__ void load_pages(const AttentionArgs &a, const Cursor &c, int key,
+                                           int *to) {
+    const int pos = c.x.pos0 + c.tile * kKeys + key;
+    const int32_t *from = a.pages + (size_t)c.x.first * a.max_pages +
+                          min(pos >> a.page_log, a.max_pages - 1);
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
+                                     (__attribute__((address_space(3))) void *)to, 4, 0, 0);
+}
+
+__device__ __forceinline__ void put_rows(const AttentionArgs &a, const Bases &y, const Cursor &c,
+                                         int key, const int *pages, Rows &rows) {
+    const int j = c.tile * kKeys + key, pos = c.x.pos0 + j, tj = j - c.x.cached;
+    const int page = pages[key];
+    const bool there = tj < 0 ? page >= 0 && page < a.num_pages : j < c.x.keys;
+    // bytes from the cache's or the tree's first, the parts that all keys
+    // share in scalars (a page holds less than 2^31 elements)
+    const unsigned long long cached0 = (2ULL * c.hk * a.d) << a.page_log;
+    const unsigned long long tree0 = 2ULL * (((unsigned long long)c.x.first * a.n) * a.Hkv + c.hk) *
+                                     a.d;
+    const uint32_t in_page = 2u * (uint32_t)(pos & ((1 << a.page_log) - 1)) * a.d;
+    const uint32_t in_tree = 2u * (uint32_t)tj * (uint32_t)(a.Hkv * a.d);
+    const unsigned long long at =
+        tj < 0 ? (unsigned long long)(uint32_t)page * (uint32_t)(2 * a.page_stride) + cached0 +
+                     in_page
+               : tree0 + in_tree;
+    const unsigned long long cache = tj < 0 ? ~0ULL : 0ULL;
+    rows.k[key] = y.k + (y.to_kc & cache) + (there ? at : kAbsent) + (kTree & ~cache);
 }
 
 template <typename E, int D>
@@ -322,11 +332,12 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
     constexpr int P = D / 8;                       // 16-byte pieces of a row
     constexpr int kLoads = kKeys * P / kThreads;   // pieces a thread loads of K, and of V
     constexpr int DT = D / 32;                     // 32-column tiles of the values
-    // The two tiles and their offsets are objects of their own, and the code
-    // names which one it reads: the compiler then knows that the loads into
-    // the other one need no wait.
+    // The two tiles are objects of their own, and the code names which one it
+    // reads: the compiler then knows that the loads into the other one need
+    // no wait.
     __shared__ __attribute__((aligned(16))) Tile<D> tile_0, tile_1;
-    __shared__ long long off_0[kKeys], off_1[kKeys];   // element offsets of the keys' rows
+    __shared__ Rows ring[kRing];         // by tile, modulo kRing
+    __shared__ int page_ids[kAhead][kKeys];
     __shared__ Smem sm;
 
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
@@ -337,29 +348,34 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
     const int wg = grid % 8 == 0 ? (blockIdx.x % 8) * (grid / 8) + blockIdx.x / 8 : blockIdx.x;
     char *ws = static_cast<char *>(a.workspace);
 
-    // ---- groups: ascending within [0, batch], else none
+    // ---- lengths and groups; groups ascend within [0, batch], else none
     int groups = a.groups;
-    if (tid == 0) sm.bad = 0, sm.max_own = 0, sm.max_shared = 0;
-    for (int g = tid; g <= groups && groups > 0; g += kThreads) sm.start[g] = a.gstart[g];
+    Batch &bat = sm.batch;
+    if (tid == 0) sm.max_own = 0, sm.max_shared = 0;
+    for (int b = tid; b < a.batch; b += kThreads) bat.length[b] = fit_length(a, a.length[b]);
+    bool bad = false;
+    for (int g = tid; g < groups; g += kThreads) {
+        const int from = a.gstart[g], to = a.gstart[g + 1];
+        bat.start[g] = from;
+        if (g == groups - 1) bat.start[groups] = to;
+        bat.shared[g] = fit_shared(a, to - from, a.gshared[g]);
+        bad |= from < 0 || to < from || to > a.batch;
+    }
     // pieces past the head size are never loaded: zero for good
     if (a.d != D)
         for (int i = tid; i < (int)sizeof(Tile<D>) / 16; i += kThreads) {
             reinterpret_cast<uint4 *>(&tile_0)[i] = make_uint4(0, 0, 0, 0);
             reinterpret_cast<uint4 *>(&tile_1)[i] = make_uint4(0, 0, 0, 0);
         }
-    __syncthreads();
-    for (int g = tid; g < groups; g += kThreads)
-        if (sm.start[g] < 0 || sm.start[g + 1] < sm.start[g] || sm.start[g + 1] > a.batch)
-            sm.bad = 1;
-    __syncthreads();
-    if (uniform(sm.bad)) groups = 0;
+    bad = __syncthreads_or(bad);
+    if (bad) groups = 0;
     const int entries = groups + a.batch;
 
     // ---- length of the line and of its longest units
     long long sum = 0;
     int own = 0, shared = 0;
     for (int e = tid; e < entries; e += kThreads) {
-        const Entry x = entry(a, sm.start, groups, e);
+        const Entry x = entry(a, bat, groups, e);
         sum += line_tiles(a, x);
         if (e < groups) shared = max(shared, x.tiles);
         else own = max(own, x.tiles);
@@ -401,7 +417,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
         long long before = 0;
         for (int e0 = 0; e0 < entries; e0 += kThreads) {
             const int e = e0 + tid;
-            const long long x = e < entries ? line_tiles(a, entry(a, sm.start, groups, e)) : 0;
+            const long long x = e < entries ? line_tiles(a, entry(a, bat, groups, e)) : 0;
             const long long inc = wave_inclusive64(x);
             __syncthreads();
             if (l == 63) sm.part[w] = inc;
@@ -418,7 +434,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
                 else {
                     const int b = e - groups;
                     bpre[b] = pre;
-                    group[b] = sm.bad ? -2 : group_of(sm.start, groups, b);
+                    group[b] = bad ? -2 : group_of(bat.start, groups, b);
                 }
             }
         }
@@ -431,44 +447,70 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
     const bool flip = sc < 0.f;        // z = scale q.k: the sign goes into q, exactly
     const uint32_t keep = sc == 0.f ? 0u : ~0u;   // and a scale of zero: masked scores stay -inf
     sc = sc == 0.f ? 1.f : fabsf(sc);
-    const char *kc = static_cast<const char *>(a.kc), *vc = static_cast<const char *>(a.vc);
-    const char *kt = static_cast<const char *>(a.k), *vt = static_cast<const char *>(a.v);
 
-    // the tile that is computed, and the one whose row offsets are looked up
+    // the tile that is computed, and the one whose rows this wave looks up
     Cursor cur, ahead;
     {
-        seek(a, sm.start, groups, entries, cur, uniform(sm.first_entry));
+        seek(a, bat, groups, entries, cur, uniform(sm.first_entry));
         const long long off = uniform(sm.first_off), unit = off / cur.x.tiles;
         cur.tile = (int)(off - unit * cur.x.tiles);
         cur.hk = (int)(unit / cur.x.row_tiles);
         cur.rt = (int)(unit % cur.x.row_tiles);
         ahead = cur;
     }
-    auto fetch = [&](Tile<D> &to, const long long *offs) {
-        const int lane = keep_in_loop(l);
+    const Bases bases{address(a.k), address(a.kc) - address(a.k)};
+    // from a cached key's row to its value's, and how much further in the tree
+    const unsigned long long to_v = address(a.vc) - address(a.kc);
+    const unsigned long long tree_v = address(a.v) - address(a.k) - to_v;
+    auto fetch = [&](Tile<D> &to, const Rows &rows) {
+        const unsigned lane = keep_in_loop(l);
+        unsigned long long kr[kLoads], vr[kLoads];
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            const int s0 = (w * kLoads + i) * 64;          // the wave's first piece
-            const int key = (s0 + lane) / P, c1 = lane % P;
-            const long long o = offs[key];
-            const size_t at = o >= 0 ? (size_t)(o & ~kTree) * 2 : 0;
-            const bool tr = o >= 0 && (o & kTree);
-            const int ck = k_piece<D>(key, c1), cv = v_piece<D>(key, c1);
-            // a key that is not there: any row (its scores are masked, its
-            // values are cleared before use)
-            if (8 * ck < a.d) load_to_lds((tr ? kt : kc) + at + 16 * ck, &to.k[8 * s0]);
-            if (8 * cv < a.d) load_to_lds((tr ? vt : vc) + at + 16 * cv, &to.v[8 * s0]);
+            const unsigned key = ((w * kLoads + i) * 64 + lane) / P;
+            kr[i] = rows.k[key];
         }
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const unsigned long long tree = kr[i] & kTree ? ~0ULL : 0ULL;
+            kr[i] &= ~(kAbsent | kTree);
+            vr[i] = kr[i] + to_v + (tree_v & tree);
+        }
+        auto go = [&](auto whole) {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int s0 = (w * kLoads + i) * 64;          // the wave's first piece
+                const unsigned key = (s0 + lane) / P, c1 = lane % P;
+                const int ck = k_piece<D>(key, c1), cv = v_piece<D>(key, c1);
+                if (whole || 8 * ck < a.d)
+                    load_to_lds(reinterpret_cast<const void *>(kr[i] + 16 * ck), &to.k[8 * s0]);
+                if (whole || 8 * cv < a.d)
+                    load_to_lds(reinterpret_cast<const void *>(vr[i] + 16 * cv), &to.v[8 * s0]);
+            }
+        };
+        if (a.d == D) go(std::true_type{});
+        else go(std::false_type{});
     };
 
-    // ---- pipeline: row offsets two tiles ahead, rows one tile ahead
-    if (w == 0) {
-        off_0[l] = key_offset(a, ahead, l, key_page(a, ahead, l));
-    }
-    advance(a, sm.start, groups, entries, ahead);
-    if (w == 0 && ahead.e < entries) off_1[l] = key_offset(a, ahead, l, key_page(a, ahead, l));
+    // ---- pipeline: page ids eight tiles ahead, the rows' places four, their
+    // bytes one.  `ahead` is the wave's own tile of the four.
+    auto skip = [&](int tiles) {
+#pragma unroll 1
+        for (int i = 0; i < tiles; ++i) advance(a, bat, groups, entries, ahead);
+    };
+    auto look_ahead = [&](int first) {   // tiles first .. first + 3 from t0 on
+        const int lane = keep_in_loop(l);
+        if (ahead.e < entries)
+            put_rows(a, bases, ahead, lane, page_ids[w], ring[(first + w) & (kRing - 1)]);
+        skip(kAhead);
+        if (ahead.e < entries) load_pages(a, ahead, lane, page_ids[w]);
+    };
+    skip(w);
+    if (ahead.e < entries) load_pages(a, ahead, l, page_ids[w]);
+    __builtin_amdgcn_s_waitcnt(kVmcntZero);
+    look_ahead(0);
     lds_barrier();
-    fetch(tile_0, off_0);
+    fetch(tile_0, ring[0]);
 
     int anc_of = -1;
     long long t = t0;
@@ -480,9 +522,11 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
         const bool is_own = cur.e >= groups;
         const int nrows = min(kRows, x.rows - r0);
         const int row_waves = nrows <= 32 ? 1 : nrows <= 64 ? 2 : 4;
+        const int l = keep_in_loop(tid) & 63, m = l & 31, h = l >> 5;
         const int wr = w & (row_waves - 1);
         const int part = row_waves == 1 ? w & 1 : w >> 1;  // its keys (fewer than 4 row waves)
-        const int half = w >> 1;                           // its columns (1 row wave)
+        // one row wave: half of the columns, in the first half of O
+        const int col0 = row_waves == 1 ? (w >> 1) * (D / 2) : 0;
 
         // ---- the tree's ancestor bits, once per sequence: after step i
         // every node knows its 2^i nearest ancestors and jumps that far
@@ -519,7 +563,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
         const size_t qrow =
             ((size_t)x.first * a.n + rr / heads) * a.Hq + (size_t)hk * heads + rr % heads;
         const int node = is_own ? rr / heads : 0;
-        const int len_b = clamp_length(a, x.first + rr / heads / a.n);
+        const int len_b = bat.length[x.first + rr / heads / a.n];
         const int lim = is_own ? x.cached : min(x.cached, len_b);   // cached keys it sees
         vec qf[D / 16];
 #pragma unroll
@@ -547,47 +591,75 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
 #pragma unroll
         for (int i = 0; i < DT; ++i) O[i] = f32x16{};
         float mx = -__builtin_inff(), ls = 0.f;
+        bool odd = false;                  // values were cleared that are not finite
 
-        auto one_tile = [&](Tile<D> &tile, Tile<D> &other, long long *offs,
-                            const long long *other_offs, int tl) {
+        auto one_tile = [&](Tile<D> &tile, Tile<D> &other, int tl) {
+            const int ti = (int)(t - t0);
             // this tile has arrived, and everyone is done with the other one
             __builtin_amdgcn_s_waitcnt(kVmcntZero);
             lds_barrier();
             // ---- a tile that not all rows see whole (the last ones): clear
-            // the values of keys that are not there, and look for infinities
-            // and NaN, which weights of zero do not keep out of the product
-            bool odd = false;
+            // the values of keys that are not there, and infinities and NaN,
+            // which a weight of zero would not keep out of the product; the
+            // second kernel gives them back to the rows that see them
             if (__builtin_expect((tl + 1) * kKeys > lim_unit, 0)) {
-                for (int i = tid; i < kKeys * P; i += kThreads) {
+                bool found = false;
+                for (int i = keep_in_loop(tid); i < kKeys * P; i += kThreads) {
                     uint4 *p = reinterpret_cast<uint4 *>(&tile.v[8 * i]);
-                    if (offs[i / P] < 0) {
-                        *p = make_uint4(0, 0, 0, 0);
-                    } else {
-                        const uint32_t x4[4] = {p->x, p->y, p->z, p->w};
+                    uint32_t x4[4] = {p->x, p->y, p->z, p->w};
+                    const bool there = !(ring[ti & (kRing - 1)].k[i / P] & kAbsent);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
                         const uint32_t lo = E::kExponent, hi = E::kExponent << 16;
-                        for (int j = 0; j < 4; ++j)
-                            odd |= (x4[j] & lo) == lo || (x4[j] & hi) == hi;
+                        const uint32_t keep_lo = (x4[j] & lo) == lo ? 0u : 0xffffu;
+                        const uint32_t keep_hi = (x4[j] & hi) == hi ? 0u : 0xffff0000u;
+                        found |= there & ((keep_lo == 0) | (keep_hi == 0));
+                        x4[j] = there ? x4[j] & (keep_lo | keep_hi) : 0u;
                     }
+                    *p = make_uint4(x4[0], x4[1], x4[2], x4[3]);
                 }
-                odd = __syncthreads_or(odd);
+                if (__syncthreads_or(found)) odd = true;
             }
-            const bool more = t + 1 < t1;
-            int page = 0;
-            if (more) {
-                advance(a, sm.start, groups, entries, ahead);
-                if (w == 0 && ahead.e < entries) page = key_page(a, ahead, l);
-                fetch(other, other_offs);
-            }
+            if (ti % kAhead == 0) look_ahead(ti + kAhead);
+            if (t + 1 < t1) fetch(other, ring[(ti + 1) & (kRing - 1)]);
 
 #pragma unroll 1
             for (int st = 0; st < kKeys / 32; ++st) {
                 if ((row_waves < 4 && st != part) || tl * kKeys + 32 * st >= x.keys) continue;
-                f32x16 z = {};
-                // piece 2 kk + h of row m, turned: one exclusive or from the first
+                // All reads of a product are issued before its first step: the
+                // keys' before the scores, the values' before the softmax.
+                // Key row m, piece 2 kk + h, turned: one exclusive or from kk = 0.
                 const int ka = (32 * st + keep_in_loop(m)) * D + 8 * k_piece<D>(m, h);
+                vec kf[D / 16];
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                    z = E::mma(*reinterpret_cast<const vec *>(&tile.k[ka ^ (16 * kk)]), qf[kk], z);
+                    kf[kk] = *reinterpret_cast<const vec *>(&tile.k[ka ^ (16 * kk)]);
+                __builtin_amdgcn_sched_barrier(0);
+                f32x16 z = {};
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) z = E::mma(kf[kk], qf[kk], z);
+                // values: columns 32 i + (m & 16) + 4 (l & 3) of key 4 h + (l >> 2) & 3,
+                // turned: one exclusive or from i = 0
+                const int vkey = 4 * h + ((keep_in_loop(l) >> 2) & 3);
+                const int vcol = (m & 16) + 4 * (l & 3);
+                const int va = ((32 * st + vkey) * D + 8 * v_piece<D>(vkey, vcol >> 3) +
+                                (vcol & 7)) ^ col0;
+                // this lane's column of tile i, keys 8 s + 4 h + (0..3)
+                uint32_t vv[DT][8];
+                auto read_values = [&](int i, uint32_t *y) {
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        const uint2 x2 = lds_transposed(&tile.v[(va ^ (32 * i)) + 8 * s * D]);
+                        y[2 * s] = x2.x, y[2 * s + 1] = x2.y;
+                    }
+                };
+#pragma unroll
+                for (int i = 0; i < DT / 2; ++i) read_values(i, vv[i]);
+                if (row_waves > 1) {
+#pragma unroll
+                    for (int i = DT / 2; i < DT; ++i) read_values(i, vv[i]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
                 const int j0 = tl * kKeys + 32 * st;
                 if (__builtin_expect(j0 + 32 > lim_unit, 0)) {
 #pragma unroll
@@ -602,7 +674,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
                 float top = z[0];
 #pragma unroll
                 for (int r = 1; r < 16; ++r) top = fmaxf(top, z[r]);
-                top = fmaxf(top, __shfl_xor(top, 32)) * sc;
+                top = max_of_halves(top) * sc;
                 const float mn = fmaxf(mx, top);
                 // a row that has seen no key yet keeps -inf; its weights are zero
                 const float base = mn == -__builtin_inff() ? 0.f : mn;
@@ -619,48 +691,34 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
                     p[r] = __builtin_amdgcn_exp2f(fmaf(z[r], sc, -base));
                     ls += p[r];
                 }
-                // columns 32 i + (m & 16) + 4 (l & 3) of key 4 h + (l >> 2) & 3,
-                // turned: one exclusive or from i = 0
-                const int vkey = 4 * h + ((keep_in_loop(l) >> 2) & 3);
-                const int vcol = (m & 16) + 4 * (l & 3);
-                const int va = (32 * st + vkey) * D + 8 * v_piece<D>(vkey, vcol >> 3) + (vcol & 7);
                 // weights rounded to the operand type: half a step each
                 // (2^-9 or 2^-12 of a weight), independent over the keys
                 const vec p0 = E::round8(p), p1 = E::round8(p + 8);
+                auto times = [&](const uint32_t *y, f32x16 o) {
+                    o = E::mma(__builtin_bit_cast(vec, make_uint4(y[0], y[1], y[2], y[3])), p0, o);
+                    return E::mma(__builtin_bit_cast(vec, make_uint4(y[4], y[5], y[6], y[7])), p1,
+                                  o);
+                };
 #pragma unroll
-                for (int i = 0; i < DT; ++i) {
-                    if (row_waves == 1 && i / (DT / 2) != half) continue;
-                    // this lane's column 32 i + m, keys 16 kk + 8 s + 4 h + (0..3)
-                    uint32_t vv[8];
+                for (int i = 0; i < DT / 2; ++i) O[i] = times(vv[i], O[i]);
+                if (row_waves > 1) {
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) {
-                        const uint2 y = lds_transposed(&tile.v[(va ^ (32 * i)) + 8 * s * D]);
-                        vv[2 * s] = y.x, vv[2 * s + 1] = y.y;
-                    }
-                    auto times = [&](const uint32_t *y, f32x16 o) {
-                        o = E::mma(__builtin_bit_cast(vec, make_uint4(y[0], y[1], y[2], y[3])), p0,
-                                   o);
-                        return E::mma(__builtin_bit_cast(vec, make_uint4(y[4], y[5], y[6], y[7])),
-                                      p1, o);
-                    };
-                    if (__builtin_expect(odd, 0)) O[i] += odd_values<E>(vv, times);
-                    O[i] = times(vv, O[i]);
+                    for (int i = DT / 2; i < DT; ++i) O[i] = times(vv[i], O[i]);
                 }
             }
-            // the offsets of this parity were last read before the barrier above
-            if (more && w == 0 && ahead.e < entries) offs[l] = key_offset(a, ahead, l, page);
         };
         for (int tl = tile0; tl < tile0 + count; ++tl, ++t) {
-            if ((t - t0) & 1) one_tile(tile_1, tile_0, off_1, off_0, tl);
-            else one_tile(tile_0, tile_1, off_0, off_1, tl);
+            if ((t - t0) & 1) one_tile(tile_1, tile_0, tl);
+            else one_tile(tile_0, tile_1, tl);
         }
         ls += __shfl_xor(ls, 32);
 
         // ---- join the two halves of the keys through the last tile's LDS
         bool writes = true;
         auto join_keys = [&](Tile<D> &tile) {
+            const int l = keep_in_loop(tid) & 63, m = l & 31, h = l >> 5;
             float *buf = reinterpret_cast<float *>(&tile);
-            const int which = row_waves == 1 ? half : wr;
+            const int which = row_waves == 1 ? w >> 1 : wr;
             static_assert(sizeof(Tile<D>) >= 4u * 2 * 32 * D, "");
             float *o = buf + (size_t)which * (32 * D);
             writes = part == 0;
@@ -668,7 +726,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
             if (!writes) {
 #pragma unroll
                 for (int i = 0; i < DT; ++i) {
-                    if (row_waves == 1 && i / (DT / 2) != half) continue;
+                    if (row_waves == 1 && i >= DT / 2) break;
 #pragma unroll
                     for (int r = 0; r < 16; ++r) o[(i * 16 + r) * 64 + l] = O[i][r];
                 }
@@ -687,7 +745,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
                 mx = mn;
 #pragma unroll
                 for (int i = 0; i < DT; ++i) {
-                    if (row_waves == 1 && i / (DT / 2) != half) continue;
+                    if (row_waves == 1 && i >= DT / 2) break;
 #pragma unroll
                     for (int r = 0; r < 16; ++r)
                         O[i][r] = O[i][r] * f + o[(i * 16 + r) * 64 + l] * g;
@@ -703,26 +761,27 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
             if ((t - 1 - t0) & 1) join_keys(tile_1);
             else join_keys(tile_0);
         }
-        // ---- the partial: m, l and o of the unit's rows
+        // ---- the partial: m, l (negative where values were cleared) and o of
+        // the unit's rows
         if (writes && rlive) {
             const int s = is_own ? slot : lay.slots.own + slot;
             const size_t at = (size_t)s * lay.slots.rows + qrow;
-            if (h == 0 && (row_waves > 1 || half == 0))
-                reinterpret_cast<float2 *>(ws + lay.off_ml)[at] = make_float2(mx, ls);
+            if (h == 0 && col0 == 0)
+                reinterpret_cast<float2 *>(ws + lay.off_ml)[at] = make_float2(mx, odd ? -ls : ls);
             float *o = reinterpret_cast<float *>(ws + lay.off_o) + at * D;
 #pragma unroll
             for (int i = 0; i < DT; ++i) {
-                if (row_waves == 1 && i / (DT / 2) != half) continue;
+                if (row_waves == 1 && i >= DT / 2) break;
 #pragma unroll
                 for (int r4 = 0; r4 < 4; ++r4)
-                    *reinterpret_cast<float4 *>(&o[32 * i + 8 * r4 + 4 * h]) =
+                    *reinterpret_cast<float4 *>(&o[col0 + 32 * i + 8 * r4 + 4 * h]) =
                         make_float4(O[i][4 * r4], O[i][4 * r4 + 1], O[i][4 * r4 + 2],
                                     O[i][4 * r4 + 3]);
             }
         }
         // on to the next unit
         cur.tile = x.tiles - 1;
-        advance(a, sm.start, groups, entries, cur);
+        advance(a, bat, groups, entries, cur);
     }
 }
 
@@ -778,7 +837,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttentionArgs a, Layout 
         const long long c = plan->tiles_per_wg;
         const long long *gpre = reinterpret_cast<const long long *>(ws + lay.off_gpre);
         const long long *bpre = reinterpret_cast<const long long *>(ws + lay.off_bpre);
-        const int sh = members < 2 ? 0 : min(max(0, a.gshared[g]), a.max_pages << a.page_log);
+        const int sh = g < 0 ? 0 : fit_shared(a, members, a.gshared[g]);
         // the unit's first tile on the line and its tiles: its partials are
         // one per workgroup between
         const int row_tiles = (a.n * heads + kRows - 1) / kRows;
@@ -796,19 +855,61 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttentionArgs a, Layout 
         }
         const float2 *ml = reinterpret_cast<const float2 *>(ws + lay.off_ml) + qrow;
         const float *o = reinterpret_cast<const float *>(ws + lay.off_o) + qrow * D + d0;
+        // eight partials at a time: their loads do not wait for each other
+        constexpr int kAtOnce = 8;
         float mx = -__builtin_inff(), ls = 0.f;
-        for (int i = 0; i < no + ns; ++i) {
-            const size_t s = (size_t)(i < no ? i : lay.slots.own + i - no) * lay.slots.rows;
-            const float2 p = ml[s];
-            const float4 v = *reinterpret_cast<const float4 *>(&o[s * D]);
-            const float mn = fmaxf(mx, p.x), base = mn == -__builtin_inff() ? 0.f : mn;
-            const float f = __builtin_amdgcn_exp2f(mx - base), e = __builtin_amdgcn_exp2f(p.x - base);
-            ls = ls * f + p.y * e;
-            acc.x = acc.x * f + v.x * e, acc.y = acc.y * f + v.y * e;
-            acc.z = acc.z * f + v.z * e, acc.w = acc.w * f + v.w * e;
-            mx = mn;
+        bool odd = false;
+        const int count = no + ns;
+        for (int i0 = 0; i0 < count; i0 += kAtOnce) {
+            float2 p[kAtOnce];
+            float4 v[kAtOnce];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                const int x = min(i0 + i, count - 1);
+                const size_t s = (size_t)(x < no ? x : lay.slots.own + x - no) * lay.slots.rows;
+                p[i] = ml[s];
+                v[i] = *reinterpret_cast<const float4 *>(&o[s * D]);
+            }
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                if (i0 + i >= count) break;
+                const float mn = fmaxf(mx, p[i].x), base = mn == -__builtin_inff() ? 0.f : mn;
+                const float f = __builtin_amdgcn_exp2f(mx - base);
+                const float e = __builtin_amdgcn_exp2f(p[i].x - base);
+                odd |= p[i].y < 0.f;
+                ls = ls * f + fabsf(p[i].y) * e;
+                acc.x = acc.x * f + v[i].x * e, acc.y = acc.y * f + v[i].y * e;
+                acc.z = acc.z * f + v[i].z * e, acc.w = acc.w * f + v[i].w * e;
+                mx = mn;
+            }
         }
         inv = 1.f / ls;
+        if (odd) {
+            // The sequence's tiles that not all rows saw whole were computed
+            // without infinities and NaN.  What this row sees of them decides
+            // its columns: one sign of infinity, or NaN.
+            const int pos0 = min(len, sh), from_own = pos0 + (len - pos0) / kKeys * kKeys;
+            int shortest = sh;
+            for (int i = 0; i < members && sh > 0; ++i)
+                shortest = min(shortest, max(0, a.length[gs + i]));
+            const int from = shortest < sh ? shortest / kKeys * kKeys : from_own;
+            float x[4] = {};
+            auto see = [&](const void *base, size_t at) {
+                const uint16_t *v = static_cast<const uint16_t *>(base) + at + d0;
+                for (int e = 0; e < 4; ++e) {
+                    const float y = E::widen(v[e]);
+                    if (!(fabsf(y) < __builtin_inff())) x[e] += y;
+                }
+            };
+            for (int pos = from; pos < len; ++pos)
+                if (pos < pos0 || pos >= from_own)
+                    see(a.vc, (size_t)row[pos >> a.page_log] * a.page_stride +
+                                  (((size_t)hk << a.page_log) +
+                                   (pos & ((1 << a.page_log) - 1))) * a.d);
+            for (int i = node; i >= 0; i = a.parent[(size_t)b * a.n + i])
+                see(a.v, (((size_t)b * a.n + i) * a.Hkv + hk) * a.d);
+            acc.x += x[0], acc.y += x[1], acc.z += x[2], acc.w += x[3];
+        }
     }
     const uint32_t lo = E::bits(acc.x * inv) | (uint32_t)E::bits(acc.y * inv) << 16;
     const uint32_t hi = E::bits(acc.z * inv) | (uint32_t)E::bits(acc.w * inv) << 16;

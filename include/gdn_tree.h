@@ -58,7 +58,7 @@ extern "C" {
 #define GDN_MAX_DIM 128
 #define GDN_MAX_CANDIDATES 32   /* child candidates per node, gdn_tree_build */
 #define GDN_MAX_HEAD_DIM 256    /* head size of gdn_tree_attention */
-#define GDN_MAX_SEQUENCES 1024  /* batch and groups of gdn_tree_attention */
+#define GDN_MAX_SEQUENCES 512   /* batch and groups of gdn_tree_attention */
 #define GDN_MAX_REQUESTS 4096   /* requests of one page_fork / page_extend call */
 
 typedef enum {

@@ -90,7 +90,7 @@ def test_attention_pointers(lib, i):
     (dict(batch=0), -1), (dict(n=0), -1), (dict(n=129), -2), (dict(Hq=3), -2), (dict(d=60), -2),
     (dict(d=264), -2), (dict(page=0), -1), (dict(page=24), -2), (dict(num=0), -1),
     (dict(width=0), -1), (dict(stride=8), -1), (dict(stride=2 * 16 * 64 + 4), -1),
-    (dict(batch=1025), -2), (dict(groups=1025, start=FAKE, shared=FAKE), -2),
+    (dict(batch=513), -2), (dict(groups=513, start=FAKE, shared=FAKE), -2),
     (dict(width=1 << 27), -2), (dict(ws=None), -1), (dict(ws_bytes=16), -1), (dict(ws=ODD), -1),
     (dict(status=ODD), -1),
 ])
