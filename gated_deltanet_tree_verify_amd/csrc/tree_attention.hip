@@ -12,9 +12,9 @@
 //
 // Work: a unit is (group, key head, 128 rows) over the shared tokens or
 // (sequence, key head, 128 rows) over its own tokens and tree nodes, cut into
-// tiles of 128 keys.  All units' tiles form one line, and workgroup i takes
-// the tiles [i c, (i + 1) c) of it, whatever units they belong to: every
-// workgroup has the same number of tiles for any mix of lengths.  Lengths are
+// tiles of 64 keys.  All units' tiles form one line, and workgroup i takes
+// the places [i c, (i + 1) c) of it, whatever units they belong to: every
+// workgroup has the same work for any mix of lengths.  Lengths are
 // device data, so every workgroup forms the line's prefix sums by itself (a
 // scan over the batch).  Each unit a workgroup meets leaves one partial
 // (m, l, o) in the workspace; a second kernel joins a row's partials.
@@ -94,12 +94,12 @@ struct Entry {
     int keys;        // all keys: cached tokens, then the tree's nodes (own entries)
     int tiles;       // ceil(keys / kKeys)
     int row_tiles;   // ceil(rows / kRows)
+    int weight;      // places of the line that a tile takes
 };
 
 // what the first kernel leaves for the second
 struct Plan {
-    long long tiles_per_wg;
-    long long total;
+    long long per_wg;      // places of the line per workgroup
 };
 
 struct Slots {
@@ -143,6 +143,15 @@ __device__ __forceinline__ int group_of(const int *start, int groups, int b) {
     return lo;
 }
 
+// what follows from an entry's rows and keys
+__device__ __forceinline__ void shape(Entry &x) {
+    x.tiles = (x.keys + kKeys - 1) / kKeys;
+    x.row_tiles = (x.rows + kRows - 1) / kRows;
+    // a wave with all of a tile's keys takes about twice as long as one that
+    // shares them (3.4 and 1.8 us a tile, two workgroups on a compute unit)
+    x.weight = x.rows > 64 ? 2 : 1;
+}
+
 __device__ __forceinline__ Entry entry(const AttentionArgs &a, const Batch &y, int groups, int e) {
     Entry x;
     const int heads = a.Hq / a.Hkv;
@@ -161,13 +170,21 @@ __device__ __forceinline__ Entry entry(const AttentionArgs &a, const Batch &y, i
         x.cached = len - x.pos0;
         x.keys = x.cached + a.n;
     }
-    x.tiles = (x.keys + kKeys - 1) / kKeys;
-    x.row_tiles = (x.rows + kRows - 1) / kRows;
+    shape(x);
     return x;
 }
 
-__device__ __forceinline__ long long line_tiles(const AttentionArgs &a, const Entry &x) {
-    return (long long)x.tiles * x.row_tiles * a.Hkv;
+// Length of an entry on the line.  A unit begins with the places of kUnit
+// tiles, for what it costs apart from its tiles (queries, partial, a masked
+// tile).  Without them the workgroups that meet many short units end last
+// (16 users' draft trees: 191 us; with 3: 155 us).
+constexpr int kUnit = 3;
+
+__device__ __forceinline__ long long unit_length(const Entry &x) {
+    return x.tiles > 0 ? (long long)x.weight * (kUnit + x.tiles) : 0;
+}
+__device__ __forceinline__ long long line_length(const AttentionArgs &a, const Entry &x) {
+    return unit_length(x) * x.row_tiles * a.Hkv;
 }
 
 __device__ __forceinline__ long long wave_inclusive64(long long x) {
@@ -193,7 +210,7 @@ struct Smem {
     Batch batch;
     long long part[kWaves];
     long long first_off;
-    int first_entry, max_own, max_shared;
+    int first_entry, max_own, max_shared, heavy;
     int lim[kWaves];                     // fewest cached keys seen, over a wave's rows
 };
 
@@ -258,7 +275,7 @@ __device__ __forceinline__ void seek(const AttentionArgs &a, const Batch &y, int
     for (c.e = e; c.e < entries; ++c.e) {
         const Entry x = entry(a, y, groups, c.e);
         c.x = {uniform(x.first), uniform(x.rows),  uniform(x.pos0),     uniform(x.cached),
-               uniform(x.keys),  uniform(x.tiles), uniform(x.row_tiles)};
+               uniform(x.keys),  uniform(x.tiles), uniform(x.row_tiles), uniform(x.weight)};
         if (c.x.tiles > 0 && c.x.row_tiles > 0) return;
     }
 }
@@ -351,7 +368,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
     // ---- lengths and groups; groups ascend within [0, batch], else none
     int groups = a.groups;
     Batch &bat = sm.batch;
-    if (tid == 0) sm.max_own = 0, sm.max_shared = 0;
+    if (tid == 0) sm.max_own = 0, sm.max_shared = 0, sm.heavy = 1;
     for (int b = tid; b < a.batch; b += kThreads) bat.length[b] = fit_length(a, a.length[b]);
     bool bad = false;
     for (int g = tid; g < groups; g += kThreads) {
@@ -373,33 +390,38 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
 
     // ---- length of the line and of its longest units
     long long sum = 0;
-    int own = 0, shared = 0;
+    int own = 0, shared = 0, heavy = 1;
     for (int e = tid; e < entries; e += kThreads) {
         const Entry x = entry(a, bat, groups, e);
-        sum += line_tiles(a, x);
-        if (e < groups) shared = max(shared, x.tiles);
-        else own = max(own, x.tiles);
+        sum += line_length(a, x);
+        const int span = x.weight * (x.tiles - 1);      // from the first tile to the last
+        if (e < groups) shared = max(shared, span);
+        else own = max(own, span);
+        heavy = max(heavy, x.weight);
     }
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
         sum += __shfl_xor(sum, o);
         own = max(own, __shfl_xor(own, o));
         shared = max(shared, __shfl_xor(shared, o));
+        heavy = max(heavy, __shfl_xor(heavy, o));
     }
     if (l == 0) {
         sm.part[w] = sum;
         atomicMax(&sm.max_own, own);
         atomicMax(&sm.max_shared, shared);
+        atomicMax(&sm.heavy, heavy);
     }
     __syncthreads();
     const long long total =
         uniform((sm.part[0] + sm.part[1]) + (sm.part[2] + sm.part[3]));
-    // a unit of T tiles meets at most (T - 2) / c + 2 workgroups: c keeps
-    // that within the partials there is room for
+    // a unit whose tiles span s places meets at most (s - 1) / c + 2
+    // workgroups: c keeps that within the partials there is room for.  With c
+    // no less than a tile's places, none of these workgroups goes without.
     long long c = (total + grid - 1) / grid;
-    c = max(c, (long long)(uniform(sm.max_own) + lay.slots.own - 3) / (lay.slots.own - 1));
-    c = max(c, (long long)(uniform(sm.max_shared) + lay.slots.shared - 3) / (lay.slots.shared - 1));
-    c = max(c, 1LL);
+    c = max(c, (long long)(uniform(sm.max_own) + lay.slots.own - 2) / (lay.slots.own - 1));
+    c = max(c, (long long)(uniform(sm.max_shared) + lay.slots.shared - 2) / (lay.slots.shared - 1));
+    c = max(c, (long long)uniform(sm.heavy));
     const long long t0 = wg * c, t1 = min(total, t0 + c);
     if (t0 >= t1 && wg != 0) return;
 
@@ -410,14 +432,12 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
         long long *bpre = reinterpret_cast<long long *>(ws + lay.off_bpre);
         int *group = reinterpret_cast<int *>(ws + lay.off_group);
         if (wg == 0 && tid == 0) {
-            Plan *p = reinterpret_cast<Plan *>(ws);
-            p->tiles_per_wg = c;
-            p->total = total;
+            reinterpret_cast<Plan *>(ws)->per_wg = c;
         }
         long long before = 0;
         for (int e0 = 0; e0 < entries; e0 += kThreads) {
             const int e = e0 + tid;
-            const long long x = e < entries ? line_tiles(a, entry(a, bat, groups, e)) : 0;
+            const long long x = e < entries ? line_length(a, entry(a, bat, groups, e)) : 0;
             const long long inc = wave_inclusive64(x);
             __syncthreads();
             if (l == 63) sm.part[w] = inc;
@@ -448,16 +468,29 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
     const uint32_t keep = sc == 0.f ? 0u : ~0u;   // and a scale of zero: masked scores stay -inf
     sc = sc == 0.f ? 1.f : fabsf(sc);
 
-    // the tile that is computed, and the one whose rows this wave looks up
+    // the tile that is computed (its place on the line and its unit's, its
+    // number in this workgroup), and the one whose rows this wave looks up
     Cursor cur, ahead;
+    long long t, v0;
+    int ti = 0;
     {
         seek(a, bat, groups, entries, cur, uniform(sm.first_entry));
-        const long long off = uniform(sm.first_off), unit = off / cur.x.tiles;
-        cur.tile = (int)(off - unit * cur.x.tiles);
+        const long long off = uniform(sm.first_off), len = unit_length(cur.x);
+        const long long unit = off / len;
+        const int place = (int)(off - unit * len);
         cur.hk = (int)(unit / cur.x.row_tiles);
         cur.rt = (int)(unit % cur.x.row_tiles);
+        v0 = t0 - place;
+        cur.tile = max(0, (place + cur.x.weight - 1) / cur.x.weight - kUnit);
+        if (cur.tile >= cur.x.tiles) {
+            v0 += len;
+            cur.tile = cur.x.tiles - 1;
+            advance(a, bat, groups, entries, cur);
+        }
         ahead = cur;
+        t = cur.e < entries ? v0 + cur.x.weight * (kUnit + cur.tile) : t1;
     }
+    if (t >= t1) return;               // places without a tile
     const Bases bases{address(a.k), address(a.kc) - address(a.k)};
     // from a cached key's row to its value's, and how much further in the tree
     const unsigned long long to_v = address(a.vc) - address(a.kc);
@@ -513,12 +546,12 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
     fetch(tile_0, ring[0]);
 
     int anc_of = -1;
-    long long t = t0;
     while (t < t1) {
         const Entry x = cur.x;
         const int tile0 = cur.tile, hk = cur.hk, r0 = cur.rt * kRows;
-        const int count = (int)min((long long)(x.tiles - tile0), t1 - t);
-        const int slot = wg - (int)((t - tile0) / c);
+        const int count =
+            (int)min((long long)(x.tiles - tile0), (t1 - t + x.weight - 1) / x.weight);
+        const int slot = wg - (int)((v0 + x.weight * kUnit) / c);
         const bool is_own = cur.e >= groups;
         const int nrows = min(kRows, x.rows - r0);
         const int row_waves = nrows <= 32 ? 1 : nrows <= 64 ? 2 : 4;
@@ -594,7 +627,6 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
         bool odd = false;                  // values were cleared that are not finite
 
         auto one_tile = [&](Tile<D> &tile, Tile<D> &other, int tl) {
-            const int ti = (int)(t - t0);
             // this tile has arrived, and everyone is done with the other one
             __builtin_amdgcn_s_waitcnt(kVmcntZero);
             lds_barrier();
@@ -621,7 +653,10 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
                 if (__syncthreads_or(found)) odd = true;
             }
             if (ti % kAhead == 0) look_ahead(ti + kAhead);
-            if (t + 1 < t1) fetch(other, ring[(ti + 1) & (kRing - 1)]);
+            // the next tile, if there may be one (past the unit its weight is
+            // not known here)
+            if ((tl + 1 < x.tiles ? t + x.weight : t + x.weight + kUnit) < t1)
+                fetch(other, ring[(ti + 1) & (kRing - 1)]);
 
 #pragma unroll 1
             for (int st = 0; st < kKeys / 32; ++st) {
@@ -707,8 +742,8 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
                 }
             }
         };
-        for (int tl = tile0; tl < tile0 + count; ++tl, ++t) {
-            if ((t - t0) & 1) one_tile(tile_1, tile_0, tl);
+        for (int tl = tile0; tl < tile0 + count; ++tl, t += x.weight, ++ti) {
+            if (ti & 1) one_tile(tile_1, tile_0, tl);
             else one_tile(tile_0, tile_1, tl);
         }
         ls += __shfl_xor(ls, 32);
@@ -758,7 +793,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
             }
         };
         if (row_waves < 4) {
-            if ((t - 1 - t0) & 1) join_keys(tile_1);
+            if ((ti - 1) & 1) join_keys(tile_1);
             else join_keys(tile_0);
         }
         // ---- the partial: m, l (negative where values were cleared) and o of
@@ -780,9 +815,14 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
             }
         }
         // on to the next unit
+        v0 += unit_length(x);
         cur.tile = x.tiles - 1;
         advance(a, bat, groups, entries, cur);
+        if (t >= t1 || cur.e >= entries) break;
+        t = v0 + cur.x.weight * kUnit;
     }
+    // nothing may still be on its way into LDS that the next workgroup gets
+    __builtin_amdgcn_s_waitcnt(kVmcntZero);
 }
 
 // Joins the partials of every row and checks the sequence: one workgroup per
@@ -834,25 +874,24 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttentionArgs a, Layout 
         inv = __builtin_nanf("");
     } else {
         const int hq = lr % a.Hq, node = lr / a.Hq, hk = hq / heads;
-        const long long c = plan->tiles_per_wg;
+        const long long c = plan->per_wg;
         const long long *gpre = reinterpret_cast<const long long *>(ws + lay.off_gpre);
         const long long *bpre = reinterpret_cast<const long long *>(ws + lay.off_bpre);
         const int sh = g < 0 ? 0 : fit_shared(a, members, a.gshared[g]);
         // the unit's first tile on the line and its tiles: its partials are
         // one per workgroup between
-        const int row_tiles = (a.n * heads + kRows - 1) / kRows;
-        const int own_tiles = (len - min(len, sh) + a.n + kKeys - 1) / kKeys;
-        const int rt = (node * heads + hq % heads) / kRows;
-        const long long o0 = bpre[b] + ((long long)hk * row_tiles + rt) * own_tiles;
-        const int no = (int)((o0 + own_tiles - 1) / c - o0 / c) + 1;
-        int ns = 0;
-        if (sh > 0) {
-            const int srow_tiles = (int)(((long long)members * a.n * heads + kRows - 1) / kRows);
-            const int stiles = (sh + kKeys - 1) / kKeys;
-            const int srt = (((b - gs) * a.n + node) * heads + hq % heads) / kRows;
-            const long long s0 = gpre[g] + ((long long)hk * srow_tiles + srt) * stiles;
-            ns = (int)((s0 + stiles - 1) / c - s0 / c) + 1;
-        }
+        auto partials = [&](long long start, int rows, int keys, int r) {
+            Entry x;
+            x.rows = rows;
+            x.keys = keys;
+            shape(x);
+            const long long first =
+                start + ((long long)hk * x.row_tiles + r / kRows) * unit_length(x) + x.weight * kUnit;
+            return (int)((first + x.weight * (x.tiles - 1)) / c - first / c) + 1;
+        };
+        const int r = node * heads + hq % heads, rows = a.n * heads;
+        const int no = partials(bpre[b], rows, len - min(len, sh) + a.n, r);
+        const int ns = sh > 0 ? partials(gpre[g], members * rows, sh, (b - gs) * rows + r) : 0;
         const float2 *ml = reinterpret_cast<const float2 *>(ws + lay.off_ml) + qrow;
         const float *o = reinterpret_cast<const float *>(ws + lay.off_o) + qrow * D + d0;
         // eight partials at a time: their loads do not wait for each other
