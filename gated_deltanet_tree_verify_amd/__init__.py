@@ -33,6 +33,7 @@ Serving operators next to the tree calls:
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -153,22 +154,28 @@ def status_string(code: int) -> str:
 # ---------------------------------------------------------------------------
 # marshalling helpers
 # ---------------------------------------------------------------------------
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
     torch = _torch()
     if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
-        return ctypes.c_void_p(stream)
-    return ctypes.c_void_p(stream.cuda_stream)
+        return stream
+    return stream.cuda_stream
 
 
 def _check(fn, code):
@@ -206,13 +213,16 @@ def _need(t, name, dtypes, shape=None):
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
+    if (t.is_cuda and t.dtype in dtypes and t.is_contiguous()
+            and (shape is None or t.shape == shape)):
+        return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
@@ -442,12 +452,17 @@ def index(parent, status=None, stream=None):
 # ---------------------------------------------------------------------------
 # serving operators
 # ---------------------------------------------------------------------------
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(name, *sizes):
+    return max(16, int(getattr(load(), name)(*sizes)))
+
+
 def _workspace(nbytes, device, stream):
     """Device memory for one call, from torch's allocator: ordered on the
     current stream, and kept until `stream` is done with it when that is
     another one."""
     torch = _torch()
-    ws = torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=device)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
     if stream is not None:
         other = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
         # the block may have been used on the current stream just before
@@ -502,7 +517,7 @@ def prefill(q, k, v, alpha, beta, cu, S, src, dst, out=None, status=None, stream
     batch = cu.shape[0] - 1
     rows, Hk, dk, H, dv, out = _rule_shapes(q, k, v, alpha, beta, S, src, dst, out, batch, status)
     dt = _qkv_dtype(q)
-    need = lib.gdn_prefill_workspace(dt, batch, rows, H, Hk, dk, dv)
+    need = _workspace_bytes("gdn_prefill_workspace", dt, batch, rows, H, Hk, dk, dv)
     if workspace is None:
         workspace = _workspace(need, q.device, stream)
     else:
@@ -591,7 +606,8 @@ def tree_attention(q, k, v, parent, k_cache, v_cache, pages, length, scale, shar
     if status is not None:
         _need(status, "status", (torch.int32,), (batch,))
     width = pages.shape[1]
-    need = lib.gdn_tree_attention_workspace(batch, n, Hq, Hkv, d, page, width, groups)
+    need = _workspace_bytes("gdn_tree_attention_workspace", batch, n, Hq, Hkv, d, page, width,
+                            groups)
     if workspace is None:
         workspace = _workspace(need, q.device, stream)
     else:

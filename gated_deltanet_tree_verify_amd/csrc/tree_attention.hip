@@ -45,6 +45,7 @@ constexpr int kWaves = 4;
 constexpr int kKeys = 64;                 // keys of a tile
 constexpr int kRows = 128;                // rows of a unit at most
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kSlack = 8.f;
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
@@ -710,16 +711,20 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
 #pragma unroll
                 for (int r = 1; r < 16; ++r) top = fmaxf(top, z[r]);
                 top = max_of_halves(top) * sc;
-                const float mn = fmaxf(mx, top);
-                // a row that has seen no key yet keeps -inf; its weights are zero
-                const float base = mn == -__builtin_inff() ? 0.f : mn;
-                if (__builtin_expect(__any(mn > mx), 0)) {
-                    const float f = __builtin_amdgcn_exp2f(mx - base);
+                // The maximum that weights are relative to follows the scores
+                // only when one passes it by kSlack (in powers of two): weights
+                // stay below 2^kSlack, sums and partials are right for any
+                // reference, and O is seldom multiplied.  A row that has seen
+                // no key yet keeps -inf; its weights are zero.
+                if (__builtin_expect(__any(top > mx + kSlack), 0)) {
+                    const float mn = fmaxf(mx, top);
+                    const float f = __builtin_amdgcn_exp2f(mx - (mn == -__builtin_inff() ? 0.f : mn));
                     ls *= f;
 #pragma unroll
                     for (int i = 0; i < DT; ++i) O[i] *= f;
                     mx = mn;
                 }
+                const float base = mx == -__builtin_inff() ? 0.f : mx;
                 float p[16];
 #pragma unroll
                 for (int r = 0; r < 16; ++r) {
