@@ -11,15 +11,24 @@
 // once, another carries the state through a sequence's chunks in order.
 //
 //   plan:  chunk slots of the sequences (prefix sums), sequences by length
-//   chunk: a workgroup per (chunk, head): decays, Gram matrices, T, Y, and
-//          the chunk's keys transposed, stored as matrix operands
-//   scan:  a workgroup per (sequence, head, 16 columns of d_v): the columns
-//          of S are independent, and 32 heads of d_v = 128 give the 256
-//          workgroups that fill the chip with a single prompt.  Its four
-//          waves split the rows of every product (16 tokens or 32 rows of
-//          S each) and exchange S, R and U, W through LDS, three barriers a
-//          chunk; the operands that do not depend on S come straight from
-//          memory into registers, a chunk ahead.
+//   chunk: a workgroup per (chunk, head): decays, Gram matrices, T and Y, and
+//          the chunk's keys (also transposed) and queries, stored as matrix
+//          operands
+//   scan:  a workgroup per (sequence, head, 16 or 64 columns of d_v): the
+//          columns of S are independent, and 32 heads of d_v = 128 give the
+//          256 workgroups that fill the chip with a single prompt.  Four waves
+//          carry the state: they split the rows of every product (16 tokens
+//          or 32 rows of S each) and exchange S, R and W through LDS, three
+//          barriers a chunk; four more form the outputs beside them.  The
+//          operands that do not depend on S come from memory into registers,
+//          a chunk ahead.
+//
+// Bound.  The chunk kernel writes 37 KiB a (chunk, head) and is held by
+// latency and that traffic (8192 tokens, 32 heads: 69 us, 2.9 TB/s).  A scan
+// workgroup reads 100 KiB a chunk through its L1: with every chunk read from
+// the same place, so from L2, the scan still takes 9/10 of its time, and the
+// products themselves (60 of 16 cycles a SIMD) are a fifth of it.  A single
+// prompt's chunks follow each other: 128 of them take 128 x 2 us.
 //
 // Operands.  A 16x16 result tile holds row 4 q + r, column m in register r of
 // lane (m = l & 15, q = l >> 4); the matrix instruction takes 8 consecutive
@@ -83,14 +92,14 @@ struct Half {
     static __device__ __forceinline__ f32x4 gram(const Raw8 &x, const Raw8 &y, f32x4 c) {
         return mma(v(x.p[0]), v(y.p[0]), c);
     }
-    // exact . fp32, two operands x at once: the instructions of one sum wait
+    // exact . fp32, two products at once: the instructions of one sum wait
     // for each other, those of the two alternate.  Smallest part first.
-    static __device__ __forceinline__ void mul(const Raw8 &x0, const Raw8 &x1, const Raw8 &y,
-                                               f32x4 &c0, f32x4 &c1) {
+    static __device__ __forceinline__ void mul(const Raw8 &x0, const Raw8 &x1, const Raw8 &y0,
+                                               const Raw8 &y1, f32x4 &c0, f32x4 &c1) {
 #pragma unroll
         for (int p = 2; p >= 0; --p) {
-            c0 = mma(v(x0.p[0]), v(y.p[p]), c0);
-            c1 = mma(v(x1.p[0]), v(y.p[p]), c1);
+            c0 = mma(v(x0.p[0]), v(y0.p[p]), c0);
+            c1 = mma(v(x1.p[0]), v(y1.p[p]), c1);
         }
     }
     // fp32 . fp32 into c + d: two sums that alternate
@@ -136,16 +145,6 @@ struct Half {
         for (int p = 0; p < 3; ++p) r.p[p] = make_uint4(a[p].x, a[p].y, b[p].x, b[p].y);
         return r;
     }
-    static __device__ __forceinline__ Raw8 load8(const elem *p, bool ok) {
-        Raw8 x = {};
-        if (ok) x.p[0] = *reinterpret_cast<const uint4 *>(p);
-        return x;
-    }
-    static __device__ __forceinline__ Raw8 load8(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-        Raw8 x;
-        x.p[0] = tile::load16<0>(r, off);
-        return x;
-    }
     static __device__ __forceinline__ uint32_t load1(__amdgpu_buffer_rsrc_t r, uint32_t off) {
         return (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, (int)off, 0, 0);
     }
@@ -168,10 +167,10 @@ struct Full {
                                                      __uint_as_float(ys[e]), c, 0, 0, 0);
         return c;
     }
-    static __device__ __forceinline__ void mul(const Raw8 &x0, const Raw8 &x1, const Raw8 &y,
-                                               f32x4 &c0, f32x4 &c1) {
-        c0 = gram(x0, y, c0);
-        c1 = gram(x1, y, c1);
+    static __device__ __forceinline__ void mul(const Raw8 &x0, const Raw8 &x1, const Raw8 &y0,
+                                               const Raw8 &y1, f32x4 &c0, f32x4 &c1) {
+        c0 = gram(x0, y0, c0);
+        c1 = gram(x1, y1, c1);
     }
     static __device__ __forceinline__ void mul2(const Raw8 &x, const Raw8 &y, f32x4 &c, f32x4 &) {
         c = gram(x, y, c);
@@ -182,20 +181,6 @@ struct Full {
     }
     static __device__ __forceinline__ Raw8 from_f32(const float *x) {
         return {{*reinterpret_cast<const uint4 *>(x), *reinterpret_cast<const uint4 *>(x + 4)}};
-    }
-    static __device__ __forceinline__ Raw8 load8(const elem *p, bool ok) {
-        Raw8 x = {};
-        if (ok) {
-            x.p[0] = reinterpret_cast<const uint4 *>(p)[0];
-            x.p[1] = reinterpret_cast<const uint4 *>(p)[1];
-        }
-        return x;
-    }
-    static __device__ __forceinline__ Raw8 load8(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-        Raw8 x;
-        x.p[0] = tile::load16<0>(r, off);
-        x.p[1] = tile::load16<0>(r, off + 16);
-        return x;
     }
     static __device__ __forceinline__ uint32_t load1(__amdgpu_buffer_rsrc_t r, uint32_t off) {
         return __builtin_amdgcn_raw_buffer_load_b32(r, (int)off, 0, 0);
@@ -213,7 +198,7 @@ __device__ __forceinline__ void store1(__amdgpu_buffer_rsrc_t r, uint32_t off, f
 // an offset past the end of any buffer: loads give zero, stores do nothing
 constexpr uint32_t kNowhere = 0x80000000u;
 
-// one (chunk, head) of the workspace
+// one (chunk, head) of the workspace; a head's chunks follow each other
 template <typename M>
 struct ChunkData {
     uint4 t[kFrags][M::kParts][64];      // T - I as operands
@@ -221,14 +206,25 @@ struct ChunkData {
     float4 vec[kC];              // beta, beta e^g, e^g, e^{g_l - g} of the tokens
 };
 
+// A chunk's keys and queries as matrix operands, per key head, in runs of
+// 1 KiB: the scan's workgroups read them 8 times (d_v = 128), and in place
+// each run would be 16 pieces in as many lines.
+template <typename M, int DK>
+struct KeyData {
+    uint4 k[4][DK / 32][M::kExact][64];       // token tile i, contraction over rows of S
+    uint4 q[4][DK / 32][M::kExact][64];
+    uint4 kt[DK / 16][2][M::kExact][64];      // rows of S, contraction over tokens
+};
+
 struct Layout {
     int slots;                   // chunk slots
-    int64_t off_pre, off_order, off_seq, off_kt, off_data, bytes;
+    int64_t off_pre, off_order, off_slot, off_keys, off_data, bytes;
 };
 
 // ---------------------------------------------------------------------------
-// plan: pre[i] = first chunk slot of sequence i (-1: bad rows), seq[slot] its
-// sequence (-1: unused slot), order = sequences, most chunks first
+// plan: pre[i] = first chunk slot of sequence i (-1: bad rows), slot[s] = the
+// sequence, first row and tokens of a chunk (sequence -1: unused slot), order
+// = sequences, most chunks first
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ int chunks_of(const RuleArgs &a, int i) {
     const rule::Sequence s = rule::sequence(a, i);
@@ -237,19 +233,25 @@ __device__ __forceinline__ int chunks_of(const RuleArgs &a, int i) {
 
 __global__ __launch_bounds__(kPlanThreads) void prefill_plan_kernel(RuleArgs a, Layout y) {
     __shared__ int s_part[kPlanThreads / 64];
-    __shared__ int s_n[kSortMax];
+    __shared__ int s_n[kSortMax], s_start[kSortMax];
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63;
     char *ws = static_cast<char *>(a.workspace);
     int *pre = reinterpret_cast<int *>(ws + y.off_pre);
     int *order = reinterpret_cast<int *>(ws + y.off_order);
-    int *seq = reinterpret_cast<int *>(ws + y.off_seq);
-    for (int s = tid; s < y.slots; s += kPlanThreads) seq[s] = -1;
+    int4 *slot = reinterpret_cast<int4 *>(ws + y.off_slot);
+    auto chunk = [&](int i, int c) {
+        const int row0 = a.cu[i] + kC * c;
+        return make_int4(i, row0, min(kC, a.cu[i + 1] - row0), 0);
+    };
     const bool sorted = a.batch <= kSortMax;
+    if (!sorted) {
+        for (int s = tid; s < y.slots; s += kPlanThreads) slot[s] = make_int4(-1, 0, 0, 0);
+        __syncthreads();
+    }
     long long sum = 0;
     for (int i0 = 0; i0 < a.batch; i0 += kPlanThreads) {
         const int i = i0 + tid;
         const int n = i < a.batch ? chunks_of(a, i) : 0;
-        if (sorted && i < a.batch) s_n[i] = n;
         int inc = max(n, 0);
 #pragma unroll
         for (int o = 1; o < 64; o <<= 1) {
@@ -270,22 +272,43 @@ __global__ __launch_bounds__(kPlanThreads) void prefill_plan_kernel(RuleArgs a, 
             // that overlap may not
             const bool ok = n >= 0 && at + n <= y.slots;
             pre[i] = ok ? (int)at : -1;
-            if (ok)
-                for (int c = 0; c < n; ++c) seq[at + c] = i;
-            if (!sorted) order[i] = i;
+            if (sorted) {
+                s_n[i] = ok ? n : -1;
+                s_start[i] = (int)min(at, (long long)y.slots);
+            } else {
+                order[i] = i;
+                if (ok)
+                    for (int c = 0; c < n; ++c) slot[at + c] = chunk(i, c);
+            }
         }
     }
+    if (!sorted) return;
     __syncthreads();
-    if (sorted && tid < a.batch) {
+    if (tid < a.batch) {
         const int n = s_n[tid];
         int rank = 0;
         for (int j = 0; j < a.batch; ++j) rank += s_n[j] > n || (s_n[j] == n && j < tid);
         order[rank] = tid;
     }
+    for (int s = tid; s < y.slots; s += kPlanThreads) {
+        int lo = 0, hi = a.batch - 1;             // last sequence that starts by slot s
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (s_start[mid] <= s) lo = mid;
+            else hi = mid - 1;
+        }
+        const int c = s - s_start[lo];
+        slot[s] = c < s_n[lo] ? chunk(lo, c) : make_int4(-1, 0, 0, 0);
+    }
 }
 
 // ---------------------------------------------------------------------------
-// chunk: T, Y, decays, transposed keys
+// chunk: T, Y, decays; keys and queries as operands
+//
+// K and Q rows go through LDS once (whole lines from memory); X and Y take
+// their place after the Gram products.  T^T is kept above the diagonal of the
+// array that holds X below it, the diagonal blocks of T^T over those of X, so
+// that four workgroups fit a compute unit (d_k = 128, bf16).
 // ---------------------------------------------------------------------------
 constexpr int kLd = kC + 4;      // LDS row stride of the 64-wide matrices (floats)
 
@@ -293,21 +316,45 @@ template <typename M, int DK>
 __global__ __launch_bounds__(kThreads) void prefill_chunk_kernel(RuleArgs a, Layout y) {
     typedef typename M::elem T;
     constexpr int J = DK / 32;
-    __shared__ float s_x[kC][kLd], s_t[kC][kLd], s_y[kC][kLd];
+    constexpr int P = DK * sizeof(T) / 16;       // 16-byte pieces of a row
+    constexpr int kPer = kC * P / kThreads;      // of K, and of Q, a thread loads
+    struct Rows {
+        uint4 k[kC][P], q[kC][P];
+    };
+    struct Square {
+        float x[kC][kLd], y[kC][kLd];
+    };
+    __shared__ union {
+        Rows in;
+        Square sq;
+    } sm;
     __shared__ double s_g[kC];
     __shared__ float s_beta[kC];
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
     const int m = l & 15, qd = l >> 4;
     char *ws = static_cast<char *>(a.workspace);
     const int slot = blockIdx.x / a.H, h = blockIdx.x % a.H;
-    const int i = reinterpret_cast<const int *>(ws + y.off_seq)[slot];
-    if (i < 0) return;
+    const int4 at = reinterpret_cast<const int4 *>(ws + y.off_slot)[slot];
+    if (at.x < 0) return;
     const int rep = a.H / a.Hk, hk = h / rep;
-    const int row0 = a.cu[i] + kC * (slot - reinterpret_cast<const int *>(ws + y.off_pre)[i]);
-    const int n = min(kC, a.cu[i + 1] - row0);
+    const int row0 = at.y, n = at.z;
     ChunkData<M> *out =
-        reinterpret_cast<ChunkData<M> *>(ws + y.off_data) + (size_t)slot * a.H + h;
+        reinterpret_cast<ChunkData<M> *>(ws + y.off_data) + (size_t)h * y.slots + slot;
 
+    const T *kp = static_cast<const T *>(a.k) + ((size_t)row0 * a.Hk + hk) * a.dk;
+    const T *qp = static_cast<const T *>(a.q) + ((size_t)row0 * a.Hk + hk) * a.dk;
+    const size_t stride = (size_t)a.Hk * a.dk;
+    constexpr int E = 16 / sizeof(T);            // elements of a piece
+    uint4 kin[kPer], qin[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int t = (tid + kThreads * i) / P, c = (tid + kThreads * i) % P;
+        kin[i] = qin[i] = make_uint4(0, 0, 0, 0);
+        if (t < n && E * c < a.dk) {
+            kin[i] = *reinterpret_cast<const uint4 *>(kp + t * stride + E * c);
+            qin[i] = *reinterpret_cast<const uint4 *>(qp + t * stride + E * c);
+        }
+    }
     // ---- decays; a token past the end has alpha 1 and beta 0
     if (w == 0) {
         float lg = 0.f, be = 0.f;
@@ -315,7 +362,8 @@ __global__ __launch_bounds__(kThreads) void prefill_chunk_kernel(RuleArgs a, Lay
             const size_t at = ((size_t)row0 + l) * a.H + h;
             // alpha = 0: far enough below any exponent to clear the state,
             // small enough to keep the other tokens' logarithms exact
-            lg = fmaxf(log2f(a.alpha[at]), -1e4f);
+            const float al = a.alpha[at];
+            lg = al == 0.f ? -1e4f : log2f(al);
             be = a.beta[at];
         }
         double g = lg;
@@ -330,41 +378,77 @@ __global__ __launch_bounds__(kThreads) void prefill_chunk_kernel(RuleArgs a, Lay
         const float eg = exp2f((float)g);
         out->vec[l] = make_float4(be, be * eg, eg, exp2f((float)(last - g)));
     }
-
-    const T *kp = static_cast<const T *>(a.k) + ((size_t)row0 * a.Hk + hk) * a.dk;
-    const T *qp = static_cast<const T *>(a.q) + ((size_t)row0 * a.Hk + hk) * a.dk;
-    const size_t stride = (size_t)a.Hk * a.dk;
-    auto rows8 = [&](const T *p, int t, int j) {
-        const int d0 = 32 * j + 8 * qd;
-        return M::load8(p + t * stride + d0, t < n && d0 < a.dk);
-    };
-    Raw8 ka[J], qa[J];
+    // pieces are turned by the row: 16 rows read at one piece spread over the banks
+    auto piece = [&](int t, int c) { return c ^ (t & (P < 16 ? P - 1 : 15)); };
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-        ka[j] = rows8(kp, 16 * w + m, j);
-        qa[j] = rows8(qp, 16 * w + m, j);
+    for (int i = 0; i < kPer; ++i) {
+        const int t = (tid + kThreads * i) / P, c = (tid + kThreads * i) % P;
+        sm.in.k[t][piece(t, c)] = kin[i];
+        sm.in.q[t][piece(t, c)] = qin[i];
     }
     __syncthreads();
+    auto operand = [&](const uint4(*rows)[P], int t, int j) {
+        Raw8 x;
+#pragma unroll
+        for (int p = 0; p < M::kExact; ++p)
+            x.p[p] = rows[t][piece(t, (4 * j + qd) * M::kExact + p)];
+        return x;
+    };
 
     // ---- tiles (w, jb) of X and Y: rows 16 w + 4 qd + r, column 16 jb + m
-    for (int jb = 0; jb <= w; ++jb) {
-        f32x4 kk = {}, qk = {};
+    f32x4 kk[4] = {}, qk[4] = {};
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        const Raw8 ka = operand(sm.in.k, 16 * w + m, j), qa = operand(sm.in.q, 16 * w + m, j);
+#pragma unroll
+        for (int jb = 0; jb < 4; ++jb)
+            if (jb <= w) {
+                const Raw8 kb = operand(sm.in.k, 16 * jb + m, j);
+                kk[jb] = M::gram(ka, kb, kk[jb]);
+                qk[jb] = M::gram(qa, kb, qk[jb]);
+            }
+    }
+    // ---- operands of the scan, once per key head
+    if (h % rep == 0) {
+        KeyData<M, DK> *to = reinterpret_cast<KeyData<M, DK> *>(ws + y.off_keys) +
+                             (size_t)hk * y.slots + slot;
 #pragma unroll
         for (int j = 0; j < J; ++j) {
-            const Raw8 kb = rows8(kp, 16 * jb + m, j);
-            kk = M::gram(ka[j], kb, kk);
-            qk = M::gram(qa[j], kb, qk);
-        }
-        const int s = 16 * jb + m;
-        const double gs = s_g[s];
+            const Raw8 kx = operand(sm.in.k, rho(w, m), j), qx = operand(sm.in.q, rho(w, m), j);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int t = 16 * w + 4 * qd + r;
-            const float e = exp2f((float)(s_g[t] - gs));
-            s_x[t][s] = s < t ? s_beta[t] * e * kk[r] : 0.f;
-            s_y[t][s] = s <= t ? e * qk[r] : 0.f;
+            for (int p = 0; p < M::kExact; ++p) {
+                to->k[w][j][p][l] = kx.p[p];
+                to->q[w][j][p][l] = qx.p[p];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < DK / 32; ++i) {      // a lane: 8 consecutive tokens of one row of S
+            const int f = 4 * i + w, ti = f >> 1, jt = f & 1, d = rho(ti, m);
+            alignas(16) T x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int t = 32 * jt + 8 * qd + e;
+                x[e] = reinterpret_cast<const T *>(&sm.in.k[t][piece(t, d / E)])[d % E];
+            }
+#pragma unroll
+            for (int p = 0; p < M::kExact; ++p)
+                to->kt[ti][jt][p][l] = reinterpret_cast<const uint4 *>(x)[p];
         }
     }
+    __syncthreads();                             // X and Y take the rows' place
+#pragma unroll
+    for (int jb = 0; jb < 4; ++jb)
+        if (jb <= w) {
+            const int s = 16 * jb + m;
+            const double gs = s_g[s];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int t = 16 * w + 4 * qd + r;
+                const float e = exp2f((float)(s_g[t] - gs));
+                sm.sq.x[t][s] = s < t ? s_beta[t] * e * kk[jb][r] : 0.f;
+                sm.sq.y[t][s] = s <= t ? e * qk[jb][r] : 0.f;
+            }
+        }
     __syncthreads();
 
     // ---- T by blocks of 16: the diagonal block of wave w by substitution,
@@ -374,21 +458,21 @@ __global__ __launch_bounds__(kThreads) void prefill_chunk_kernel(RuleArgs a, Lay
     for (int r = 0; r < 16; ++r) {
         float acc = r == m ? 1.f : 0.f;
 #pragma unroll
-        for (int s = 0; s < r; ++s) acc = fmaf(-s_x[16 * w + r][16 * w + s], t[s], acc);
+        for (int s = 0; s < r; ++s) acc = fmaf(-sm.sq.x[16 * w + r][16 * w + s], t[s], acc);
         t[r] = acc;
     }
     f32x4 tb[4];                       // tiles (k, w) of T, by k - w
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-        const float lo = qd & 1 ? t[4 + r] : t[r], hi = qd & 1 ? t[12 + r] : t[8 + r];
-        tb[0][r] = qd & 2 ? hi : lo;
-        s_t[16 * w + 4 * qd + r][16 * w + m] = tb[0][r];
+        // of values: a choice between elements would keep t in memory
+        const float t0 = t[r], t1 = t[4 + r], t2 = t[8 + r], t3 = t[12 + r];
+        tb[0][r] = qd & 2 ? (qd & 1 ? t3 : t2) : (qd & 1 ? t1 : t0);
     }
+    *reinterpret_cast<f32x4 *>(&sm.sq.x[16 * w + m][16 * w + 4 * qd]) = tb[0];
     __syncthreads();
     // below it, T_iw = -T_ii sum_k X_ik T_kw: fp32 products (contraction
     // index 4 qd + r of a block at step r)
-    auto block = [&](const float(*x)[kLd], int bi, int bk, const f32x4 &b, f32x4 c) {
-        const f32x4 av = *reinterpret_cast<const f32x4 *>(&x[16 * bi + m][16 * bk + 4 * qd]);
+    auto product = [&](const f32x4 &av, const f32x4 &b, f32x4 c) {
 #pragma unroll
         for (int r = 0; r < 4; ++r)
             c = __builtin_amdgcn_mfma_f32_16x16x4f32(av[r], b[r], c, 0, 0, 0);
@@ -400,65 +484,59 @@ __global__ __launch_bounds__(kThreads) void prefill_chunk_kernel(RuleArgs a, Lay
         if (bi < 4) {
             f32x4 p = {};
 #pragma unroll
-            for (int dk = 0; dk < di; ++dk) p = block(s_x, bi, w + dk, tb[dk], p);
-            const f32x4 z = block(s_t, bi, bi, p, f32x4{});
+            for (int dk = 0; dk < di; ++dk)
+                p = product(*reinterpret_cast<const f32x4 *>(
+                                &sm.sq.x[16 * bi + m][16 * (w + dk) + 4 * qd]),
+                            tb[dk], p);
+            f32x4 tii;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                tb[di][r] = -z[r];
-                s_t[16 * bi + 4 * qd + r][16 * w + m] = -z[r];
-            }
+            for (int r = 0; r < 4; ++r) tii[r] = sm.sq.x[16 * bi + 4 * qd + r][16 * bi + m];
+            tb[di] = -product(tii, p, f32x4{});
+            *reinterpret_cast<f32x4 *>(&sm.sq.x[16 * w + m][16 * bi + 4 * qd]) = tb[di];
         }
     }
     __syncthreads();
 
-    // ---- out as operands: tile w's rows
-    const int tr = rho(w, m);
-    for (int j = 0; j <= w >> 1; ++j) {
-        const int k0 = 32 * j + 8 * qd, f = frag_of(w, j);
-        float tv[8], yv[8];
+    // ---- out as operands, three of the twelve pieces a wave
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            tv[e] = k0 + e < tr ? s_t[tr][k0 + e] : 0.f;
-            yv[e] = k0 + e <= tr ? s_y[tr][k0 + e] : 0.f;
+    for (int i = 0; i < 2 * kFrags / 4; ++i) {
+        const int job = 4 * i + w, f = job % kFrags;
+        const int ti = f < 2 ? f : (f + 2) >> 1, j = f < 2 ? 0 : f & 1;
+        const int tr = rho(ti, m), k0 = 32 * j + 8 * qd;
+        float v[8];
+        if (job < kFrags) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = k0 + e < tr ? sm.sq.x[k0 + e][tr] : 0.f;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = k0 + e <= tr ? sm.sq.y[tr][k0 + e] : 0.f;
         }
-        const Raw8 tx = M::from_f32(tv), yx = M::from_f32(yv);
+        const Raw8 x = M::from_f32(v);
+        uint4(*to)[64] = job < kFrags ? out->t[f] : out->y[f];
 #pragma unroll
-        for (int p = 0; p < M::kParts; ++p) {
-            out->t[f][p][l] = tx.p[p];
-            out->y[f][p][l] = yx.p[p];
-        }
-    }
-    // ---- the keys transposed, once per key head: tile i's rows are rows of
-    // S, 8 consecutive tokens a lane
-    if (h % rep == 0) {
-        uint4 *kt = reinterpret_cast<uint4 *>(ws + y.off_kt) +
-                    ((size_t)slot * a.Hk + hk) * (DK / 16) * 2 * M::kExact * 64;
-        for (int f = w; f < (DK / 16) * 2; f += 4) {
-            const int ti = f >> 1, jt = f & 1, d = rho(ti, m);
-            alignas(16) T x[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int tok = 32 * jt + 8 * qd + e;
-                x[e] = tok < n && d < a.dk ? kp[tok * stride + d] : T(0);
-            }
-#pragma unroll
-            for (int p = 0; p < M::kExact; ++p)
-                kt[(f * M::kExact + p) * 64 + l] = reinterpret_cast<const uint4 *>(x)[p];
-        }
+        for (int p = 0; p < M::kParts; ++p) to[p][l] = x.p[p];
     }
 }
 
 // ---------------------------------------------------------------------------
 // scan: the state through a sequence's chunks
 // ---------------------------------------------------------------------------
+// Eight waves: four carry the state, four form the outputs.  The state waves'
+// products wait for each other, and a wave that waits to issue a load issues
+// no product: the second wave of a SIMD fills these gaps (8192 tokens, 32
+// heads, 16 columns a workgroup: 280 us; all in four waves: 328 us).
+constexpr int kScanThreads = 512;
+
 template <typename M, int DK, typename OT, int G>
-__global__ __launch_bounds__(kThreads, 2) void prefill_scan_kernel(RuleArgs a, Layout y,
-                                                                   int tiles) {
+__global__ __launch_bounds__(kScanThreads, 2) void prefill_scan_kernel(
+    RuleArgs a, Layout y, int tiles) {
     typedef typename M::elem T;
     constexpr int J = DK / 32;
     constexpr int N = M::kParts;
+    __shared__ __attribute__((aligned(16))) float s_vec[8][64];
     __shared__ uint4 s_s[G][J][N][64], s_r[G][2][N][64], s_u[G][2][N][64], s_w[G][2][N][64];
-    const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
+    const int w = wave & 3;                         // of the four of its role
     const int m = l & 15, qd = l >> 4;
     char *ws = static_cast<char *>(a.workspace);
     // the column tiles of a (sequence, head) read the same chunk data: they
@@ -484,7 +562,7 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_scan_kernel(RuleArgs a, L
     if (sq.fault) {
         OT *out = static_cast<OT *>(a.out) + (size_t)h * a.dv + col0;
         if (!(sq.fault & kFaultBadLength))
-            for (int t = tid >> 4; t < sq.len; t += kThreads / 16)
+            for (int t = tid >> 4; t < sq.len; t += kScanThreads / 16)
 #pragma unroll
                 for (int g = 0; g < G; ++g)
                     if (col0 + kCols * g < a.dv)
@@ -493,6 +571,136 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_scan_kernel(RuleArgs a, L
         return;
     }
 
+    const T *vp = static_cast<const T *>(a.v) + (size_t)sq.first * ostride + (size_t)h * a.dv;
+    const OT *op = static_cast<const OT *>(a.out) + (size_t)sq.first * ostride + (size_t)h * a.dv;
+    const ChunkData<M> *data =
+        reinterpret_cast<const ChunkData<M> *>(ws + y.off_data) + (size_t)h * y.slots + pre;
+    const KeyData<M, DK> *keys =
+        reinterpret_cast<const KeyData<M, DK> *>(ws + y.off_keys) + (size_t)hk * y.slots + pre;
+
+    const int tok4 = 32 * (w >> 1) + 8 * qd + 4 * (w & 1);   // its four tokens of R, U, O
+    // rows of V and O are addressed from a chunk's first: 32-bit offsets, and
+    // what lies past its tokens reads as zero with no branch, so that a load
+    // is waited for where it is used
+    uint32_t voff[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+        voff[g] = col0 + kCols * g < a.dv ? (uint32_t)(tok4 * ostride + col0 + kCols * g) : kNowhere;
+    auto tokens = [&](int c) { return min(kC, sq.len - kC * c); };
+    auto rsrc = [&](const void *p, size_t row, size_t width, size_t size, int c) {
+        return tile::make_rsrc(static_cast<const char *>(p) + (size_t)kC * c * row * size,
+                               (uint32_t)(((tokens(c) - 1) * row + width) * size));
+    };
+    // an element offset of kNowhere stays past the end in bytes
+    auto bytes = [&](uint32_t off, int r, uint32_t size) {
+        return off == kNowhere ? kNowhere : (off + (uint32_t)(r * ostride)) * size;
+    };
+    // tiles 0 and 1 of a triangle have no second operand: its registers get
+    // the first once more (behind a branch, the loads would be waited for
+    // where the branch ends)
+    auto load_frags = [&](const uint4(*from)[N][64], Raw8 *to) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int f = frag_of(w, min(j, w >> 1));
+#pragma unroll
+            for (int n = 0; n < N; ++n) to[j].p[n] = from[f][n][l];
+        }
+    };
+    auto load_rows = [&](const uint4(*from)[J][M::kExact][64], Raw8 *to) {
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int n = 0; n < M::kExact; ++n) to[j].p[n] = from[w][j][n][l];
+    };
+    // the wave's 16 tokens' factors: one number a lane, and through LDS four
+    // numbers of four tokens
+    auto load_vec = [&](int c) {
+        return reinterpret_cast<const float *>(
+            &data[c].vec[rho(w, l >> 2)])[l & 3];
+    };
+    auto read = [&](uint4(*buf)[N][64], int j) {
+        Raw8 b;
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            b.p[n] = buf[j][n][l];
+        return b;
+    };
+    // f(g, operands of group g) for the column groups of buf.  All of a
+    // group's reads are issued a group ahead of its products, and in one go:
+    // left to the compiler, they are issued a few at a time and waited for
+    // each time (8192 tokens: 280 us, so 262 us).
+    auto groups = [&](auto &buf, auto f) {
+        constexpr int K = sizeof(buf[0]) / sizeof(buf[0][0]);
+        Raw8 b[2][K];
+#pragma unroll
+        for (int j = 0; j < K; ++j) b[0][j] = read(buf[0], j);
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            if (g + 1 < G)
+#pragma unroll
+                for (int j = 0; j < K; ++j) b[(g + 1) & 1][j] = read(buf[g + 1], j);
+            __builtin_amdgcn_sched_barrier(0);
+            f(g, b[g & 1]);
+        }
+    };
+    // rows of x times the columns of S, two sums that alternate
+    auto times_state = [&](const Raw8 *x, const Raw8 *b) {
+        f32x4 even = {}, odd = {};
+#pragma unroll
+        for (int j = 0; j < J; j += 2) M::mul(x[j], x[j + 1], b[j], b[j + 1], even, odd);
+        return even + odd;
+    };
+    // c + the wave's rows of a lower triangle times b
+    auto times_lower = [&](const Raw8 *x, const Raw8 *b, f32x4 c) {
+        f32x4 more = {};
+        M::mul2(x[0], b[0], c, more);
+        if (w >> 1) M::mul2(x[1], b[1], c, more);
+        return c + more;
+    };
+
+    // An operand's registers are loaded again, for the next chunk, as soon as
+    // they have been used for the last time: a chunk ahead of their next use.
+    const int chunks = (sq.len + kC - 1) / kC;
+    if (wave >= 4) {
+        // ---- outputs: e^g Q S while the state waves form U, Y U while they
+        // update S
+        Raw8 qf[J], yf[2];
+        float vec1 = 0.f;
+        if (chunks > 0) {
+            load_rows(keys->q, qf);
+            vec1 = load_vec(0);
+            load_frags(data->y, yf);
+        }
+        lds_barrier();
+        for (int c = 0; c < chunks; ++c) {
+            const int next = min(c + 1, chunks - 1);
+            s_vec[wave][l] = vec1;
+            vec1 = load_vec(next);
+            lds_barrier();
+            f32x4 o[G];
+            groups(s_s, [&](int g, const Raw8 *b) { o[g] = times_state(qf, b); });
+            load_rows(keys[next].q, qf);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float eg = s_vec[wave][4 * (4 * qd + r) + 2];
+#pragma unroll
+                for (int g = 0; g < G; ++g) o[g][r] *= eg;
+            }
+            lds_barrier();
+            const __amdgpu_buffer_rsrc_t ro = rsrc(op, ostride, a.dv, sizeof(OT), c);
+            groups(s_u, [&](int g, const Raw8 *b) { o[g] = times_lower(yf, b, o[g]); });
+            load_frags(data[next].y, yf);
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    store1(ro, bytes(voff[g], r, sizeof(OT)), o[g][r], OT{});
+            lds_barrier();
+        }
+        return;
+    }
+
+    __builtin_amdgcn_s_setprio(3);          // the outputs are never waited for
     // ---- rows rho(2 w, .) and rho(2 w + 1, .) of the state's columns
     const size_t slab = (size_t)a.H * a.dk * a.dv;
     const size_t sat = (size_t)h * a.dk * a.dv + col0;
@@ -508,188 +716,89 @@ __global__ __launch_bounds__(kThreads, 2) void prefill_scan_kernel(RuleArgs a, L
                     st[g][e >> 2][e & 3] =
                         a.S[sq.src * slab + sat + (size_t)(sr + e) * a.dv + kCols * g];
     }
-    auto put_state = [&]() {
-        if (w < J)
+    if (w < J)
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
-                M::put_tile(s_s[g], w, 0, l, st[g][0]);
-                M::put_tile(s_s[g], w, 1, l, st[g][1]);
-            }
-    };
-    put_state();
-
-    const T *kp = static_cast<const T *>(a.k) + ((size_t)sq.first * a.Hk + hk) * a.dk;
-    const T *qp = static_cast<const T *>(a.q) + ((size_t)sq.first * a.Hk + hk) * a.dk;
-    const T *vp = static_cast<const T *>(a.v) + (size_t)sq.first * ostride + (size_t)h * a.dv;
-    const OT *op = static_cast<const OT *>(a.out) + (size_t)sq.first * ostride + (size_t)h * a.dv;
-    const size_t kstride = (size_t)a.Hk * a.dk;
-    const ChunkData<M> *data =
-        reinterpret_cast<const ChunkData<M> *>(ws + y.off_data) + (size_t)pre * a.H + h;
-    const size_t ktsize = (size_t)(DK / 16) * 2 * M::kExact * 64;
-    const uint4 *ktp =
-        reinterpret_cast<const uint4 *>(ws + y.off_kt) + ((size_t)pre * a.Hk + hk) * ktsize;
-
-    const int tok = rho(w, m);                      // this lane's row of K, Q
-    const int tok4 = 32 * (w >> 1) + 8 * qd + 4 * (w & 1);   // its four tokens of R, U, O
-    // rows of a chunk are addressed from its first: 32-bit offsets, and what
-    // lies past the chunk's tokens reads as zero with no branch, so that a
-    // load is waited for where it is used
-    uint32_t koff[J], voff[G];
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-        const int d0 = 32 * j + 8 * qd;
-        koff[j] = d0 < a.dk ? (uint32_t)((tok * kstride + d0) * sizeof(T)) : kNowhere;
-    }
-#pragma unroll
-    for (int g = 0; g < G; ++g)
-        voff[g] = col0 + kCols * g < a.dv ? (uint32_t)(tok4 * ostride + col0 + kCols * g) : kNowhere;
-    auto tokens = [&](int c) { return min(kC, sq.len - kC * c); };
-    auto rsrc = [&](const void *p, size_t row, size_t width, size_t size, int c) {
-        return tile::make_rsrc(static_cast<const char *>(p) + (size_t)kC * c * row * size,
-                               (uint32_t)(((tokens(c) - 1) * row + width) * size));
-    };
-    // an element offset of kNowhere stays past the end in bytes
-    auto bytes = [&](uint32_t off, int r, uint32_t size) {
-        return off == kNowhere ? kNowhere : (off + (uint32_t)(r * ostride)) * size;
-    };
-    Raw8 kf[J], qf[J], tf[2], yf[2], kt[2][2];
-    float4 vec[4];
-    uint32_t vv[G][4];
-    float egl = 0.f;
-    auto load_kq = [&](int c) {
-        const __amdgpu_buffer_rsrc_t rk = rsrc(kp, kstride, a.dk, sizeof(T), c);
-        const __amdgpu_buffer_rsrc_t rq = rsrc(qp, kstride, a.dk, sizeof(T), c);
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-            kf[j] = M::load8(rk, koff[j]);
-            qf[j] = M::load8(rq, koff[j]);
+        for (int g = 0; g < G; ++g) {
+            M::put_tile(s_s[g], w, 0, l, st[g][0]);
+            M::put_tile(s_s[g], w, 1, l, st[g][1]);
         }
-    };
-    auto load_tv = [&](int c) {
-        const ChunkData<M> *p = data + (size_t)c * a.H;
+
+    Raw8 kf[J], tf[2], kt[2][2];
+    float vec1 = 0.f, egl = 0.f;
+    uint32_t vv[G][4];
+    auto load_v = [&](int c) {
         const __amdgpu_buffer_rsrc_t rv = rsrc(vp, ostride, a.dv, sizeof(T), c);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
+        for (int r = 0; r < 4; ++r)
 #pragma unroll
             for (int g = 0; g < G; ++g) vv[g][r] = M::load1(rv, bytes(voff[g], r, sizeof(T)));
-            vec[r] = p->vec[tok4 + r];
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            if (j <= w >> 1) {
-                const int f = frag_of(w, j);
-#pragma unroll
-                for (int n = 0; n < N; ++n) tf[j].p[n] = p->t[f][n][l];
-            }
+        vec1 = load_vec(c);
     };
-    auto load_yk = [&](int c) {
-        const ChunkData<M> *p = data + (size_t)c * a.H;
-        egl = p->vec[kC - 1].z;
-        if (w < J) {
-            const uint4 *q = ktp + (size_t)c * a.Hk * ktsize;
+    auto load_kt = [&](int c) {
+        egl = data[c].vec[kC - 1].z;
+        const KeyData<M, DK> *p = keys + c;
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
+        for (int s = 0; s < 2; ++s)
 #pragma unroll
-                for (int jt = 0; jt < 2; ++jt) {
-                    const int f = ((2 * w + s) * 2 + jt) * M::kExact;
+            for (int jt = 0; jt < 2; ++jt)
+                // waves past the rows of S: any tile will do
 #pragma unroll
-                    for (int n = 0; n < M::kExact; ++n) kt[s][jt].p[n] = q[(f + n) * 64 + l];
-                }
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-            if (j <= w >> 1) {
-                const int f = frag_of(w, j);
-#pragma unroll
-                for (int n = 0; n < N; ++n) yf[j].p[n] = p->y[f][n][l];
-            }
+                for (int n = 0; n < M::kExact; ++n)
+                    kt[s][jt].p[n] = p->kt[(2 * w + s) & (DK / 16 - 1)][jt][n][l];
     };
-    auto read = [&](uint4(*buf)[N][64], int j) {
-        Raw8 b;
-#pragma unroll
-        for (int n = 0; n < N; ++n)
-            b.p[n] = buf[j][n][l];
-        return b;
-    };
-
-    // Each phase first reads the operands that the barrier before it made
-    // good, then issues the loads whose registers the last phase set free (a
-    // chunk ahead of their use, a third of them in each phase), then
-    // multiplies.
-    const int chunks = (sq.len + kC - 1) / kC;
     if (chunks > 0) {
-        load_kq(0);
-        load_tv(0);
+        load_rows(keys->k, kf);
+        load_v(0);
+        load_frags(data->t, tf);
+        load_kt(0);
     }
     lds_barrier();
     for (int c = 0; c < chunks; ++c) {
         const int next = min(c + 1, chunks - 1);
-        // ---- R of 16 tokens (and Q S)
-        f32x4 ks[G] = {}, qs[G] = {}, uu[G];
-        float wl[4];
-        load_yk(c);
+        // ---- R of 16 tokens
+        f32x4 uu[G];
+        s_vec[wave][l] = vec1;
+        float4 vec[4];
 #pragma unroll
-        for (int j = 0; j < J; ++j)
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-                const Raw8 b = read(s_s[g], j);
-                M::mul(kf[j], qf[j], b, ks[g], qs[g]);
-            }
+        for (int r = 0; r < 4; ++r)
+            vec[r] = reinterpret_cast<const float4 *>(s_vec[wave])[4 * qd + r];
+        groups(s_s, [&](int g, const Raw8 *b) { uu[g] = times_state(kf, b); });
+        load_rows(keys[next].k, kf);
 #pragma unroll
         for (int g = 0; g < G; ++g) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                uu[g][r] = vec[r].x * M::widen(vv[g][r]) - vec[r].y * ks[g][r];
-                qs[g][r] *= vec[r].z;
-            }
+            for (int r = 0; r < 4; ++r)
+                uu[g][r] = vec[r].x * M::widen(vv[g][r]) - vec[r].y * uu[g][r];
             M::put_tile(s_r[g], w >> 1, w & 1, l, uu[g]);
         }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) wl[r] = vec[r].w;
+        load_v(next);
         lds_barrier();
 
         // ---- U = R + (T - I) R, W
-        load_kq(next);
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-            f32x4 more = {};
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                if (j <= w >> 1) M::mul2(tf[j], read(s_r[g], j), uu[g], more);
-            uu[g] += more;
+        groups(s_r, [&](int g, const Raw8 *b) {
+            uu[g] = times_lower(tf, b, uu[g]);
+            if (g == G - 1) load_frags(data[next].t, tf);
             f32x4 wv;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) wv[r] = wl[r] * uu[g][r];
+            for (int r = 0; r < 4; ++r) wv[r] = vec[r].w * uu[g][r];
             M::put_tile(s_w[g], w >> 1, w & 1, l, wv);
             M::put_tile(s_u[g], w >> 1, w & 1, l, uu[g]);
-        }
+        });
         lds_barrier();
 
-        // ---- S <- e^{g_l} S + K^T W, O = e^g Q S + Y U
-        load_tv(next);
+        // ---- S <- e^{g_l} S + K^T W
         if (w < J) {
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
+            groups(s_w, [&](int g, const Raw8 *b) {
                 st[g][0] *= egl;
                 st[g][1] *= egl;
 #pragma unroll
                 for (int jt = 0; jt < 2; ++jt)
-                    M::mul(kt[0][jt], kt[1][jt], read(s_w[g], jt), st[g][0], st[g][1]);
-            }
-            put_state();
+                    M::mul(kt[0][jt], kt[1][jt], b[jt], b[jt], st[g][0], st[g][1]);
+                M::put_tile(s_s[g], w, 0, l, st[g][0]);
+                M::put_tile(s_s[g], w, 1, l, st[g][1]);
+            });
         }
-        const __amdgpu_buffer_rsrc_t ro = rsrc(op, ostride, a.dv, sizeof(OT), c);
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-            f32x4 more = {};
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                if (j <= w >> 1) M::mul2(yf[j], read(s_u[g], j), qs[g], more);
-            qs[g] += more;
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                store1(ro, bytes(voff[g], r, sizeof(OT)), qs[g][r], OT{});
-        }
+        load_kt(next);
         lds_barrier();
     }
     if (slive) {
@@ -708,23 +817,26 @@ int64_t up256(int64_t x) { return (x + 255) & ~(int64_t)255; }
 Layout layout(const RuleArgs &a) {
     Layout y;
     const int DK = a.dk > 64 ? 128 : 64;
-    const int64_t kt = (int64_t)(DK / 16) * 2 * 64 * 16 * (a.dtype == GDN_DTYPE_BF16 ? 1 : 2);
+    const int64_t keys = 3LL * kC * DK * (a.dtype == GDN_DTYPE_BF16 ? 2 : 4);
     y.slots = a.rows / kC + a.batch;      // every sequence may end in a partial chunk
     y.off_pre = 0;
     y.off_order = up256(4LL * a.batch);
-    y.off_seq = y.off_order + up256(4LL * a.batch);
-    y.off_kt = y.off_seq + up256(4LL * y.slots);
-    y.off_data = y.off_kt + kt * y.slots * a.Hk;
+    y.off_slot = y.off_order + up256(4LL * a.batch);
+    y.off_keys = y.off_slot + up256(16LL * y.slots);
+    y.off_data = y.off_keys + keys * y.slots * a.Hk;
     const int64_t data = a.dtype == GDN_DTYPE_BF16 ? sizeof(ChunkData<Half>)
                                                    : sizeof(ChunkData<Full>);
     y.bytes = y.off_data + data * y.slots * a.H;
     return y;
 }
 
-// Two column groups a wave load the chunk's operands once for 32 columns; one
-// group gives twice the workgroups.
+// Four column groups a wave load a chunk's operands once for 64 columns; one
+// group gives four times the workgroups.  Sixteen prompts of 1 to 2049 tokens,
+// 32 heads: scan 205 us with four groups, 284 us with one.  One prompt of 8192
+// tokens has 64 workgroups of four groups, whose chunks take 3.2 us against
+// 2.0 us: one group there.
 bool wide_scan(const RuleArgs &a) {
-    const long long wide = (long long)a.batch * a.H * ((a.dv + 2 * kCols - 1) / (2 * kCols));
+    const long long wide = (long long)a.batch * a.H * ((a.dv + 4 * kCols - 1) / (4 * kCols));
     return wide >= device_cu_count();
 }
 
@@ -732,7 +844,7 @@ template <typename M, int DK, typename OT, int G>
 hipError_t launch_scan(const RuleArgs &a, const Layout &y, hipStream_t s) {
     const int tiles = (a.dv + kCols * G - 1) / (kCols * G);
     hipLaunchKernelGGL((prefill_scan_kernel<M, DK, OT, G>),
-                       dim3((unsigned)a.batch * a.H * tiles), dim3(kThreads), 0, s, a, y, tiles);
+                       dim3((unsigned)a.batch * a.H * tiles), dim3(kScanThreads), 0, s, a, y, tiles);
     return hipGetLastError();
 }
 
@@ -747,8 +859,8 @@ hipError_t launch(const RuleArgs &a, hipStream_t s) {
     e = hipGetLastError();
     if (e != hipSuccess) return e;
     const bool half = a.out_dtype == GDN_DTYPE_BF16;
-    if (wide_scan(a)) return half ? launch_scan<M, DK, uint16_t, 2>(a, y, s)
-                                  : launch_scan<M, DK, float, 2>(a, y, s);
+    if (wide_scan(a)) return half ? launch_scan<M, DK, uint16_t, 4>(a, y, s)
+                                  : launch_scan<M, DK, float, 4>(a, y, s);
     return half ? launch_scan<M, DK, uint16_t, 1>(a, y, s) : launch_scan<M, DK, float, 1>(a, y, s);
 }
 
