@@ -165,6 +165,25 @@ def _torch():
     return _torch_module
 
 
+_native_module = None
+
+
+def _native():
+    """csrc/binding.cpp: argument checks and calls of the serving operators"""
+    global _native_module
+    if _native_module is None:
+        load()
+        _torch()
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise RuntimeError("the binding's native part cannot be loaded; run "
+                               "gated_deltanet_tree_verify_amd.build()") from e
+        _binding.explain(_explain)
+        _native_module = _binding
+    return _native_module
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -172,7 +191,7 @@ def _ptr(t):
 def _stream(stream):
     torch = _torch()
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -209,21 +228,27 @@ def _issue(name, fn, args, keep, result, prepare):
     return result
 
 
-def _need(t, name, dtypes, shape=None):
+def _explain(t, name, dtypes, shape=None):
+    """raises what is wrong with an argument"""
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if (t.is_cuda and t.dtype in dtypes and t.is_contiguous()
-            and (shape is None or t.shape == shape)):
-        return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if tuple(t.shape) != tuple(shape):
+    if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _need(t, name, dtypes, shape=None):
+    """a contiguous GPU tensor of one of the dtypes, of this shape if given;
+    from the first call on this name is the native check itself"""
+    global _need
+    _need = _native().need
+    _need(t, name, dtypes, shape)
 
 
 def _qkv_dtype(q):
@@ -457,21 +482,20 @@ def _workspace_bytes(name, *sizes):
     return max(16, int(getattr(load(), name)(*sizes)))
 
 
-def _workspace(nbytes, device, stream):
-    """Device memory for one call, from torch's allocator: ordered on the
-    current stream, and kept until `stream` is done with it when that is
-    another one."""
+def _empty(shape, dtype, device, stream):
+    """Device memory from torch's allocator, ordered on the current stream:
+    where the call runs on another one, that waits for whatever may have used
+    the block just before, and keeps the block until it is done with it."""
     torch = _torch()
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    t = torch.empty(shape, dtype=dtype, device=device)
     if stream is not None:
         other = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
-        # the block may have been used on the current stream just before
         other.wait_stream(torch.cuda.current_stream(device))
-        ws.record_stream(other)
-    return ws
+        t.record_stream(other)
+    return t
 
 
-def _rule_shapes(q, k, v, alpha, beta, S, src, dst, out, batch, status):
+def _rule_shapes(q, k, v, alpha, beta, S, src, dst, out, batch, status, stream):
     torch = _torch()
     _need(q, "q", (torch.bfloat16, torch.float32))
     if q.dim() != 3:
@@ -490,7 +514,7 @@ def _rule_shapes(q, k, v, alpha, beta, S, src, dst, out, batch, status):
     _need(src, "src", (torch.int32,), (batch,))
     _need(dst, "dst", (torch.int32,), (batch,))
     if out is None:
-        out = torch.empty((rows, H, dv), dtype=q.dtype, device=q.device)
+        out = _empty((rows, H, dv), q.dtype, q.device, stream)
     _need(out, "out", (torch.bfloat16, torch.float32), (rows, H, dv))
     if status is not None:
         _need(status, "status", (torch.int32,), (batch,))
@@ -510,35 +534,36 @@ def prefill(q, k, v, alpha, beta, cu, S, src, dst, out=None, status=None, stream
     one is allocated when None.  prepare=True returns a Launch.
     """
     torch = _torch()
-    lib = load()
+    native = _native()
     _need(cu, "cu", (torch.int32,))
     if cu.dim() != 1 or cu.shape[0] < 2:
         raise ValueError("cu must be [batch + 1]")
     batch = cu.shape[0] - 1
-    rows, Hk, dk, H, dv, out = _rule_shapes(q, k, v, alpha, beta, S, src, dst, out, batch, status)
+    rows, Hk, dk, H, dv, out = _rule_shapes(q, k, v, alpha, beta, S, src, dst, out, batch, status,
+                                        stream)
     dt = _qkv_dtype(q)
     need = _workspace_bytes("gdn_prefill_workspace", dt, batch, rows, H, Hk, dk, dv)
     if workspace is None:
-        workspace = _workspace(need, q.device, stream)
+        workspace = _empty(need, torch.uint8, q.device, stream)
     else:
         _need(workspace, "workspace", (torch.uint8,))
-    args = (_ptr(q), _ptr(k), _ptr(v), dt, _ptr(alpha), _ptr(beta), _ptr(cu), _ptr(S), _ptr(src),
-            _ptr(dst), _ptr(out), _qkv_dtype(out), batch, rows, S.shape[0], H, Hk, dk, dv,
-            _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream))
-    return _issue("gdn_prefill", lib.gdn_prefill, args,
+    args = (q, k, v, dt, alpha, beta, cu, S, src,
+            dst, out, _qkv_dtype(out), batch, rows, S.shape[0], H, Hk, dk, dv,
+            workspace, workspace.numel(), status, _stream(stream))
+    return _issue("gdn_prefill", native.gdn_prefill, args,
                   (q, k, v, alpha, beta, cu, S, src, dst, out, workspace, status), out, prepare)
 
 
 def step(q, k, v, alpha, beta, S, src, dst, out=None, status=None, stream=None, prepare=False):
     """gdn_step: one token for every sequence (row i: sequence i); arguments
     as for prefill without cu.  Returns out; S is updated in place."""
-    lib = load()
+    native = _native()
     rows, Hk, dk, H, dv, out = _rule_shapes(q, k, v, alpha, beta, S, src, dst, out, q.shape[0],
-                                            status)
-    args = (_ptr(q), _ptr(k), _ptr(v), _qkv_dtype(q), _ptr(alpha), _ptr(beta), _ptr(S), _ptr(src),
-            _ptr(dst), _ptr(out), _qkv_dtype(out), rows, S.shape[0], H, Hk, dk, dv, _ptr(status),
+                                            status, stream)
+    args = (q, k, v, _qkv_dtype(q), alpha, beta, S, src,
+            dst, out, _qkv_dtype(out), rows, S.shape[0], H, Hk, dk, dv, status,
             _stream(stream))
-    return _issue("gdn_step", lib.gdn_step, args,
+    return _issue("gdn_step", native.gdn_step, args,
                   (q, k, v, alpha, beta, S, src, dst, out, status), out, prepare)
 
 
@@ -573,7 +598,7 @@ def tree_attention(q, k, v, parent, k_cache, v_cache, pages, length, scale, shar
     all of them.  Returns out [batch][n][Hq][d].  prepare=True: a Launch.
     """
     torch = _torch()
-    lib = load()
+    native = _native()
     _need(q, "q", (torch.bfloat16, torch.float16))
     if q.dim() != 4:
         raise ValueError("q must be [batch][n][Hq][d]")
@@ -601,7 +626,7 @@ def tree_attention(q, k, v, parent, k_cache, v_cache, pages, length, scale, shar
         _need(tokens, "shared tokens", (torch.int32,), (groups,))
         _need(start, "group starts", (torch.int32,), (groups + 1,))
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream)
     _need(out, "out", (q.dtype,), q.shape)
     if status is not None:
         _need(status, "status", (torch.int32,), (batch,))
@@ -609,14 +634,14 @@ def tree_attention(q, k, v, parent, k_cache, v_cache, pages, length, scale, shar
     need = _workspace_bytes("gdn_tree_attention_workspace", batch, n, Hq, Hkv, d, page, width,
                             groups)
     if workspace is None:
-        workspace = _workspace(need, q.device, stream)
+        workspace = _empty(need, torch.uint8, q.device, stream)
     else:
         _need(workspace, "workspace", (torch.uint8,))
-    args = (_ptr(q), _ptr(k), _ptr(v), DTYPE_BF16 if q.dtype == torch.bfloat16 else DTYPE_F16,
-            _ptr(parent), _ptr(k_cache), _ptr(v_cache), stride, _ptr(pages), _ptr(length),
-            _ptr(start), _ptr(tokens), groups, float(scale), _ptr(out), batch, n, Hq, Hkv, d, page,
-            num, width, _ptr(workspace), workspace.numel(), _ptr(status), _stream(stream))
-    return _issue("gdn_tree_attention", lib.gdn_tree_attention, args,
+    args = (q, k, v, DTYPE_BF16 if q.dtype == torch.bfloat16 else DTYPE_F16,
+            parent, k_cache, v_cache, stride, pages, length,
+            start, tokens, groups, float(scale), out, batch, n, Hq, Hkv, d, page,
+            num, width, workspace, workspace.numel(), status, _stream(stream))
+    return _issue("gdn_tree_attention", native.gdn_tree_attention, args,
                   (q, k, v, parent, k_cache, v_cache, pages, length, start, tokens, out, workspace,
                    status), out, prepare)
 
@@ -639,19 +664,19 @@ def page_fork(table, length, ref, src, dst, page, copies=None, status=None, stre
     of the page table; returns copies int32 [m][2], the partial pages that
     page_copy has to move ({-1, -1}: none)."""
     torch = _torch()
-    lib = load()
+    native = _native()
     seqs, width, pool = _need_table(table, length, ref)
     _need(src, "src", (torch.int32,))
     m = src.numel()
     _need(dst, "dst", (torch.int32,), src.shape)
     if copies is None:
-        copies = torch.empty((m, 2), dtype=torch.int32, device=table.device)
+        copies = _empty((m, 2), torch.int32, table.device, stream)
     _need(copies, "copies", (torch.int32,), (m, 2))
     if status is not None:
         _need(status, "status", (torch.int32,), (m,))
-    args = (_ptr(table), _ptr(length), _ptr(ref), _ptr(src), _ptr(dst), _ptr(copies), m, seqs,
-            width, pool, int(page), _ptr(status), _stream(stream))
-    return _issue("gdn_page_fork", lib.gdn_page_fork, args,
+    args = (table, length, ref, src, dst, copies, m, seqs,
+            width, pool, int(page), status, _stream(stream))
+    return _issue("gdn_page_fork", native.gdn_page_fork, args,
                   (table, length, ref, src, dst, copies, status), copies, prepare)
 
 
@@ -660,33 +685,33 @@ def page_extend(table, length, ref, dst, add, page, begin=None, status=None, str
     """gdn_page_extend: room for add[r] more tokens in row dst[r]; returns
     begin int32 [m], the lengths before (-1: not enough free pages)."""
     torch = _torch()
-    lib = load()
+    native = _native()
     seqs, width, pool = _need_table(table, length, ref)
     _need(dst, "dst", (torch.int32,))
     m = dst.numel()
     _need(add, "add", (torch.int32,), dst.shape)
     if begin is None:
-        begin = torch.empty_like(dst)
+        begin = _empty(dst.shape, torch.int32, dst.device, stream)
     _need(begin, "begin", (torch.int32,), dst.shape)
     if status is not None:
         _need(status, "status", (torch.int32,), (m,))
-    args = (_ptr(table), _ptr(length), _ptr(ref), _ptr(dst), _ptr(add), _ptr(begin), m, seqs,
-            width, pool, int(page), _ptr(status), _stream(stream))
-    return _issue("gdn_page_extend", lib.gdn_page_extend, args,
+    args = (table, length, ref, dst, add, begin, m, seqs,
+            width, pool, int(page), status, _stream(stream))
+    return _issue("gdn_page_extend", native.gdn_page_extend, args,
                   (table, length, ref, dst, add, begin, status), begin, prepare)
 
 
 def page_free(table, length, ref, done, page, status=None, stream=None, prepare=False):
     """gdn_page_free: the rows `done` give their pages back and become empty."""
     torch = _torch()
-    lib = load()
+    native = _native()
     seqs, width, pool = _need_table(table, length, ref)
     _need(done, "done", (torch.int32,))
     if status is not None:
         _need(status, "status", (torch.int32,), (done.numel(),))
-    args = (_ptr(table), _ptr(length), _ptr(ref), _ptr(done), done.numel(), seqs, width, pool,
-            int(page), _ptr(status), _stream(stream))
-    return _issue("gdn_page_free", lib.gdn_page_free, args, (table, length, ref, done, status),
+    args = (table, length, ref, done, done.numel(), seqs, width, pool,
+            int(page), status, _stream(stream))
+    return _issue("gdn_page_free", native.gdn_page_free, args, (table, length, ref, done, status),
                   None, prepare)
 
 
@@ -696,22 +721,22 @@ def page_compact(table, length, ref, page, copies=None, count=None, workspace=No
     follow); returns (copies int32 [pool // 2][2], count int32 []): what
     page_copy has to move."""
     torch = _torch()
-    lib = load()
+    native = _native()
     seqs, width, pool = _need_table(table, length, ref)
     if copies is None:
-        copies = torch.empty((pool // 2, 2), dtype=torch.int32, device=table.device)
+        copies = _empty((pool // 2, 2), torch.int32, table.device, stream)
     _need(copies, "copies", (torch.int32,), (pool // 2, 2))
     if count is None:
-        count = torch.empty((), dtype=torch.int32, device=table.device)
+        count = _empty((), torch.int32, table.device, stream)
     _need(count, "count", (torch.int32,), ())
     if workspace is None:
-        workspace = _workspace(4 * pool, table.device, stream)
+        workspace = _empty(4 * pool, torch.uint8, table.device, stream)
     _need(workspace, "workspace", (torch.uint8,))
     if workspace.numel() < 4 * pool:
         raise ValueError("workspace must hold 4 bytes for every page of the pool")
-    args = (_ptr(table), _ptr(length), _ptr(ref), _ptr(copies), _ptr(count), _ptr(workspace), seqs,
+    args = (table, length, ref, copies, count, workspace, seqs,
             width, pool, int(page), _stream(stream))
-    return _issue("gdn_page_compact", lib.gdn_page_compact, args,
+    return _issue("gdn_page_compact", native.gdn_page_compact, args,
                   (table, length, ref, copies, count, workspace), (copies, count), prepare)
 
 
@@ -719,7 +744,7 @@ def page_copy(cache, copies, count=None, stream=None, prepare=False):
     """gdn_page_copy: cache [planes][pool][...], page `to` <- page `from` in
     every plane for the first count (default: all) of copies [m][2]."""
     torch = _torch()
-    lib = load()
+    native = _native()
     _need(cache, "cache", (torch.bfloat16, torch.float16, torch.float32, torch.uint8))
     if cache.dim() < 3:
         raise ValueError("cache must be [planes][pool][...]")
@@ -732,9 +757,9 @@ def page_copy(cache, copies, count=None, stream=None, prepare=False):
             raise ValueError("count must hold one number")
     planes, pool = cache.shape[0], cache.shape[1]
     nbytes = cache.stride(1) * cache.element_size()
-    args = (_ptr(cache), _ptr(copies), _ptr(count), copies.shape[0], planes, pool, nbytes,
+    args = (cache, copies, count, copies.shape[0], planes, pool, nbytes,
             _stream(stream))
-    return _issue("gdn_page_copy", lib.gdn_page_copy, args, (cache, copies, count), cache, prepare)
+    return _issue("gdn_page_copy", native.gdn_page_copy, args, (cache, copies, count), cache, prepare)
 
 
 def kv_commit(k_cache, v_cache, table, dst, begin, k, v, path, add, status=None, stream=None,
@@ -743,7 +768,7 @@ def kv_commit(k_cache, v_cache, table, dst, begin, k, v, path, add, status=None,
     path[r][: add[r]] of k, v [m][n][Hkv][d]) become tokens begin[r] .. of the
     table's rows dst[r]."""
     torch = _torch()
-    lib = load()
+    native = _native()
     kinds = (torch.bfloat16, torch.float16, torch.float32)
     _need(k, "k", kinds)
     if k.dim() != 4:
@@ -765,8 +790,8 @@ def kv_commit(k_cache, v_cache, table, dst, begin, k, v, path, add, status=None,
         raise ValueError("path must be [m][max_path]")
     if status is not None:
         _need(status, "status", (torch.int32,), (m,))
-    args = (_ptr(k_cache), _ptr(v_cache), stride, _ptr(table), _ptr(dst), _ptr(begin), _ptr(k),
-            _ptr(v), _ptr(path), _ptr(add), m, n, path.shape[1], Hkv, d, k.element_size(),
-            table.shape[0], table.shape[1], num, page, _ptr(status), _stream(stream))
-    return _issue("gdn_kv_commit", lib.gdn_kv_commit, args,
+    args = (k_cache, v_cache, stride, table, dst, begin, k,
+            v, path, add, m, n, path.shape[1], Hkv, d, k.element_size(),
+            table.shape[0], table.shape[1], num, page, status, _stream(stream))
+    return _issue("gdn_kv_commit", native.gdn_kv_commit, args,
                   (k_cache, v_cache, table, dst, begin, k, v, path, add, status), None, prepare)

@@ -1,4 +1,5 @@
-"""Compile libgdntree.so (HIP, gfx950) in-tree with hipcc.
+"""Compile libgdntree.so (HIP, gfx950) in-tree with hipcc, and the binding's
+native part, _binding.so, with the host compiler.
 
 Usage: python -m gated_deltanet_tree_verify_amd._build
 """
@@ -14,6 +15,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgdntree.so")
+BINDING = os.path.join(PKG, "_binding.so")
 ARCH = "gfx950"
 
 # Packed fp32 vector ops are kept off: hipcc would otherwise fuse scalar fp32
@@ -46,7 +48,32 @@ def build(verbose: bool = False) -> str:
     if verbose and err.strip():
         print(err, file=sys.stderr)
     os.replace(tmp, LIB)
+    build_binding(verbose)
     return LIB
+
+
+def build_binding(verbose: bool = False) -> str:
+    """_binding.so: needs torch's headers, and libgdntree.so beside it."""
+    import sysconfig
+    from torch.utils import cpp_extension
+    import torch
+    lib_dir = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI),
+           "-I", INCLUDE, "-isystem", sysconfig.get_paths()["include"]]
+    for d in cpp_extension.include_paths():
+        cmd += ["-isystem", d]
+    cmd += [os.path.join(CSRC, "binding.cpp"), "-o", tmp, "-L", PKG, "-l:" + os.path.basename(LIB),
+            "-L", lib_dir, "-ltorch_python",
+            "-ltorch", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed ({res.returncode}):\n{res.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 if __name__ == "__main__":

@@ -161,3 +161,32 @@ def test_binding_refuses_what_the_gpu_calls_cannot_take():
     with pytest.raises(ValueError, match="GPU tensor"):
         g.kv_commit(h(8, 1, 16, 64), h(8, 1, 16, 64), i(4, 4), i(1), i(1), h(1, 1, 1, 64),
                     h(1, 1, 1, 64), i(1, 1), i(1))
+
+
+def test_native_calls_check_their_arguments():
+    pytest.importorskip("torch")
+    native = g._native()
+    ok = (FAKE, FAKE, FAKE, FAKE, 0, 4, 4, 8, 16, None, None)
+    assert native.gdn_page_free(*ok) == 0              # no rows: nothing launched
+    assert native.gdn_page_free(None, *ok[1:]) == -1
+    with pytest.raises(TypeError):
+        native.gdn_page_free(*ok[:-1])
+    with pytest.raises(TypeError):
+        native.gdn_page_free("table", *ok[1:])
+    with pytest.raises(TypeError):
+        native.gdn_page_free(*ok[:4], 1.5, *ok[5:])
+    for big in (1 << 31, -(1 << 31) - 1, 1 << 70):
+        with pytest.raises(OverflowError):
+            native.gdn_page_free(*ok[:4], big, *ok[5:])
+
+
+def test_native_check_says_what_is_wrong():
+    torch = pytest.importorskip("torch")
+    need = g._native().need
+    x = torch.zeros(2, 3)
+    with pytest.raises(ValueError, match="x must be a GPU tensor"):
+        need(x, "x", (torch.float32,), (2, 3))
+    with pytest.raises(TypeError, match="x must be a torch.Tensor"):
+        need([0.0], "x", (torch.float32,))
+    with pytest.raises(TypeError):
+        need(x, "x")
