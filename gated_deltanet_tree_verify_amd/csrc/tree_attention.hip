@@ -359,7 +359,6 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
     __shared__ Smem sm;
 
     const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
-    const int m = l & 31, h = l >> 5;
     // consecutive workgroups of the line share keys: give each XCD (block
     // index modulo 8) a run of them
     const int grid = gridDim.x;
@@ -732,7 +731,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
                     ls += p[r];
                 }
                 // weights rounded to the operand type: half a step each
-                // (2^-9 or 2^-12 of a weight), independent over the keys
+                // (2^-8 or 2^-11 of a weight at most), independent over the keys
                 const vec p0 = E::round8(p), p1 = E::round8(p + 8);
                 auto times = [&](const uint32_t *y, f32x16 o) {
                     o = E::mma(__builtin_bit_cast(vec, make_uint4(y[0], y[1], y[2], y[3])), p0, o);
@@ -838,71 +837,56 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttentionArgs a, Layout 
     __shared__ int s_fault;
     const int b = blockIdx.x / parts, part = blockIdx.x % parts, tid = threadIdx.x;
     const char *ws = static_cast<const char *>(a.workspace);
-    const Plan *plan = reinterpret_cast<const Plan *>(ws);
-    const int g = reinterpret_cast<const int *>(ws + lay.off_group)[b];
     const int heads = a.Hq / a.Hkv;
-
-    // ---- the sequence's own faults
-    if (tid == 0) s_fault = g == -2 ? kFaultBadGroup : 0;
-    __syncthreads();
+    // what does not depend on another load first: each round trip to memory
+    // is a tenth of a single token's time
+    const int g = reinterpret_cast<const int *>(ws + lay.off_group)[b];
+    const long long c = reinterpret_cast<const Plan *>(ws)->per_wg;
+    const long long own0 = reinterpret_cast<const long long *>(ws + lay.off_bpre)[b];
     const int raw = a.length[b];
+    if (tid == 0) s_fault = g == -2 ? kFaultBadGroup : 0;
     int fault = 0;
     const bool len_ok = raw >= 0 && raw <= a.max_pages << a.page_log;
     if (!len_ok) fault = kFaultBadLength;
     const int len = len_ok ? raw : 0;
     for (int i = tid; i < a.n; i += kThreads)
         if (!parent_ok(a.parent[(size_t)b * a.n + i], i)) fault |= kFaultBadParent;
-    const int32_t *row = a.pages + (size_t)b * a.max_pages;
-    const int used = (int)(((long long)len + (1 << a.page_log) - 1) >> a.page_log);
     const int gs = g >= 0 ? a.gstart[g] : b;
     const int members = g >= 0 ? a.gstart[g + 1] - gs : 1;
-    const int said = g >= 0 ? min(len, max(0, a.gshared[g])) : 0;
-    const int same = (int)(((long long)said + (1 << a.page_log) - 1) >> a.page_log);
-    for (int c = tid; c < used; c += kThreads) {
-        const int p = row[c];
-        if (p < 0 || p >= a.num_pages) fault |= kFaultBadPage;
-        if (c < same && p != a.pages[(size_t)gs * a.max_pages + c]) fault |= kFaultBadGroup;
-    }
-    if (g >= 0 && a.gshared[g] < 0) fault |= kFaultBadGroup;
-    if (fault) atomicOr(&s_fault, fault);
-    __syncthreads();
-    fault = s_fault;
-    if (a.status && part == 0 && tid == 0) a.status[b] = fault;
+    const int said = g >= 0 ? a.gshared[g] : 0;
+    const int sh = g < 0 ? 0 : fit_shared(a, members, said);
+    const long long shared0 = g < 0 ? 0 : reinterpret_cast<const long long *>(ws + lay.off_gpre)[g];
 
+    // ---- the row's partials.  What the first kernel did with lengths that
+    // do not fit is done here: there are as many partials as are counted, and
+    // a fault found below only replaces the result.
     const int lr = part * kPer + tid / kLanes, d0 = 4 * (tid % kLanes);
-    if (lr >= a.n * a.Hq || d0 >= a.d) return;
-    const size_t qrow = (size_t)b * a.n * a.Hq + lr;
-    uint16_t *out = static_cast<uint16_t *>(a.out) + qrow * a.d + d0;
+    const bool live = lr < a.n * a.Hq && d0 < a.d;
+    const int hq = lr % a.Hq, node = min(lr / a.Hq, a.n - 1), hk = hq / heads;
+    const size_t qrow = (size_t)b * a.n * a.Hq + (live ? lr : 0);
+    // the unit's first tile on the line and its tiles: its partials are one
+    // per workgroup between
+    auto partials = [&](long long start, int rows, int keys, int r) {
+        Entry x;
+        x.rows = rows;
+        x.keys = keys;
+        shape(x);
+        const long long first =
+            start + ((long long)hk * x.row_tiles + r / kRows) * unit_length(x) + x.weight * kUnit;
+        return (int)((first + x.weight * (x.tiles - 1)) / c - first / c) + 1;
+    };
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float inv;
-    if (fault) {
-        inv = __builtin_nanf("");
-    } else {
-        const int hq = lr % a.Hq, node = lr / a.Hq, hk = hq / heads;
-        const long long c = plan->per_wg;
-        const long long *gpre = reinterpret_cast<const long long *>(ws + lay.off_gpre);
-        const long long *bpre = reinterpret_cast<const long long *>(ws + lay.off_bpre);
-        const int sh = g < 0 ? 0 : fit_shared(a, members, a.gshared[g]);
-        // the unit's first tile on the line and its tiles: its partials are
-        // one per workgroup between
-        auto partials = [&](long long start, int rows, int keys, int r) {
-            Entry x;
-            x.rows = rows;
-            x.keys = keys;
-            shape(x);
-            const long long first =
-                start + ((long long)hk * x.row_tiles + r / kRows) * unit_length(x) + x.weight * kUnit;
-            return (int)((first + x.weight * (x.tiles - 1)) / c - first / c) + 1;
-        };
+    float ls = 0.f;
+    bool odd = false;
+    if (live) {
         const int r = node * heads + hq % heads, rows = a.n * heads;
-        const int no = partials(bpre[b], rows, len - min(len, sh) + a.n, r);
-        const int ns = sh > 0 ? partials(gpre[g], members * rows, sh, (b - gs) * rows + r) : 0;
+        const int no = partials(own0, rows, len - min(len, sh) + a.n, r);
+        const int ns = sh > 0 ? partials(shared0, members * rows, sh, (b - gs) * rows + r) : 0;
         const float2 *ml = reinterpret_cast<const float2 *>(ws + lay.off_ml) + qrow;
         const float *o = reinterpret_cast<const float *>(ws + lay.off_o) + qrow * D + d0;
         // eight partials at a time: their loads do not wait for each other
         constexpr int kAtOnce = 8;
-        float mx = -__builtin_inff(), ls = 0.f;
-        bool odd = false;
+        float mx = -__builtin_inff();
         const int count = no + ns;
         for (int i0 = 0; i0 < count; i0 += kAtOnce) {
             float2 p[kAtOnce];
@@ -927,6 +911,31 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttentionArgs a, Layout 
                 mx = mn;
             }
         }
+    }
+
+    // ---- the sequence's pages
+    const int32_t *row = a.pages + (size_t)b * a.max_pages;
+    const int used = (int)(((long long)len + (1 << a.page_log) - 1) >> a.page_log);
+    const int same_tokens = min(len, max(0, said));
+    const int same = (int)(((long long)same_tokens + (1 << a.page_log) - 1) >> a.page_log);
+    for (int c = tid; c < used; c += kThreads) {
+        const int p = row[c];
+        if (p < 0 || p >= a.num_pages) fault |= kFaultBadPage;
+        if (c < same && p != a.pages[(size_t)gs * a.max_pages + c]) fault |= kFaultBadGroup;
+    }
+    if (said < 0) fault |= kFaultBadGroup;
+    __syncthreads();                     // s_fault has its first value
+    if (fault) atomicOr(&s_fault, fault);
+    __syncthreads();
+    fault = s_fault;
+    if (a.status && part == 0 && tid == 0) a.status[b] = fault;
+    if (!live) return;
+
+    uint16_t *out = static_cast<uint16_t *>(a.out) + qrow * a.d + d0;
+    float inv;
+    if (fault) {
+        inv = __builtin_nanf("");
+    } else {
         inv = 1.f / ls;
         if (odd) {
             // The sequence's tiles that not all rows saw whole were computed
