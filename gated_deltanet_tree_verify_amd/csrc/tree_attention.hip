@@ -188,14 +188,28 @@ __device__ __forceinline__ long long line_length(const AttentionArgs &a, const E
     return unit_length(x) * x.row_tiles * a.Hkv;
 }
 
+// Sums and maxima over a wave by lane moves inside the vector unit: row shifts
+// by 1, 2, 4 and 8, then lane 15 of a row of 16 to the next row, lane 31 to the
+// upper half.  (Exchanges through LDS cost a round trip each; a single token's
+// call spends 1 us less on its line this way.)
+template <typename F>
+__device__ __forceinline__ int wave_scan(int x, F op) {
+    x = op(x, __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false));
+    x = op(x, __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false));
+    x = op(x, __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false));
+    x = op(x, __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false));
+    x = op(x, __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false));
+    return op(x, __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false));
+}
+__device__ __forceinline__ int wave_max(int x) {       // of numbers that are not negative
+    return __builtin_amdgcn_readlane(wave_scan(x, [](int a, int b) { return max(a, b); }), 63);
+}
+// 0 <= x < 2^52, in two parts whose sums fit 32 bits
 __device__ __forceinline__ long long wave_inclusive64(long long x) {
-    const int l = threadIdx.x & 63;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const long long up = __shfl_up(x, o);
-        if (l >= o) x += up;
-    }
-    return x;
+    auto add = [](int a, int b) { return (int)((uint32_t)a + (uint32_t)b); };
+    const uint32_t lo = (uint32_t)wave_scan((int)(x & 0x3ffffff), add);
+    const uint32_t hi = (uint32_t)wave_scan((int)(x >> 26), add);
+    return ((long long)hi << 26) + lo;
 }
 
 template <int D>
@@ -399,14 +413,11 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
         else own = max(own, span);
         heavy = max(heavy, x.weight);
     }
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        sum += __shfl_xor(sum, o);
-        own = max(own, __shfl_xor(own, o));
-        shared = max(shared, __shfl_xor(shared, o));
-        heavy = max(heavy, __shfl_xor(heavy, o));
-    }
-    if (l == 0) {
+    sum = wave_inclusive64(sum);
+    own = wave_max(own);
+    shared = wave_max(shared);
+    heavy = wave_max(heavy);
+    if (l == 63) {
         sm.part[w] = sum;
         atomicMax(&sm.max_own, own);
         atomicMax(&sm.max_shared, shared);

@@ -294,6 +294,8 @@ gdn_status gdn_tree_index(const int32_t *parent, int32_t *depth,
  * where src[i] = -1, and leaves its state in slot dst[i].  dst[i] may be
  * src[i]; otherwise the dst slots must be distinct and no other sequence's
  * src.  An empty sequence copies its state.  alpha = 0 clears the state.
+ * A value that is not finite, or a negative alpha, spoils the outputs of its
+ * 64-token chunk and of the later tokens of its own sequence, and the state.
  * Faults, per sequence: GDN_FAULT_BAD_LENGTH (cu not ascending within
  * [0, rows]: nothing of it is written) and GDN_FAULT_BAD_SLOT (src or dst:
  * its out rows are NaN, no state is written).

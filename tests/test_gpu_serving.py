@@ -126,6 +126,63 @@ def test_prefill(gpu_lib, lens, H, Hk, dk, dv, dtype, out):
     assert torch.equal(d["S"].cpu()[untouched], x["S"][untouched])
 
 
+def check_prefill(lib, lens, H, Hk, dk, dv, dtype, out, seed):
+    batch = len(lens)
+    x = rule_inputs(lens, H, Hk, dk, dv, dtype, 2 * batch, seed)
+    src = [i if i % 3 else -1 for i in range(batch)]
+    dst = [batch + i for i in range(batch)]
+    d = {n: t.cuda() for n, t in x.items()}
+    o = torch.full((sum(lens), H, dv), float("nan"), dtype=DT[out], device="cuda")
+    st = ints([-1] * batch)
+    lib.prefill(d["q"], d["k"], d["v"], d["alpha"], d["beta"], d["cu"], d["S"], ints(src),
+                ints(dst), out=o, status=st)
+    torch.cuda.synchronize()
+    assert st.tolist() == [0] * batch
+    ro, rS = rule_ref(x, x["cu"].tolist(), src, dst)
+    near_out(o, ro, "out")
+    near(d["S"], rS, "S")
+    assert torch.equal(d["S"].cpu()[:batch], x["S"][:batch])
+
+
+@pytest.mark.parametrize("H,Hk,dk,dv,dtype,out", [
+    (32, 16, 128, 128, "bf16", "fp32"), (32, 32, 64, 72, "bf16", "bf16"),
+    (32, 8, 128, 40, "fp32", "fp32"), (64, 64, 48, 64, "fp32", "bf16"),
+])
+def test_prefill_many_sequences(gpu_lib, H, Hk, dk, dv, dtype, out):
+    """enough (sequence, head) pairs that a workgroup takes 64 columns"""
+    print("prefill many", H, Hk, dk, dv, dtype, out, flush=True)
+    check_prefill(gpu_lib, [1, 64, 0, 65, 3, 130, 17, 63], H, Hk, dk, dv, dtype, out, 11)
+
+
+@pytest.mark.parametrize("batch", [1023, 1024, 1025, 1100])
+def test_prefill_thousand_sequences(gpu_lib, batch):
+    """around the number of sequences that are ordered by length"""
+    print("prefill", batch, "sequences", flush=True)
+    check_prefill(gpu_lib, [i * 7 % 4 for i in range(batch - 1)] + [70], 1, 1, 8, 8, "fp32",
+                  "fp32", 13)
+
+
+def test_prefill_keeps_values_that_are_not_finite_in_their_sequence(gpu_lib):
+    lens = [70, 200, 40]
+    x = rule_inputs(lens, 2, 1, 64, 64, "bf16", 3, 17)
+    bad = {n: t.clone() for n, t in x.items()}
+    bad["v"][70 + 130, 0, 5] = float("nan")          # chunk 2 of sequence 1, head 0
+    bad["alpha"][70 + 130, 1] = -0.5
+    got = []
+    for y in (x, bad):
+        d = {n: t.cuda() for n, t in y.items()}
+        o = gpu_lib.prefill(d["q"], d["k"], d["v"], d["alpha"], d["beta"], d["cu"], d["S"],
+                            ints([0, 1, 2]), ints([0, 1, 2]),
+                            out=torch.empty(310, 2, 64, device="cuda"))
+        got.append((o.cpu(), d["S"].cpu()))
+    (o, S), (ob, Sb) = got
+    assert torch.equal(ob[:70 + 128], o[:70 + 128]) and torch.equal(ob[270:], o[270:])
+    assert torch.equal(Sb[[0, 2]], S[[0, 2]])
+    assert torch.isnan(ob[200:270, 0, 5]).all() and torch.isnan(ob[200:270, 1]).all()
+    assert torch.equal(ob[198:270, 0, 16:], o[198:270, 0, 16:])      # other columns of the state
+    assert torch.isnan(Sb[1, 0, :, 5]).all() and torch.isnan(Sb[1, 1]).all()
+
+
 def test_prefill_cleared_and_saturated_gates(gpu_lib):
     """alpha = 0 clears the state, alpha = 1 keeps it, beta = 0 writes nothing"""
     lens = [150, 70]
