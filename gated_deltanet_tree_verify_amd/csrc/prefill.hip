@@ -202,7 +202,8 @@ constexpr uint32_t kNowhere = 0x80000000u;
 template <typename M>
 struct ChunkData {
     uint4 t[kFrags][M::kParts][64];      // T - I as operands
-    uint4 y[kFrags][M::kParts][64];      // Y
+    uint4 y[kFrags][2][64];              // Y, 8 fp32 values a lane: the output waves have the
+                                         // time to split them, and a third less is moved
     float4 vec[kC];              // beta, beta e^g, e^g, e^{g_l - g} of the tokens
 };
 
@@ -511,10 +512,15 @@ __global__ __launch_bounds__(kThreads) void prefill_chunk_kernel(RuleArgs a, Lay
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = k0 + e <= tr ? sm.sq.y[tr][k0 + e] : 0.f;
         }
-        const Raw8 x = M::from_f32(v);
-        uint4(*to)[64] = job < kFrags ? out->t[f] : out->y[f];
+        if (job < kFrags) {
+            const Raw8 x = M::from_f32(v);
 #pragma unroll
-        for (int p = 0; p < M::kParts; ++p) to[p][l] = x.p[p];
+            for (int p = 0; p < M::kParts; ++p) out->t[f][p][l] = x.p[p];
+        } else {
+            const Raw8 x = Full::from_f32(v);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) out->y[f][p][l] = x.p[p];
+        }
     }
 }
 
@@ -598,12 +604,13 @@ __global__ __launch_bounds__(kScanThreads, 2) void prefill_scan_kernel(
     // tiles 0 and 1 of a triangle have no second operand: its registers get
     // the first once more (behind a branch, the loads would be waited for
     // where the branch ends)
-    auto load_frags = [&](const uint4(*from)[N][64], Raw8 *to) {
+    auto load_frags = [&](const auto *from, Raw8 *to) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int f = frag_of(w, min(j, w >> 1));
 #pragma unroll
-            for (int n = 0; n < N; ++n) to[j].p[n] = from[f][n][l];
+            for (int n = 0; n < (int)(sizeof(from[0]) / sizeof(from[0][0])); ++n)
+                to[j].p[n] = from[f][n][l];
         }
     };
     auto load_rows = [&](const uint4(*from)[J][M::kExact][64], Raw8 *to) {
@@ -676,6 +683,15 @@ __global__ __launch_bounds__(kScanThreads, 2) void prefill_scan_kernel(
             const int next = min(c + 1, chunks - 1);
             s_vec[wave][l] = vec1;
             vec1 = load_vec(next);
+            Raw8 yx[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                alignas(16) float v[8];
+                *reinterpret_cast<uint4 *>(v) = yf[j].p[0];
+                *reinterpret_cast<uint4 *>(v + 4) = yf[j].p[1];
+                yx[j] = M::from_f32(v);
+            }
+            load_frags(data[next].y, yf);
             lds_barrier();
             f32x4 o[G];
             groups(s_s, [&](int g, const Raw8 *b) { o[g] = times_state(qf, b); });
@@ -688,8 +704,7 @@ __global__ __launch_bounds__(kScanThreads, 2) void prefill_scan_kernel(
             }
             lds_barrier();
             const __amdgpu_buffer_rsrc_t ro = rsrc(op, ostride, a.dv, sizeof(OT), c);
-            groups(s_u, [&](int g, const Raw8 *b) { o[g] = times_lower(yf, b, o[g]); });
-            load_frags(data[next].y, yf);
+            groups(s_u, [&](int g, const Raw8 *b) { o[g] = times_lower(yx, b, o[g]); });
 #pragma unroll
             for (int g = 0; g < G; ++g)
 #pragma unroll
