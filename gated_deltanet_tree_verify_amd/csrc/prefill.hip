@@ -601,16 +601,17 @@ __global__ __launch_bounds__(kScanThreads, 2) void prefill_scan_kernel(
     auto bytes = [&](uint32_t off, int r, uint32_t size) {
         return off == kNowhere ? kNowhere : (off + (uint32_t)(r * ostride)) * size;
     };
-    // tiles 0 and 1 of a triangle have no second operand: its registers get
-    // the first once more (behind a branch, the loads would be waited for
-    // where the branch ends)
-    auto load_frags = [&](const auto *from, Raw8 *to) {
+    // tiles 0 and 1 of a triangle have no second operand: zero, from past the
+    // end (behind a branch, the loads would be waited for where it ends)
+    auto load_frags = [&](const auto &from, Raw8 *to) {
+        constexpr uint32_t kPieces = sizeof(from[0]) / sizeof(from[0][0]);
+        const __amdgpu_buffer_rsrc_t r = tile::make_rsrc(from, sizeof(from));
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const int f = frag_of(w, min(j, w >> 1));
+            const uint32_t at = j <= w >> 1 ? 16u * (kPieces * 64 * frag_of(w, j) + l) : kNowhere;
 #pragma unroll
-            for (int n = 0; n < (int)(sizeof(from[0]) / sizeof(from[0][0])); ++n)
-                to[j].p[n] = from[f][n][l];
+            for (uint32_t n = 0; n < kPieces; ++n)
+                to[j].p[n] = tile::load16<0>(r, at + 1024 * n);
         }
     };
     auto load_rows = [&](const uint4(*from)[J][M::kExact][64], Raw8 *to) {
