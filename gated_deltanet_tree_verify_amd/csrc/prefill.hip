@@ -23,12 +23,15 @@
 //          operands that do not depend on S come from memory into registers,
 //          a chunk ahead.
 //
-// Bound.  The chunk kernel writes 37 KiB a (chunk, head) and is held by
-// latency and that traffic (8192 tokens, 32 heads: 69 us, 2.9 TB/s).  A scan
-// workgroup reads 100 KiB a chunk through its L1: with every chunk read from
-// the same place, so from L2, the scan still takes 9/10 of its time, and the
-// products themselves (60 of 16 cycles a SIMD) are a fifth of it.  A single
-// prompt's chunks follow each other: 128 of them take 128 x 2 us.
+// Bound.  The chunk kernel writes 25 KiB a (chunk, head) and 48 KiB a (chunk,
+// key head) and is held by that traffic (8192 tokens, 32 heads over 16 key
+// heads: 63 us for 333 MB, 5.3 TB/s with its inputs).  A scan workgroup reads
+// 72 KiB of operands a chunk through its L1 besides V: with every chunk read
+// from one place, so from the L2, the scan keeps nine tenths of its time; with
+// loads two chunks ahead all of it; and the products (36 of 16 cycles on a
+// state wave's SIMD, 24 more for the outputs) are a fifth.  What remains is
+// the three exchanges through LDS.  A single prompt's chunks follow each
+// other: 128 of them take 128 x 1.9 us.
 //
 // Operands.  A 16x16 result tile holds row 4 q + r, column m in register r of
 // lane (m = l & 15, q = l >> 4); the matrix instruction takes 8 consecutive
@@ -201,9 +204,9 @@ constexpr uint32_t kNowhere = 0x80000000u;
 // one (chunk, head) of the workspace; a head's chunks follow each other
 template <typename M>
 struct ChunkData {
-    uint4 t[kFrags][M::kParts][64];      // T - I as operands
-    uint4 y[kFrags][2][64];              // Y, 8 fp32 values a lane: the output waves have the
-                                         // time to split them, and a third less is moved
+    // T - I and Y as operands, 8 fp32 values a lane: the scan's output waves
+    // have the time to split them, and a third less is moved
+    uint4 t[kFrags][2][64], y[kFrags][2][64];
     float4 vec[kC];              // beta, beta e^g, e^g, e^{g_l - g} of the tokens
 };
 
@@ -504,7 +507,7 @@ __global__ __launch_bounds__(kThreads) void prefill_chunk_kernel(RuleArgs a, Lay
         const int job = 4 * i + w, f = job % kFrags;
         const int ti = f < 2 ? f : (f + 2) >> 1, j = f < 2 ? 0 : f & 1;
         const int tr = rho(ti, m), k0 = 32 * j + 8 * qd;
-        float v[8];
+        alignas(16) float v[8];
         if (job < kFrags) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = k0 + e < tr ? sm.sq.x[k0 + e][tr] : 0.f;
@@ -512,15 +515,9 @@ __global__ __launch_bounds__(kThreads) void prefill_chunk_kernel(RuleArgs a, Lay
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = k0 + e <= tr ? sm.sq.y[tr][k0 + e] : 0.f;
         }
-        if (job < kFrags) {
-            const Raw8 x = M::from_f32(v);
+        uint4(*to)[64] = job < kFrags ? out->t[f] : out->y[f];
 #pragma unroll
-            for (int p = 0; p < M::kParts; ++p) out->t[f][p][l] = x.p[p];
-        } else {
-            const Raw8 x = Full::from_f32(v);
-#pragma unroll
-            for (int p = 0; p < 2; ++p) out->y[f][p][l] = x.p[p];
-        }
+        for (int p = 0; p < 2; ++p) to[p][l] = reinterpret_cast<const uint4 *>(v)[p];
     }
 }
 
@@ -530,7 +527,7 @@ __global__ __launch_bounds__(kThreads) void prefill_chunk_kernel(RuleArgs a, Lay
 // Eight waves: four carry the state, four form the outputs.  The state waves'
 // products wait for each other, and a wave that waits to issue a load issues
 // no product: the second wave of a SIMD fills these gaps (8192 tokens, 32
-// heads, 16 columns a workgroup: 280 us; all in four waves: 328 us).
+// heads, 16 columns a workgroup, when it was built: 280 us; all in four waves: 328 us).
 constexpr int kScanThreads = 512;
 
 template <typename M, int DK, typename OT, int G>
@@ -541,6 +538,7 @@ __global__ __launch_bounds__(kScanThreads, 2) void prefill_scan_kernel(
     constexpr int N = M::kParts;
     __shared__ __attribute__((aligned(16))) float s_vec[8][64];
     __shared__ uint4 s_s[G][J][N][64], s_r[G][2][N][64], s_u[G][2][N][64], s_w[G][2][N][64];
+    __shared__ uint4 s_t[kFrags][N][64];
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
     const int w = wave & 3;                         // of the four of its role
     const int m = l & 15, qd = l >> 4;
@@ -666,17 +664,25 @@ __global__ __launch_bounds__(kScanThreads, 2) void prefill_scan_kernel(
         return c + more;
     };
 
+    auto split = [&](const Raw8 &x) {
+        alignas(16) float v[8];
+        *reinterpret_cast<uint4 *>(v) = x.p[0];
+        *reinterpret_cast<uint4 *>(v + 4) = x.p[1];
+        return M::from_f32(v);
+    };
+
     // An operand's registers are loaded again, for the next chunk, as soon as
     // they have been used for the last time: a chunk ahead of their next use.
     const int chunks = (sq.len + kC - 1) / kC;
     if (wave >= 4) {
         // ---- outputs: e^g Q S while the state waves form U, Y U while they
         // update S
-        Raw8 qf[J], yf[2];
+        Raw8 qf[J], tf[2], yf[2];
         float vec1 = 0.f;
         if (chunks > 0) {
             load_rows(keys->q, qf);
             vec1 = load_vec(0);
+            load_frags(data->t, tf);
             load_frags(data->y, yf);
         }
         lds_barrier();
@@ -687,11 +693,13 @@ __global__ __launch_bounds__(kScanThreads, 2) void prefill_scan_kernel(
             Raw8 yx[2];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                alignas(16) float v[8];
-                *reinterpret_cast<uint4 *>(v) = yf[j].p[0];
-                *reinterpret_cast<uint4 *>(v + 4) = yf[j].p[1];
-                yx[j] = M::from_f32(v);
+                const Raw8 tx = split(tf[j]);
+                if (j <= w >> 1)
+#pragma unroll
+                    for (int n = 0; n < N; ++n) s_t[frag_of(w, j)][n][l] = tx.p[n];
+                yx[j] = split(yf[j]);
             }
+            load_frags(data[next].t, tf);
             load_frags(data[next].y, yf);
             lds_barrier();
             f32x4 o[G];
@@ -739,7 +747,7 @@ __global__ __launch_bounds__(kScanThreads, 2) void prefill_scan_kernel(
             M::put_tile(s_s[g], w, 1, l, st[g][1]);
         }
 
-    Raw8 kf[J], tf[2], kt[2][2];
+    Raw8 kf[J], kt[2][2];
     float vec1 = 0.f, egl = 0.f;
     uint32_t vv[G][4];
     auto load_v = [&](int c) {
@@ -765,7 +773,6 @@ __global__ __launch_bounds__(kScanThreads, 2) void prefill_scan_kernel(
     if (chunks > 0) {
         load_rows(keys->k, kf);
         load_v(0);
-        load_frags(data->t, tf);
         load_kt(0);
     }
     lds_barrier();
@@ -791,9 +798,9 @@ __global__ __launch_bounds__(kScanThreads, 2) void prefill_scan_kernel(
         lds_barrier();
 
         // ---- U = R + (T - I) R, W
+        const Raw8 tf[2] = {read(s_t, frag_of(w, 0)), read(s_t, frag_of(w, w >> 1))};
         groups(s_r, [&](int g, const Raw8 *b) {
             uu[g] = times_lower(tf, b, uu[g]);
-            if (g == G - 1) load_frags(data[next].t, tf);
             f32x4 wv;
 #pragma unroll
             for (int r = 0; r < 4; ++r) wv[r] = vec[r].w * uu[g][r];
@@ -847,10 +854,14 @@ Layout layout(const RuleArgs &a) {
 }
 
 // Four column groups a wave load a chunk's operands once for 64 columns; one
-// group gives four times the workgroups.  Sixteen prompts of 1 to 2049 tokens,
-// 32 heads: scan 205 us with four groups, 284 us with one.  One prompt of 8192
-// tokens has 64 workgroups of four groups, whose chunks take 3.2 us against
-// 2.0 us: one group there.
+// group gives four times the workgroups.  A chunk takes 3.9 us with four, 1.9
+// us with one, and a compute unit holds one workgroup of either.  32 heads of
+// d_v = 128, whole calls: 1 prompt of 2048 tokens 82 us with one group (152
+// with four), 2 prompts 160 (170), 3 prompts 236 (194), 4 prompts 312 (229);
+// sixteen prompts of 1 to 2049 tokens: scan 199 us with four groups, 323 with
+// one.  Lengths are device data: where one prompt is much longer than the
+// others (4096, 512, 512), one group is better (179, 292), and so four are
+// taken only from as many workgroups as there are compute units.
 bool wide_scan(const RuleArgs &a) {
     const long long wide = (long long)a.batch * a.H * ((a.dv + 4 * kCols - 1) / (4 * kCols));
     return wide >= device_cu_count();
