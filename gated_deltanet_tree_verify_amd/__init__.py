@@ -567,22 +567,30 @@ def step(q, k, v, alpha, beta, S, src, dst, out=None, status=None, stream=None, 
                   (q, k, v, alpha, beta, S, src, dst, out, status), out, prepare)
 
 
-def _need_cache(t, name, dtypes, Hkv, page, d):
-    """A cache [pages][Hkv][page][d] whose pages are contiguous (the stride
-    between pages is free); returns (pages, page stride)."""
+def _need_cache(k_cache, v_cache, dtypes, Hkv, d):
+    """Caches [pages][Hkv][page][d] whose pages are contiguous (the stride
+    between pages is free); returns (pages, page, page stride)."""
+    native = _native()
+    got = native.cache(k_cache, dtypes, Hkv, d)
+    if got is None or native.cache(v_cache, dtypes, Hkv, d) != got:
+        _explain_caches(k_cache, v_cache, dtypes, Hkv, d)
+    return got
+
+
+def _explain_caches(k_cache, v_cache, dtypes, Hkv, d):
     torch = _torch()
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
-    if t.dim() != 4 or t.shape[1] != Hkv or t.shape[3] != d or (page and t.shape[2] != page):
-        raise ValueError(f"{name} must be [pages][{Hkv}][page][{d}]")
-    page = t.shape[2]
-    if t.stride()[1:] != (page * d, d, 1):
-        raise ValueError(f"the pages of {name} must be contiguous")
-    return t.shape[0], t.stride(0) if t.shape[0] > 1 else Hkv * page * d
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a GPU tensor")
+        if t.dtype not in dtypes:
+            raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+        if t.dim() != 4 or t.shape[1] != Hkv or t.shape[3] != d:
+            raise ValueError(f"{name} must be [pages][{Hkv}][page][{d}]")
+        if t.stride()[1:] != (t.shape[2] * d, d, 1):
+            raise ValueError(f"the pages of {name} must be contiguous")
+    raise ValueError("k_cache and v_cache must have the same pages and strides")
 
 
 def tree_attention(q, k, v, parent, k_cache, v_cache, pages, length, scale, shared=None, out=None,
@@ -609,10 +617,7 @@ def tree_attention(q, k, v, parent, k_cache, v_cache, pages, length, scale, shar
     Hkv = k.shape[2]
     _need(v, "v", (q.dtype,), k.shape)
     _need(parent, "parent", (torch.int32,), (batch, n))
-    num, stride = _need_cache(k_cache, "k_cache", (q.dtype,), Hkv, 0, d)
-    page = k_cache.shape[2]
-    if _need_cache(v_cache, "v_cache", (q.dtype,), Hkv, page, d) != (num, stride):
-        raise ValueError("k_cache and v_cache must have the same pages and strides")
+    num, page, stride = _need_cache(k_cache, v_cache, (q.dtype,), Hkv, d)
     _need(pages, "pages", (torch.int32,))
     if pages.dim() != 2 or pages.shape[0] != batch:
         raise ValueError("pages must be [batch][max_pages]")
@@ -775,10 +780,7 @@ def kv_commit(k_cache, v_cache, table, dst, begin, k, v, path, add, status=None,
         raise ValueError("k must be [m][n][Hkv][d]")
     m, n, Hkv, d = k.shape
     _need(v, "v", (k.dtype,), k.shape)
-    num, stride = _need_cache(k_cache, "k_cache", (k.dtype,), Hkv, 0, d)
-    page = k_cache.shape[2]
-    if _need_cache(v_cache, "v_cache", (k.dtype,), Hkv, page, d) != (num, stride):
-        raise ValueError("k_cache and v_cache must have the same pages and strides")
+    num, page, stride = _need_cache(k_cache, v_cache, (k.dtype,), Hkv, d)
     _need(table, "table", (torch.int32,))
     if table.dim() != 2:
         raise ValueError("table must be [seqs][max_pages]")

@@ -7,6 +7,7 @@
 //   need(t, name, dtypes, shape=None)   nothing, if t is a contiguous GPU
 //       tensor of one of the dtypes and of this shape (None: any); otherwise
 //       whatever the function given to explain() raises for the same arguments
+//   cache(t, dtypes, heads, d)   pages, page size and stride of a paged cache
 //   gdn_*(arguments of the C entry point)   its status; a pointer is an int,
 //       None or a tensor
 #define PY_SSIZE_T_CLEAN
@@ -21,17 +22,21 @@ namespace {
 
 PyObject *g_explain = nullptr;
 
+bool known_dtype(const at::Tensor &x, PyObject *dtypes) {
+    for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(dtypes); ++i) {
+        PyObject *d = PyTuple_GET_ITEM(dtypes, i);
+        if (THPDtype_Check(d) &&
+            reinterpret_cast<THPDtype *>(d)->scalar_type == x.scalar_type())
+            return true;
+    }
+    return false;
+}
+
 bool suits(PyObject *t, PyObject *dtypes, PyObject *shape) {
     if (!THPVariable_Check(t) || !PyTuple_Check(dtypes)) return false;
     const at::Tensor &x = THPVariable_Unpack(t);
-    if (!x.is_cuda() || !x.is_contiguous()) return false;
-    bool known = false;
-    for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(dtypes) && !known; ++i) {
-        PyObject *d = PyTuple_GET_ITEM(dtypes, i);
-        known = THPDtype_Check(d) &&
-                reinterpret_cast<THPDtype *>(d)->scalar_type == x.scalar_type();
-    }
-    if (!known || shape == Py_None) return known;
+    if (!x.is_cuda() || !x.is_contiguous() || !known_dtype(x, dtypes)) return false;
+    if (shape == Py_None) return true;
     if (!PyTuple_Check(shape) || PyTuple_GET_SIZE(shape) != x.dim()) return false;
     for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(shape); ++i) {
         const long long n = PyLong_AsLongLong(PyTuple_GET_ITEM(shape, i));
@@ -42,6 +47,26 @@ bool suits(PyObject *t, PyObject *dtypes, PyObject *shape) {
         if (n != x.size(i)) return false;
     }
     return true;
+}
+
+// cache(t, dtypes, heads, d): (pages, tokens a page, elements between pages)
+// of a cache [pages][heads][page][d] on the GPU whose pages are contiguous,
+// or None
+PyObject *cache(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    if (n != 4) {
+        PyErr_SetString(PyExc_TypeError, "cache(t, dtypes, heads, d)");
+        return nullptr;
+    }
+    const long long heads = PyLong_AsLongLong(args[2]), d = PyLong_AsLongLong(args[3]);
+    if (PyErr_Occurred()) return nullptr;
+    if (!THPVariable_Check(args[0]) || !PyTuple_Check(args[1])) Py_RETURN_NONE;
+    const at::Tensor &x = THPVariable_Unpack(args[0]);
+    if (!x.is_cuda() || !known_dtype(x, args[1]) || x.dim() != 4 || x.size(1) != heads ||
+        x.size(3) != d || x.stride(1) != x.size(2) * d || x.stride(2) != d || x.stride(3) != 1)
+        Py_RETURN_NONE;
+    const long long page = x.size(2);
+    return Py_BuildValue("LLL", (long long)x.size(0), page,
+                         x.size(0) > 1 ? (long long)x.stride(0) : heads * page * d);
 }
 
 PyObject *need(PyObject *, PyObject *const *args, Py_ssize_t n) {
@@ -120,6 +145,7 @@ struct Entry<F> {
 
 PyMethodDef g_methods[] = {
     {"need", (PyCFunction)(void (*)(void))need, METH_FASTCALL, nullptr},
+    {"cache", (PyCFunction)(void (*)(void))cache, METH_FASTCALL, nullptr},
     {"explain", explain, METH_O, nullptr},
     ENTRY(gdn_prefill),
     ENTRY(gdn_step),

@@ -116,6 +116,14 @@ struct Requests {
     int len[GDN_MAX_REQUESTS];        // length of the row that is read, before the call
     int16_t fault[GDN_MAX_REQUESTS];
 };
+struct Forks : Requests {
+    int src[GDN_MAX_REQUESTS], dst[GDN_MAX_REQUESTS];
+    int last[GDN_MAX_REQUESTS];       // the page of its own, -1: none
+};
+// Rows that a wave takes at once: their loads do not wait for each other (64
+// forks of 1000 to 2000 tokens: 11 us, one row at a time 14 us; 4 forks: 7.7
+// and 6.4 us, below the host's time for the calls around it).
+constexpr int kRowsAtOnce = 4;
 
 // A row that several requests would write goes to the first of them: each
 // puts r - m < 0 into the row's length with an atomic minimum (lengths are
@@ -136,8 +144,10 @@ __device__ void claim_rows(const PageArgs &a, const int32_t *dst, int m, Request
 __global__ __launch_bounds__(kThreads) void page_fork_kernel(PageArgs a, const int32_t *src,
                                                              const int32_t *dst, int2 *copies,
                                                              int m) {
-    __shared__ Requests q;
-    const int tid = threadIdx.x, page = 1 << a.page_log;
+    __shared__ Forks q;
+    const int tid = threadIdx.x, l = tid & 63, page = 1 << a.page_log;
+    constexpr int kRound = kRowsAtOnce * kWaves;
+    const int r_first = tid >> 6;
 
     // every request by itself: rows, length, the ids it would share
     for (int r = tid; r < m; r += kThreads) {
@@ -150,16 +160,35 @@ __global__ __launch_bounds__(kThreads) void page_fork_kernel(PageArgs a, const i
         }
         q.fault[r] = (int16_t)fault;
         q.len[r] = len;
+        q.src[r] = s;
+        q.dst[r] = d;
+        q.last[r] = -1;
         copies[r] = make_int2(-1, -1);
     }
     __syncthreads();
-    for (int r = tid >> 6; r < m; r += kWaves) {
-        if (q.fault[r]) continue;
-        const int32_t *row = a.table + (size_t)src[r] * a.width;
-        const int used = pages_of(q.len[r], a.page_log);
-        bool bad = false;
-        for (int c = tid & 63; c < used; c += 64) bad |= row[c] < 0 || row[c] >= a.pool;
-        if (__any(bad) && (tid & 63) == 0) q.fault[r] = kFaultBadPage;
+    for (int r0 = r_first; r0 < m; r0 += kRound) {
+        const int32_t *row[kRowsAtOnce];
+        int used[kRowsAtOnce], most = 0;
+        bool bad[kRowsAtOnce];
+#pragma unroll
+        for (int k = 0; k < kRowsAtOnce; ++k) {
+            const int r = r0 + k * kWaves;
+            const bool live = r < m && q.fault[min(r, m - 1)] == 0;
+            row[k] = a.table + (live ? (size_t)q.src[r] * a.width : 0);
+            used[k] = live ? pages_of(q.len[r], a.page_log) : 0;
+            most = max(most, used[k]);
+            bad[k] = false;
+        }
+        for (int c = l; c < most; c += 64) {
+            int p[kRowsAtOnce];
+#pragma unroll
+            for (int k = 0; k < kRowsAtOnce; ++k) p[k] = c < used[k] ? row[k][c] : 0;
+#pragma unroll
+            for (int k = 0; k < kRowsAtOnce; ++k) bad[k] |= p[k] < 0 || p[k] >= a.pool;
+        }
+#pragma unroll
+        for (int k = 0; k < kRowsAtOnce; ++k)
+            if (__any(bad[k]) && l == 0) q.fault[r0 + k * kWaves] = kFaultBadPage;
     }
     claim_rows(a, dst, m, q);
 
@@ -170,36 +199,44 @@ __global__ __launch_bounds__(kThreads) void page_fork_kernel(PageArgs a, const i
     hand_out(a.ref, a.pool, got, q.part, [&](int rank, int p) {
         const int r = owner(q.upto, m, rank);
         const int whole = q.len[r] >> a.page_log;
-        copies[r] = make_int2(a.table[(size_t)src[r] * a.width + whole], p);
+        copies[r] = make_int2(a.table[(size_t)q.src[r] * a.width + whole], p);
+        q.last[r] = p;
         a.ref[p] = 1;
     });
     __syncthreads();
 
-    // the rows: a wave each
-    for (int r = tid >> 6; r < m; r += kWaves) {
-        const int l = tid & 63;
-        int fault = q.fault[r];
-        if (!fault) {
-            const int len = q.len[r], whole = len >> a.page_log;
-            const bool part = (len & (page - 1)) != 0;
-            const bool ok = !part || q.upto[r] <= got;
-            const int32_t *from = a.table + (size_t)src[r] * a.width;
-            int32_t *to = a.table + (size_t)dst[r] * a.width;
-            const int last = part && ok ? copies[r].y : -1;
-            for (int c = l; c < a.width; c += 64) {
-                int p = -1;
-                if (ok && c < whole) {
-                    p = from[c];
-                    atomicAdd(&a.ref[p], 1);
-                } else if (c == whole) {
-                    p = last;
-                }
-                to[c] = p;
+    // the rows
+    for (int r0 = r_first; r0 < m; r0 += kRound) {
+        const int32_t *from[kRowsAtOnce];
+        int32_t *to[kRowsAtOnce];
+        int whole[kRowsAtOnce], last[kRowsAtOnce];
+        bool live[kRowsAtOnce];
+#pragma unroll
+        for (int k = 0; k < kRowsAtOnce; ++k) {
+            const int r = r0 + k * kWaves;
+            live[k] = r < m && q.fault[min(r, m - 1)] == 0;
+            const int len = live[k] ? q.len[r] : 0;
+            const bool ok = live[k] && ((len & (page - 1)) == 0 || q.upto[r] <= got);
+            from[k] = a.table + (live[k] ? (size_t)q.src[r] * a.width : 0);
+            to[k] = a.table + (live[k] ? (size_t)q.dst[r] * a.width : 0);
+            whole[k] = ok ? len >> a.page_log : 0;
+            last[k] = ok ? q.last[r] : -1;
+            if (l == 0 && r < m) {
+                if (live[k]) a.length[q.dst[r]] = ok ? len : 0;
+                if (a.status) a.status[r] = live[k] ? (ok ? 0 : kFaultNoPage) : q.fault[r];
             }
-            if (l == 0) a.length[dst[r]] = ok ? len : 0;
-            if (!ok) fault = kFaultNoPage;
         }
-        if (l == 0 && a.status) a.status[r] = fault;
+        for (int c = l; c < a.width; c += 64) {
+            int p[kRowsAtOnce];
+#pragma unroll
+            for (int k = 0; k < kRowsAtOnce; ++k)
+                p[k] = c < whole[k] ? from[k][c] : c == whole[k] ? last[k] : -1;
+#pragma unroll
+            for (int k = 0; k < kRowsAtOnce; ++k) {
+                if (c < whole[k]) atomicAdd(&a.ref[p[k]], 1);
+                if (live[k]) to[k][c] = p[k];
+            }
+        }
     }
 }
 

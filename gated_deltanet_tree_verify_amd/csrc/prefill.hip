@@ -25,7 +25,7 @@
 //
 // Bound.  The chunk kernel writes 25 KiB a (chunk, head) and 48 KiB a (chunk,
 // key head) and is held by that traffic (8192 tokens, 32 heads over 16 key
-// heads: 63 us for 333 MB, 5.3 TB/s with its inputs).  A scan workgroup reads
+// heads: 63 us for 274 MB with its inputs, 4.3 TB/s).  A scan workgroup reads
 // 72 KiB of operands a chunk through its L1 besides V: with every chunk read
 // from one place, so from the L2, the scan keeps nine tenths of its time; with
 // loads two chunks ahead all of it; and the products (36 of 16 cycles on a
