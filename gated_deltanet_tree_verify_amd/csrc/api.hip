@@ -44,9 +44,12 @@ gdn_status rule_status(const gdn::RuleArgs &a) {
     if (a.H % a.Hk != 0 || !dim_ok(a.dk) || !dim_ok(a.dv)) return GDN_ERR_UNSUPPORTED;
     // a chunk's rows are addressed with 32-bit byte offsets
     if (a.H > 16384) return GDN_ERR_UNSUPPORTED;
-    // grids of (tokens / 64 + batch) * H workgroups and up to 16 per (sequence, head)
-    if (((long long)a.rows / 64 + a.batch) * a.H > 0x7ffffffLL) return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
+}
+
+// threads of a launch are counted in 32 bits
+bool grid_ok(long long workgroups, long long threads) {
+    return workgroups <= 0xffffffffLL / threads;
 }
 
 gdn_status page_status(const gdn::PageArgs &a, int m, int page) {
@@ -268,6 +271,10 @@ gdn_status gdn_prefill(const void *q, const void *k, const void *v, gdn_dtype qk
     if (!cu) return GDN_ERR_INVALID_ARG;
     const gdn_status st = rule_status(a);
     if (st != GDN_OK) return st;
+    // chunks of 64 tokens and heads; sequences, heads and 16 columns
+    if (!grid_ok(((long long)rows / 64 + batch) * H, 256) ||
+        !grid_ok((long long)batch * H * ((d_v + 15) / 16), 512))
+        return GDN_ERR_UNSUPPORTED;
     const int64_t need = gdn::prefill_workspace(a);
     if (need > 0 && (!workspace || workspace_bytes < need)) return GDN_ERR_INVALID_ARG;
     return from_hip(gdn::launch_prefill(a, static_cast<hipStream_t>(stream)));
@@ -282,6 +289,7 @@ gdn_status gdn_step(const void *q, const void *k, const void *v, gdn_dtype qkv_d
                     status};
     const gdn_status st = rule_status(a);
     if (st != GDN_OK) return st;
+    if (!grid_ok((long long)batch * H * ((d_v + 31) / 32), 256)) return GDN_ERR_UNSUPPORTED;
     return from_hip(gdn::launch_step(a, static_cast<hipStream_t>(stream)));
 }
 
@@ -322,6 +330,8 @@ gdn_status gdn_tree_attention(const void *q, const void *k, const void *v, gdn_d
     if ((long long)max_pages * page > 0x3fffffffLL ||
         (long long)batch * n * Hq > 0x3fffffffLL)
         return GDN_ERR_UNSUPPORTED;
+    // the joining kernel: a workgroup of 256 for every 4 rows (d > 128) to 16 (d <= 64)
+    if (!grid_ok((long long)batch * (((long long)n * Hq + 3) / 4), 256)) return GDN_ERR_UNSUPPORTED;
     if (page_stride % 8 != 0 || page_stride < (int64_t)Hkv * page * d) return GDN_ERR_INVALID_ARG;
     // rows inside a page, or inside a tree, are addressed with 32-bit byte offsets
     if (page_stride > 0x7fffffffLL || (long long)Hkv * d > 0xffffffLL) return GDN_ERR_UNSUPPORTED;

@@ -44,6 +44,17 @@ def test_prefill_refuses(lib, kw, code):
     assert prefill(lib, **kw) == code
 
 
+def test_rule_refuses_more_threads_than_a_launch_has(lib):
+    big = dict(dk=8, dv=8, H=1024, Hk=1024, slots=8)
+    assert prefill(lib, batch=8192, rows=8192, **big) == -2        # 2^23 workgroups of 512
+    assert prefill(lib, batch=1, rows=1 << 20, **big) == -2        # 2^24 of 256
+    assert prefill(lib, batch=8191, rows=0, ws=None, **big) == -1  # these pass: the workspace lacks
+    assert prefill(lib, batch=1, rows=(1 << 20) - 65, ws=None, **big) == -1
+    step = lambda batch: lib.gdn_step(FAKE, FAKE, FAKE, 1, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 0,
+                                      batch, 8, 1024, 1024, 8, 8, None, None)
+    assert step(1 << 14) == -2
+
+
 def test_prefill_workspace(lib):
     need = lib.gdn_prefill_workspace(1, 3, 1000, 4, 2, 128, 128)
     assert need >= 0
