@@ -951,12 +951,14 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttentionArgs a, Layout 
         if (odd) {
             // The sequence's tiles that not all rows saw whole were computed
             // without infinities and NaN.  What this row sees of them decides
-            // its columns: one sign of infinity, or NaN.
+            // its columns: one sign of infinity, or NaN.  Of the shared tokens
+            // these are the tiles from the shortest member's end on, the one
+            // where the shared part ends inside a tile among them.
             const int pos0 = min(len, sh), from_own = pos0 + (len - pos0) / kKeys * kKeys;
             int shortest = sh;
             for (int i = 0; i < members && sh > 0; ++i)
                 shortest = min(shortest, max(0, a.length[gs + i]));
-            const int from = shortest < sh ? shortest / kKeys * kKeys : from_own;
+            const int from = sh > 0 ? shortest / kKeys * kKeys : from_own;
             float x[4] = {};
             auto see = [&](const void *base, size_t at) {
                 const uint16_t *v = static_cast<const uint16_t *>(base) + at + d0;

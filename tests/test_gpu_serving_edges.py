@@ -1,0 +1,53 @@
+"""The serving operators at the edges of their contracts: values that are not
+finite at the end of a shared part, groups whose members differ in length,
+weights far below a row's largest, requests that cannot be served, caches whose
+strides say nothing.  Plain 64-bit implementations and tolerances as in
+test_gpu_serving.py.
+"""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_serving import (DT, Pages, attend, attention_inputs, attention_near, attention_ref,
+                              gen, half_step, ints)
+
+pytestmark = pytest.mark.gpu
+INF, NAN = float("inf"), float("nan")
+
+
+def group(first, last, tokens):
+    return ints([first, last]), ints([tokens])
+
+
+def cell(x, b, t):
+    """page and offset of sequence b's token t"""
+    page = x["kc"].shape[2]
+    return int(x["pages"][b, t // page]), t % page
+
+
+# ---------------------------------------------------------------------------
+# attention
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("shared,lengths,n,dtype", [
+    (96, [100, 100], 1, "bf16"), (144, [150, 160, 150], 3, "fp16"), (200, [200, 200], 2, "bf16"),
+    (33, [40, 40], 1, "bf16"), (128, [130, 130], 1, "bf16"), (90, [90, 64, 77], 2, "bf16"),
+])
+def test_values_not_finite_at_the_end_of_a_shared_part(gpu_lib, shared, lengths, n, dtype):
+    """they reach every row that sees them, wherever the shared part ends"""
+    print("shared", shared, lengths, n, dtype, flush=True)
+    x = attention_inputs(lengths, n, 4, 2, 64, 16, dtype, 61, [(0, len(lengths), shared)])
+    ref, mag = attention_ref(x, 0.1)
+    for t, col, value in ((shared - 1, 5, INF), (max(0, shared - 1) // 64 * 64, 9, NAN),
+                          (shared // 2, 13, -INF)):
+        page, off = cell(x, 0, t)
+        x["vc"][page, :, off, col] = value
+        ref[[b for b, L in enumerate(lengths) if L > t], ..., col] = value
+    got = attend(gpu_lib, x, 0.1, shared=group(0, len(lengths), shared)).cpu()
+    torch.cuda.synchronize()
+    for col in (5, 9, 13):
+        assert torch.equal(torch.isnan(got[..., col]), torch.isnan(ref[..., col])), col
+        for sign in (INF, -INF):
+            assert torch.equal(got[..., col] == sign, ref[..., col] == sign), col
+    fine = torch.isfinite(ref)
+    assert torch.isfinite(got[fine]).all()
+    attention_near(got[fine], ref[fine], mag[fine])
