@@ -811,8 +811,8 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
             if ((ti - 1) & 1) join_keys(tile_1);
             else join_keys(tile_0);
         }
-        // ---- the partial: m, l (negative where values were cleared) and o of
-        // the unit's rows
+        // ---- the partial: m, l (its sign bit set where values were cleared,
+        // also on a sum of zero: all scores -inf) and o of the unit's rows
         if (writes && rlive) {
             const int s = is_own ? slot : lay.slots.own + slot;
             const size_t at = (size_t)s * lay.slots.rows + qrow;
@@ -915,7 +915,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttentionArgs a, Layout 
                 const float mn = fmaxf(mx, p[i].x), base = mn == -__builtin_inff() ? 0.f : mn;
                 const float f = __builtin_amdgcn_exp2f(mx - base);
                 const float e = __builtin_amdgcn_exp2f(p[i].x - base);
-                odd |= p[i].y < 0.f;
+                odd |= (int)__float_as_uint(p[i].y) < 0;
                 ls = ls * f + fabsf(p[i].y) * e;
                 acc.x = acc.x * f + v[i].x * e, acc.y = acc.y * f + v[i].y * e;
                 acc.z = acc.z * f + v[i].z * e, acc.w = acc.w * f + v[i].w * e;

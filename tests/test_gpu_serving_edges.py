@@ -51,3 +51,20 @@ def test_values_not_finite_at_the_end_of_a_shared_part(gpu_lib, shared, lengths,
     fine = torch.isfinite(ref)
     assert torch.isfinite(got[fine]).all()
     attention_near(got[fine], ref[fine], mag[fine])
+
+
+def test_values_not_finite_under_weights_that_are_zero(gpu_lib):
+    """scores of -inf give weights of exactly zero, and 0 * inf is NaN: also
+    where they fill a part of the softmax by themselves"""
+    x = attention_inputs([200, 200], 1, 4, 2, 64, 16, "bf16", 67, [(0, 2, 144)])
+    x["q"][..., 0] = 1.0
+    for t in range(128, 144):
+        page, off = cell(x, 0, t)
+        x["kc"][page, :, off, 0] = -INF
+    ref, mag = attention_ref(x, 0.1)
+    page, off = cell(x, 0, 131)
+    x["vc"][page, :, off, 5] = INF
+    got = attend(gpu_lib, x, 0.1, shared=group(0, 2, 144)).cpu()
+    assert not torch.isfinite(got[..., 5]).any()
+    cols = [c for c in range(64) if c != 5]
+    attention_near(got[..., cols], ref[..., cols], mag[..., cols])
