@@ -957,7 +957,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttentionArgs a, Layout 
             const int pos0 = min(len, sh), from_own = pos0 + (len - pos0) / kKeys * kKeys;
             int shortest = sh;
             for (int i = 0; i < members && sh > 0; ++i)
-                shortest = min(shortest, max(0, a.length[gs + i]));
+                shortest = min(shortest, fit_length(a, a.length[gs + i]));
             const int from = sh > 0 ? shortest / kKeys * kKeys : from_own;
             float x[4] = {};
             auto see = [&](const void *base, size_t at) {

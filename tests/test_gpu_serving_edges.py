@@ -68,3 +68,20 @@ def test_values_not_finite_under_weights_that_are_zero(gpu_lib):
     assert not torch.isfinite(got[..., 5]).any()
     cols = [c for c in range(64) if c != 5]
     attention_near(got[..., cols], ref[..., cols], mag[..., cols])
+
+
+def test_values_not_finite_beside_a_member_that_does_not_fit(gpu_lib):
+    """a member whose length passes its table does not hide what the others see"""
+    x = attention_inputs([200, 200, 200], 2, 4, 2, 64, 16, "bf16", 71, [(0, 3, 128)])
+    ref, mag = attention_ref(x, 0.1)
+    page, off = cell(x, 0, 70)
+    x["vc"][page, :, off, 5] = INF
+    for length in (100000, -3):
+        x["length"][2] = length
+        st = ints([-1] * 3)
+        got = attend(gpu_lib, x, 0.1, shared=group(0, 3, 128), status=st).cpu()
+        assert st.tolist() == [0, 0, gpu_lib.FAULT_BAD_LENGTH]
+        assert torch.isnan(got[2]).all()
+        assert (got[:2, ..., 5] == INF).all(), length
+        cols = [c for c in range(64) if c != 5]
+        attention_near(got[:2][..., cols], ref[:2][..., cols], mag[:2][..., cols])
