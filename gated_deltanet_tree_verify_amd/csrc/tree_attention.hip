@@ -89,6 +89,7 @@ struct F16 {
 // one entry of the line: a group's shared tokens or a sequence's own
 struct Entry {
     int first;       // first sequence of its rows
+    int paged;       // sequence whose page row names its cached keys
     int rows;        // query rows per key head
     int pos0;        // cache position of key 0
     int cached;      // keys that are cached tokens
@@ -101,6 +102,10 @@ struct Entry {
 // what the first kernel leaves for the second
 struct Plan {
     long long per_wg;      // places of the line per workgroup
+};
+struct GroupLine {
+    long long pre;         // places before the group's units
+    int shared, whole;     // as in Batch
 };
 
 struct Slots {
@@ -118,8 +123,11 @@ struct Layout {
 // do not fit count as 0, and without sound groups there are none.
 struct Batch {
     int length[GDN_MAX_SEQUENCES];
-    int start[GDN_MAX_SEQUENCES + 1];
-    int shared[GDN_MAX_SEQUENCES];     // tokens computed once for a group
+    uint16_t start[GDN_MAX_SEQUENCES + 1];
+    uint16_t whole[GDN_MAX_SEQUENCES]; // the group's longest member (the first of them): its
+                                       // page row holds every shared token that anyone sees
+    int shared[GDN_MAX_SEQUENCES];     // tokens computed once for a group, no more than that
+                                       // member has
 };
 
 __device__ __forceinline__ int fit_length(const AttentionArgs &a, int len) {
@@ -133,7 +141,7 @@ __device__ __forceinline__ int fit_shared(const AttentionArgs &a, int members, i
 }
 
 // group of sequence b, or -1.  start ascends within [0, batch] (checked).
-__device__ __forceinline__ int group_of(const int *start, int groups, int b) {
+__device__ __forceinline__ int group_of(const uint16_t *start, int groups, int b) {
     if (groups == 0 || b < start[0] || b >= start[groups]) return -1;
     int lo = 0, hi = groups - 1;            // last g with start[g] <= b
     while (lo < hi) {
@@ -158,6 +166,7 @@ __device__ __forceinline__ Entry entry(const AttentionArgs &a, const Batch &y, i
     const int heads = a.Hq / a.Hkv;
     if (e < groups) {
         x.first = y.start[e];
+        x.paged = y.whole[e];
         x.rows = (y.start[e + 1] - y.start[e]) * a.n * heads;
         x.pos0 = 0;
         x.cached = y.shared[e];
@@ -166,6 +175,7 @@ __device__ __forceinline__ Entry entry(const AttentionArgs &a, const Batch &y, i
         const int b = e - groups, g = group_of(y.start, groups, b);
         const int len = y.length[b];
         x.first = b;
+        x.paged = b;
         x.rows = a.n * heads;
         x.pos0 = g < 0 ? 0 : min(len, y.shared[g]);
         x.cached = len - x.pos0;
@@ -226,6 +236,7 @@ struct Smem {
     long long part[kWaves];
     long long first_off;
     int first_entry, max_own, max_shared, heavy;
+    int flags[kWaves];                   // bad groups, shared tokens
     int lim[kWaves];                     // fewest cached keys seen, over a wave's rows
 };
 
@@ -289,8 +300,9 @@ __device__ __forceinline__ void seek(const AttentionArgs &a, const Batch &y, int
     c.tile = c.rt = c.hk = 0;
     for (c.e = e; c.e < entries; ++c.e) {
         const Entry x = entry(a, y, groups, c.e);
-        c.x = {uniform(x.first), uniform(x.rows),  uniform(x.pos0),     uniform(x.cached),
-               uniform(x.keys),  uniform(x.tiles), uniform(x.row_tiles), uniform(x.weight)};
+        c.x = {uniform(x.first), uniform(x.paged), uniform(x.rows),
+               uniform(x.pos0),  uniform(x.cached), uniform(x.keys),
+               uniform(x.tiles), uniform(x.row_tiles), uniform(x.weight)};
         if (c.x.tiles > 0 && c.x.row_tiles > 0) return;
     }
 }
@@ -331,7 +343,7 @@ __device__ __forceinline__ unsigned long long address(const void *p) {
 __device__ __forceinline__ void load_pages(const AttentionArgs &a, const Cursor &c, int key,
                                            int *to) {
     const int pos = c.x.pos0 + c.tile * kKeys + key;
-    const int32_t *from = a.pages + (size_t)c.x.first * a.max_pages +
+    const int32_t *from = a.pages + (size_t)c.x.paged * a.max_pages +
                           min(pos >> a.page_log, a.max_pages - 1);
     __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
                                      (__attribute__((address_space(3))) void *)to, 4, 0, 0);
@@ -381,15 +393,22 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
 
     // ---- lengths and groups; groups ascend within [0, batch], else none
     int groups = a.groups;
+    // a group's longest member: its length, then the first that has it (the
+    // ring is not in use yet)
+    unsigned long long *longest = &ring[0].k[0];
+    static_assert(sizeof(ring) >= 8 * GDN_MAX_SEQUENCES, "");
     Batch &bat = sm.batch;
     if (tid == 0) sm.max_own = 0, sm.max_shared = 0, sm.heavy = 1;
     for (int b = tid; b < a.batch; b += kThreads) bat.length[b] = fit_length(a, a.length[b]);
-    bool bad = false;
+    bool bad = false, any_shared = false;
     for (int g = tid; g < groups; g += kThreads) {
         const int from = a.gstart[g], to = a.gstart[g + 1];
-        bat.start[g] = from;
-        if (g == groups - 1) bat.start[groups] = to;
+        bat.start[g] = (uint16_t)from;
+        if (g == groups - 1) bat.start[groups] = (uint16_t)to;
         bat.shared[g] = fit_shared(a, to - from, a.gshared[g]);
+        bat.whole[g] = (uint16_t)from;
+        longest[g] = 0;
+        any_shared |= bat.shared[g] > 0;
         bad |= from < 0 || to < from || to > a.batch;
     }
     // pieces past the head size are never loaded: zero for good
@@ -398,8 +417,27 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
             reinterpret_cast<uint4 *>(&tile_0)[i] = make_uint4(0, 0, 0, 0);
             reinterpret_cast<uint4 *>(&tile_1)[i] = make_uint4(0, 0, 0, 0);
         }
-    bad = __syncthreads_or(bad);
+    if (const int f = (__any(bad) ? 1 : 0) | (__any(any_shared) ? 2 : 0); l == 0) sm.flags[w] = f;
+    __syncthreads();
+    const int flags = uniform(sm.flags[0] | sm.flags[1] | sm.flags[2] | sm.flags[3]);
+    bad = flags & 1;
     if (bad) groups = 0;
+    if (flags == 2) {
+        for (int b = tid; b < a.batch; b += kThreads) {
+            const int g = group_of(bat.start, groups, b);
+            if (g >= 0)
+                atomicMax(&longest[g], (unsigned long long)bat.length[b] << 9 |
+                                           (unsigned)(GDN_MAX_SEQUENCES - 1 - b));
+        }
+        __syncthreads();
+        for (int g = tid; g < groups; g += kThreads) {
+            const unsigned long long x = longest[g];
+            bat.whole[g] = (uint16_t)(GDN_MAX_SEQUENCES - 1 - (int)(x & 511));
+            bat.shared[g] = min(bat.shared[g], (int)(x >> 9));
+        }
+        __syncthreads();
+    }
+    static_assert(GDN_MAX_SEQUENCES == 512, "nine bits of a sequence");
     const int entries = groups + a.batch;
 
     // ---- length of the line and of its longest units
@@ -439,7 +477,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
     // ---- where this workgroup's tiles begin; workgroup 0 writes the line
     // down for the second kernel
     {
-        long long *gpre = reinterpret_cast<long long *>(ws + lay.off_gpre);
+        GroupLine *gpre = reinterpret_cast<GroupLine *>(ws + lay.off_gpre);
         long long *bpre = reinterpret_cast<long long *>(ws + lay.off_bpre);
         int *group = reinterpret_cast<int *>(ws + lay.off_group);
         if (wg == 0 && tid == 0) {
@@ -461,7 +499,7 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
                 sm.first_off = t0 - pre;
             }
             if (wg == 0 && e < entries) {
-                if (e < groups) gpre[e] = pre;
+                if (e < groups) gpre[e] = {pre, bat.shared[e], bat.whole[e]};
                 else {
                     const int b = e - groups;
                     bpre[b] = pre;
@@ -865,8 +903,9 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttentionArgs a, Layout 
     const int gs = g >= 0 ? a.gstart[g] : b;
     const int members = g >= 0 ? a.gstart[g + 1] - gs : 1;
     const int said = g >= 0 ? a.gshared[g] : 0;
-    const int sh = g < 0 ? 0 : fit_shared(a, members, said);
-    const long long shared0 = g < 0 ? 0 : reinterpret_cast<const long long *>(ws + lay.off_gpre)[g];
+    const GroupLine line =
+        g < 0 ? GroupLine{0, 0, b} : reinterpret_cast<const GroupLine *>(ws + lay.off_gpre)[g];
+    const int sh = line.shared;
 
     // ---- the row's partials.  What the first kernel did with lengths that
     // do not fit is done here: there are as many partials as are counted, and
@@ -892,7 +931,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttentionArgs a, Layout 
     if (live) {
         const int r = node * heads + hq % heads, rows = a.n * heads;
         const int no = partials(own0, rows, len - min(len, sh) + a.n, r);
-        const int ns = sh > 0 ? partials(shared0, members * rows, sh, (b - gs) * rows + r) : 0;
+        const int ns = sh > 0 ? partials(line.pre, members * rows, sh, (b - gs) * rows + r) : 0;
         const float2 *ml = reinterpret_cast<const float2 *>(ws + lay.off_ml) + qrow;
         const float *o = reinterpret_cast<const float *>(ws + lay.off_o) + qrow * D + d0;
         // eight partials at a time: their loads do not wait for each other
@@ -932,7 +971,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttentionArgs a, Layout 
     for (int c = tid; c < used; c += kThreads) {
         const int p = row[c];
         if (p < 0 || p >= a.num_pages) fault |= kFaultBadPage;
-        if (c < same && p != a.pages[(size_t)gs * a.max_pages + c]) fault |= kFaultBadGroup;
+        if (c < same && p != a.pages[(size_t)line.whole * a.max_pages + c]) fault |= kFaultBadGroup;
     }
     if (said < 0) fault |= kFaultBadGroup;
     __syncthreads();                     // s_fault has its first value
@@ -1006,7 +1045,7 @@ Layout layout(const AttentionArgs &a) {
     y.slots.shared = (int)slots;
     const int64_t held = y.slots.rows * (a.groups > 0 ? 2 * slots : slots);
     y.off_gpre = up16(sizeof(Plan));
-    y.off_bpre = up16(y.off_gpre + 8LL * a.groups);
+    y.off_bpre = up16(y.off_gpre + (int64_t)sizeof(GroupLine) * a.groups);
     y.off_group = up16(y.off_bpre + 8LL * a.batch);
     y.off_ml = up16(y.off_group + 4LL * a.batch);
     y.off_o = up16(y.off_ml + 8 * held);

@@ -83,7 +83,8 @@ typedef enum { GDN_DTYPE_F32 = 0, GDN_DTYPE_BF16 = 1, GDN_DTYPE_F16 = 2 } gdn_dt
 #define GDN_FAULT_BAD_PAGE 16  /* a page id in use outside the cache         */
 #define GDN_FAULT_BAD_GROUP 32 /* group offsets not ascending over the batch,
                                   or a member's page row that differs from
-                                  its group's within the shared tokens       */
+                                  its group's longest member's within the
+                                  shared tokens                              */
 #define GDN_FAULT_NO_PAGE 64   /* not enough free pages for the request      */
 
 /*
@@ -345,7 +346,8 @@ gdn_status gdn_step(const void *q, const void *k, const void *v,
  * pages; that part of the cache is read once for all of them.  The result
  * does not depend on the grouping.  Sequences before group_start[0] and from
  * group_start[groups] on share nothing; members shorter than the shared part
- * use what they have.
+ * use what they have, and every member's entries are those of the group's
+ * longest one within its own tokens.
  * Faults, per sequence (its out rows are NaN): GDN_FAULT_BAD_PARENT,
  * _BAD_LENGTH, _BAD_PAGE, _BAD_GROUP.
  * page is a power of two, d a multiple of 8 up to GDN_MAX_HEAD_DIM,

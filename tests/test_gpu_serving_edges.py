@@ -85,3 +85,46 @@ def test_values_not_finite_beside_a_member_that_does_not_fit(gpu_lib):
         assert (got[:2, ..., 5] == INF).all(), length
         cols = [c for c in range(64) if c != 5]
         attention_near(got[:2][..., cols], ref[:2][..., cols], mag[:2][..., cols])
+
+
+SHORT = [
+    # lengths, n, page, groups
+    ([50, 130], 1, 16, [(0, 2, 128)]),                    # the first member is short
+    ([0, 130, 131], 3, 16, [(0, 3, 128)]),                # and empty
+    ([130, 50, 200, 0, 200], 2, 16, [(0, 5, 192)]),       # the longest is in the middle, twice
+    ([40, 60], 1, 16, [(0, 2, 128)]),                     # nobody has the whole of it
+    ([0, 0], 4, 32, [(0, 2, 64)]),
+    ([10, 70, 30, 300, 290], 1, 8, [(0, 2, 64), (2, 5, 280)]),
+    ([5] + [300] * 70, 1, 16, [(0, 71, 256)]),            # rows over several units
+]
+
+
+@pytest.mark.parametrize("lengths,n,page,groups", SHORT)
+def test_groups_with_members_shorter_than_the_shared_part(gpu_lib, lengths, n, page, groups):
+    """entries past a length are not read, whichever member it is"""
+    print("short members", lengths[:6], n, page, groups, flush=True)
+    x = attention_inputs(lengths, n, 8, 2, 64, page, "bf16", 73, groups)
+    for b, L in enumerate(lengths):
+        x["pages"][b, -(-L // page):] = -1
+    ref, mag = attention_ref(x, 0.125)
+    st = ints([-1] * len(lengths))
+    shared = (ints([groups[0][0]] + [g[1] for g in groups]), ints([g[2] for g in groups]))
+    got = attend(gpu_lib, x, 0.125, shared=shared, status=st)
+    torch.cuda.synchronize()
+    assert st.tolist() == [0] * len(lengths)
+    attention_near(got, ref, mag)
+
+
+def test_short_members_with_other_pages(gpu_lib):
+    """a member is held against the longest one, within its own tokens"""
+    x = attention_inputs([30, 130, 70], 1, 2, 1, 64, 16, "bf16", 79, [(0, 3, 128)])
+    x["pages"][0, 2:] = -1
+    x["pages"][2, 4] = (x["pages"][2, 4] + 1) % x["kc"].shape[0]
+    ref, mag = attention_ref({n: torch.nan_to_num(t) if n in ("kc", "vc") else t
+                              for n, t in x.items()}, 0.125)
+    st = ints([-1] * 3)
+    got = attend(gpu_lib, x, 0.125, shared=group(0, 3, 128), status=st)
+    torch.cuda.synchronize()
+    assert st.tolist() == [0, 0, gpu_lib.FAULT_BAD_GROUP]
+    assert torch.isnan(got[2]).all()
+    attention_near(got[:2], ref[:2], mag[:2])
