@@ -3,7 +3,7 @@
 //
 // A row (sequence, node, query head) attends to the tokens of its sequence's
 // cache and to its node's ancestors-or-self.  The softmax is split over the
-// keys: any part of them gives m = max z, l = sum e^{z - m} and
+// keys: any part of them gives m (any number near max z), l = sum e^{z - m} and
 // o = sum e^{z - m} v, and parts join by
 //     m = max m_i,   out = sum e^{m_i - m} o_i / sum e^{m_i - m} l_i,
 // so a prefix that several sequences share is one part, computed for all
@@ -45,7 +45,6 @@ constexpr int kWaves = 4;
 constexpr int kKeys = 64;                 // keys of a tile
 constexpr int kRows = 128;                // rows of a unit at most
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kSlack = 8.f;
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
@@ -64,6 +63,10 @@ struct Bf16 {
     static __device__ __forceinline__ uint16_t bits(float x) { return bf16_bits(x); }
     static __device__ __forceinline__ float widen(uint16_t x) { return to_f32(x); }
     static constexpr uint32_t kExponent = 0x7f80u;     // all ones: infinite or NaN
+    // Weights are 2^x relative to a reference that follows the scores: it is
+    // set kLift below the largest, and set again once a score passes it by
+    // kTop.  bf16 has fp32's range: any reference does.
+    static constexpr float kLift = 0.f, kTop = 8.f;
 };
 struct F16 {
     typedef f16x8 vec;
@@ -81,6 +84,12 @@ struct F16 {
         return static_cast<float>(__builtin_bit_cast(_Float16, x));
     }
     static constexpr uint32_t kExponent = 0x7c00u;
+    // fp16 has five exponent bits: weights of up to 2^15 leave all of them to
+    // the small ones.  A weight is a normal number down to 2^-26 of the
+    // largest, and never off by more than 2^-37 of it.  (With the largest at 1,
+    // everything below 2^-25 of it went missing from the product with V while
+    // the sum counted it.)
+    static constexpr float kLift = 12.f, kTop = 15.f;
 };
 
 // ---------------------------------------------------------------------------
@@ -759,13 +768,13 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
 #pragma unroll
                 for (int r = 1; r < 16; ++r) top = fmaxf(top, z[r]);
                 top = max_of_halves(top) * sc;
-                // The maximum that weights are relative to follows the scores
-                // only when one passes it by kSlack (in powers of two): weights
-                // stay below 2^kSlack, sums and partials are right for any
-                // reference, and O is seldom multiplied.  A row that has seen
-                // no key yet keeps -inf; its weights are zero.
-                if (__builtin_expect(__any(top > mx + kSlack), 0)) {
-                    const float mn = fmaxf(mx, top);
+                // The reference of the weights follows the scores only when
+                // one passes it by kTop (in powers of two): weights stay below
+                // 2^kTop, sums and partials are right for any reference, and O
+                // is seldom multiplied.  A row that has seen no key yet keeps
+                // -inf; its weights are zero.
+                if (__builtin_expect(__any(top > mx + E::kTop), 0)) {
+                    const float mn = fmaxf(mx, top - E::kLift);
                     const float f = __builtin_amdgcn_exp2f(mx - (mn == -__builtin_inff() ? 0.f : mn));
                     ls *= f;
 #pragma unroll
@@ -780,7 +789,8 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
                     ls += p[r];
                 }
                 // weights rounded to the operand type: half a step each
-                // (2^-8 or 2^-11 of a weight at most), independent over the keys
+                // (2^-8 or 2^-11 of a weight at most, and for fp16 2^-37 of the
+                // largest), independent over the keys
                 const vec p0 = E::round8(p), p1 = E::round8(p + 8);
                 auto times = [&](const uint32_t *y, f32x16 o) {
                     o = E::mma(__builtin_bit_cast(vec, make_uint4(y[0], y[1], y[2], y[3])), p0, o);

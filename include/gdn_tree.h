@@ -353,7 +353,8 @@ gdn_status gdn_step(const void *q, const void *k, const void *v,
  * page is a power of two, d a multiple of 8 up to GDN_MAX_HEAD_DIM,
  * page_stride a multiple of 8, batch and groups at most GDN_MAX_SEQUENCES.
  * Arithmetic: products of dtype operands summed in fp32, maxima and sums in
- * fp32, weights rounded to dtype for the product with V, one rounding of out.
+ * fp32, weights rounded to dtype for the product with V (half a step of the
+ * weight; fp16 also 2^-37 of a row's largest), one rounding of out.
  */
 int64_t gdn_tree_attention_workspace(int batch, int n, int Hq, int Hkv, int d,
                                      int page, int max_pages, int groups);

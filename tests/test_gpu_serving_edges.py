@@ -128,3 +128,26 @@ def test_short_members_with_other_pages(gpu_lib):
     assert st.tolist() == [0, 0, gpu_lib.FAULT_BAD_GROUP]
     assert torch.isnan(got[2]).all()
     attention_near(got[:2], ref[:2], mag[:2])
+
+
+@pytest.mark.parametrize("below", [25.3, 30.0])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_keys_far_below_the_largest(gpu_lib, below, dtype):
+    """every 32nd key is large and has no value, the others are 2^-below of it.
+    fp16 weights are relative to 2^12 at least, so that one is off by half a
+    step of its own or by 2^-25 / 2^12 of the largest, 31 of them to each
+    large one."""
+    x = attention_inputs([4096], 1, 1, 1, 64, 128, dtype, 83)
+    for n in ("q", "kc", "k"):
+        x[n].zero_()
+    x["vc"].copy_((torch.nan_to_num(x["vc"]).abs() + 0.5) * 4096)
+    x["q"][..., 0] = below * np.log(2) / 4
+    x["kc"][:, :, ::32, 0] = 4
+    x["vc"][:, :, ::32] = 0
+    ref, mag = attention_ref(x, 1.0)
+    got = attend(gpu_lib, x, 1.0).cpu()
+    floor = 32 * 2.0 ** -37 * float(x["vc"].max()) if dtype == "fp16" else 0.0
+    h = half_step(DT[dtype])
+    tol = h * ref.abs() + (h + 1e-4) * mag + floor + torch.finfo(DT[dtype]).smallest_normal * h
+    off = (got.double() - ref).abs()
+    assert (off <= tol).all(), ((off / tol).max().item(), ref.max(), got.max())
