@@ -14,6 +14,7 @@
 #include <Python.h>
 
 #include <torch/csrc/Dtype.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "gdn_tree.h"
@@ -21,6 +22,25 @@
 namespace {
 
 PyObject *g_explain = nullptr;
+
+// f(), or `failed` with the Python exception set that its C++ exception stands
+// for.  Sizes, strides and addresses raise for tensors whose metadata is not
+// plain (symbolic sizes, subclasses that answer in Python, no storage), and no
+// C++ exception may cross the interpreter's frames.
+template <typename R, typename F>
+R guarded(R failed, F f) {
+    try {
+        return f();
+    } catch (python_error &e) {
+        if (!PyErr_Occurred()) e.restore();
+        if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (const std::exception &e) {
+        PyErr_SetString(PyExc_RuntimeError, e.what());
+    } catch (...) {
+        PyErr_SetString(PyExc_RuntimeError, "a C++ exception");
+    }
+    return failed;
+}
 
 bool known_dtype(const at::Tensor &x, PyObject *dtypes) {
     for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(dtypes); ++i) {
@@ -32,7 +52,7 @@ bool known_dtype(const at::Tensor &x, PyObject *dtypes) {
     return false;
 }
 
-bool suits(PyObject *t, PyObject *dtypes, PyObject *shape) {
+bool plain(PyObject *t, PyObject *dtypes, PyObject *shape) {
     if (!THPVariable_Check(t) || !PyTuple_Check(dtypes)) return false;
     const at::Tensor &x = THPVariable_Unpack(t);
     if (!x.is_cuda() || !x.is_contiguous() || !known_dtype(x, dtypes)) return false;
@@ -49,9 +69,17 @@ bool suits(PyObject *t, PyObject *dtypes, PyObject *shape) {
     return true;
 }
 
+// false as well where the tensor's metadata raises: the function given to
+// explain() asks the same of it, and lets its exception through
+bool suits(PyObject *t, PyObject *dtypes, PyObject *shape) {
+    const bool ok = guarded(false, [&] { return plain(t, dtypes, shape); });
+    if (!ok) PyErr_Clear();
+    return ok;
+}
+
 // cache(t, dtypes, heads, d): (pages, tokens a page, elements between pages)
 // of a cache [pages][heads][page][d] on the GPU whose pages are contiguous,
-// or None
+// or None (also where its metadata raises, as above)
 PyObject *cache(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (n != 4) {
         PyErr_SetString(PyExc_TypeError, "cache(t, dtypes, heads, d)");
@@ -61,12 +89,18 @@ PyObject *cache(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (PyErr_Occurred()) return nullptr;
     if (!THPVariable_Check(args[0]) || !PyTuple_Check(args[1])) Py_RETURN_NONE;
     const at::Tensor &x = THPVariable_Unpack(args[0]);
-    if (!x.is_cuda() || !known_dtype(x, args[1]) || x.dim() != 4 || x.size(1) != heads ||
-        x.size(3) != d || x.stride(1) != x.size(2) * d || x.stride(2) != d || x.stride(3) != 1)
-        Py_RETURN_NONE;
-    const long long page = x.size(2);
-    return Py_BuildValue("LLL", (long long)x.size(0), page,
-                         x.size(0) > 1 ? (long long)x.stride(0) : heads * page * d);
+    long long pages = 0, page = 0, stride = 0;
+    const bool ok = guarded(false, [&] {
+        if (!x.is_cuda() || !known_dtype(x, args[1]) || x.dim() != 4 || x.size(1) != heads ||
+            x.size(3) != d || x.stride(1) != x.size(2) * d || x.stride(2) != d || x.stride(3) != 1)
+            return false;
+        pages = x.size(0), page = x.size(2);
+        stride = pages > 1 ? (long long)x.stride(0) : heads * page * d;
+        return true;
+    });
+    if (ok) return Py_BuildValue("LLL", pages, page, stride);
+    PyErr_Clear();
+    Py_RETURN_NONE;
 }
 
 PyObject *need(PyObject *, PyObject *const *args, Py_ssize_t n) {
@@ -131,12 +165,8 @@ struct Entry<F> {
                          (Py_ssize_t)sizeof...(A));
             return nullptr;
         }
-        try {
-            return call(F, args, std::index_sequence_for<A...>{});
-        } catch (const std::exception &e) {      // a tensor without storage
-            PyErr_SetString(PyExc_RuntimeError, e.what());
-            return nullptr;
-        }
+        return guarded((PyObject *)nullptr,
+                       [&] { return call(F, args, std::index_sequence_for<A...>{}); });
     }
 };
 

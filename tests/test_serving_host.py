@@ -1,6 +1,8 @@
 """Refusals of the serving operators: arguments that the C entry points and
 the binding turn down before any launch.  Nothing here reaches a GPU."""
 import os
+import subprocess
+import sys
 
 import pytest
 
@@ -201,3 +203,59 @@ def test_native_check_says_what_is_wrong():
         need([0.0], "x", (torch.float32,))
     with pytest.raises(TypeError):
         need(x, "x")
+
+
+ODD_TENSORS = r"""
+import torch
+import gated_deltanet_tree_verify_amd as g
+from torch._subclasses.fake_tensor import FakeTensorMode
+from torch.fx.experimental.symbolic_shapes import ShapeEnv
+
+class Raises(torch.Tensor):
+    @staticmethod
+    def __new__(cls, shape):
+        return torch.Tensor._make_wrapper_subclass(
+            cls, shape, device="cuda", dtype=torch.float32, dispatch_sizes_strides_policy="strides")
+
+    @classmethod
+    def __torch_dispatch__(cls, func, types, args=(), kwargs=None):
+        raise LookupError("this tensor has no " + str(func))
+
+native, f32 = g._native(), (torch.float32,)
+mode = FakeTensorMode(shape_env=ShapeEnv(), allow_non_fake_inputs=True)
+with mode:
+    size = mode.shape_env.create_unbacked_symint()
+    unknown = torch.empty(size, 3, device="cuda")
+    unknown4 = torch.empty(size, 2, 16, 8, device="cuda")
+    fake = torch.empty(2, 3, device="cuda")
+    fake4 = torch.empty(6, 2, 16, 8, device="cuda")
+
+def tells(f, *kinds):
+    try:
+        f()
+    except kinds as e:
+        print(type(e).__name__, str(e).splitlines()[0][:60])
+    else:
+        raise SystemExit("accepted")
+
+native.need(fake, "x", f32, (2, 3))
+assert native.cache(fake4, f32, 2, 8) == (6, 16, 256)
+tells(lambda: native.need(Raises((2, 3)), "x", f32, (2, 3)), LookupError)
+tells(lambda: native.need(unknown, "x", f32, (2, 3)), ValueError, RuntimeError)
+tells(lambda: g._need(Raises((2, 3)), "x", f32), LookupError)
+assert native.cache(Raises((6, 2, 16, 8)), f32, 2, 8) is None
+assert native.cache(unknown4, f32, 2, 8) is None
+tells(lambda: g._need_cache(Raises((6, 2, 16, 8)), fake4, f32, 2, 8), LookupError)
+# the older entry points check theirs with the same code
+tells(lambda: g.accept(unknown, fake, fake), TypeError, RuntimeError, ValueError)
+print("alive")
+"""
+
+
+def test_tensors_whose_metadata_raises_do_not_end_the_process():
+    """exceptions of a tensor's own checks come out as Python exceptions"""
+    pytest.importorskip("torch")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", ODD_TENSORS], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and r.stdout.endswith("alive\n"), (r.returncode, r.stdout, r.stderr)
