@@ -588,7 +588,8 @@ def _explain_caches(k_cache, v_cache, dtypes, Hkv, d):
             raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
         if t.dim() != 4 or t.shape[1] != Hkv or t.shape[3] != d:
             raise ValueError(f"{name} must be [pages][{Hkv}][page][{d}]")
-        if t.stride()[1:] != (t.shape[2] * d, d, 1):
+        if any(t.shape[i] != 1 and t.stride(i) != s
+               for i, s in ((1, t.shape[2] * d), (2, d), (3, 1))):
             raise ValueError(f"the pages of {name} must be contiguous")
     raise ValueError("k_cache and v_cache must have the same pages and strides")
 

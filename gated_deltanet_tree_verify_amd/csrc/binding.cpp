@@ -78,7 +78,8 @@ bool suits(PyObject *t, PyObject *dtypes, PyObject *shape) {
 }
 
 // cache(t, dtypes, heads, d): (pages, tokens a page, elements between pages)
-// of a cache [pages][heads][page][d] on the GPU whose pages are contiguous,
+// of a cache [pages][heads][page][d] on the GPU whose pages are contiguous (the
+// stride of a dimension of one says nothing),
 // or None (also where its metadata raises, as above)
 PyObject *cache(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (n != 4) {
@@ -92,8 +93,11 @@ PyObject *cache(PyObject *, PyObject *const *args, Py_ssize_t n) {
     long long pages = 0, page = 0, stride = 0;
     const bool ok = guarded(false, [&] {
         if (!x.is_cuda() || !known_dtype(x, args[1]) || x.dim() != 4 || x.size(1) != heads ||
-            x.size(3) != d || x.stride(1) != x.size(2) * d || x.stride(2) != d || x.stride(3) != 1)
+            x.size(3) != d)
             return false;
+        const long long dense[4] = {0, x.size(2) * d, d, 1};
+        for (int i = 1; i < 4; ++i)
+            if (x.size(i) != 1 && x.stride(i) != dense[i]) return false;
         pages = x.size(0), page = x.size(2);
         stride = pages > 1 ? (long long)x.stride(0) : heads * page * d;
         return true;

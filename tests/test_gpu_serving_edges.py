@@ -151,3 +151,30 @@ def test_keys_far_below_the_largest(gpu_lib, below, dtype):
     tol = h * ref.abs() + (h + 1e-4) * mag + floor + torch.finfo(DT[dtype]).smallest_normal * h
     off = (got.double() - ref).abs()
     assert (off <= tol).all(), ((off / tol).max().item(), ref.max(), got.max())
+
+
+def loose(t, *dims):
+    """t, with strides that mean nothing in the given dimensions of size one"""
+    strides = list(t.stride())
+    for i in dims:
+        assert t.shape[i] == 1
+        strides[i] = 24
+    return t.as_strided(t.shape, strides)
+
+
+@pytest.mark.parametrize("Hkv,page,dims", [(1, 16, (1,)), (2, 1, (2,)), (1, 1, (1, 2))])
+def test_strides_of_dimensions_of_one(gpu_lib, Hkv, page, dims):
+    x = attention_inputs([33, 5], 2, 2, Hkv, 64, page, "bf16", 89)
+    d = {n: t.cuda() for n, t in x.items()}
+    want = attend(gpu_lib, x, 0.1)
+    odd = {n: loose(d[n], *dims) for n in ("kc", "vc")}
+    got = gpu_lib.tree_attention(d["q"], d["k"], d["v"], d["parent"], odd["kc"], odd["vc"],
+                                 d["pages"], d["length"], 0.1)
+    assert torch.equal(got, want)
+    plain = [d["kc"].clone(), d["vc"].clone()]
+    args = (d["pages"], ints([0, 1]), ints([3, 0]), d["k"], d["v"], ints([[0, 1], [1, 1]]),
+            ints([2, 1]))
+    gpu_lib.kv_commit(*plain, *args)
+    gpu_lib.kv_commit(odd["kc"], odd["vc"], *args)
+    for a, b in zip(plain, (d["kc"], d["vc"])):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))

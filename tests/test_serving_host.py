@@ -259,3 +259,26 @@ def test_tensors_whose_metadata_raises_do_not_end_the_process():
     r = subprocess.run([sys.executable, "-c", ODD_TENSORS], cwd=root, capture_output=True, text=True,
                        timeout=300)
     assert r.returncode == 0 and r.stdout.endswith("alive\n"), (r.returncode, r.stdout, r.stderr)
+
+
+def test_cache_strides_that_say_nothing():
+    """dimensions of one may have any stride; others are refused as before"""
+    torch = pytest.importorskip("torch")
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    native, bf16 = g._native(), (torch.bfloat16,)
+    with FakeTensorMode():
+        x = torch.empty(9, 1, 16, 64, dtype=torch.bfloat16, device="cuda")
+        y = torch.empty(9, 2, 1, 64, dtype=torch.bfloat16, device="cuda")
+        z = torch.empty(1, 2, 16, 64, dtype=torch.bfloat16, device="cuda")
+        for t, strides, heads, want in (
+                (x, (1024, 24, 64, 1), 1, (9, 16, 1024)), (x, (2048, 0, 64, 1), 1, (9, 16, 2048)),
+                (y, (128, 64, 7, 1), 2, (9, 1, 128)), (z, (5, 1024, 64, 1), 2, (1, 16, 2048))):
+            u = t.as_strided(t.shape, strides)
+            assert native.cache(u, bf16, heads, 64) == want
+            assert g._need_cache(u, u, bf16, heads, 64) == want
+        for t, strides, heads in ((x, (1024, 1024, 65, 1), 1), (y, (128, 65, 64, 1), 2),
+                                  (z, (2048, 1000, 64, 1), 2), (z, (2048, 1024, 64, 2), 2)):
+            u = t.as_strided(t.shape, strides)
+            assert native.cache(u, bf16, heads, 64) is None
+            with pytest.raises(ValueError, match="the pages of k_cache must be contiguous"):
+                g._need_cache(u, u, bf16, heads, 64)
