@@ -296,8 +296,12 @@ __global__ __launch_bounds__(kThreads) void page_extend_kernel(PageArgs a, const
     }
 }
 
-// one wave per row; the exchange of the length claims it, so a row that is
-// named twice is given back once
+// One wave per row.  The row's ids are checked before anything is written: each
+// has to be in the pool and counted.  Then the exchange of the length claims the
+// row, so one that is named twice is given back once.  A wave that finds ids
+// that cannot be freed looks at the length again: it is 0 where another wave
+// has just freed the row (the claim is visible before that wave's writes), and
+// only otherwise the ids are at fault.
 __global__ __launch_bounds__(64) void page_free_kernel(PageArgs a,
                                                        const int32_t *__restrict__ done) {
     const int r = blockIdx.x, l = threadIdx.x;
@@ -305,29 +309,32 @@ __global__ __launch_bounds__(64) void page_free_kernel(PageArgs a,
     int fault = 0;
     if (!row_ok(a, row)) fault = kFaultBadSlot;
     else {
-        int len = 0;
-        if (l == 0) {
-            len = a.length[row];
-            if (len >= 0 && len <= (long long)a.width << a.page_log)
-                len = atomicExch(&a.length[row], 0);
-            else
-                len = -1;
-        }
-        len = __shfl(len, 0);
+        const auto length = [&] {
+            return __hip_atomic_load(&a.length[row], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        };
+        const int len = __builtin_amdgcn_readfirstlane(length());
         int32_t *t = a.table + (size_t)row * a.width;
-        if (len < 0) fault = kFaultBadLength;
+        if (len < 0 || len > (long long)a.width << a.page_log) fault = kFaultBadLength;
         else if (len > 0) {
             const int used = pages_of(len, a.page_log);
             bool bad = false;
-            for (int c = l; c < a.width; c += 64) {
+            for (int c = l; c < used; c += 64) {
                 const int p = t[c];
-                if (c < used) {
-                    if (p >= 0 && p < a.pool) atomicSub(&a.ref[p], 1);
-                    else bad = true;
-                }
-                t[c] = -1;
+                bad |= p < 0 || p >= a.pool || a.ref[min(max(p, 0), a.pool - 1)] <= 0;
             }
-            if (__any(bad)) fault = kFaultBadPage;
+            if (__any(bad)) {
+                __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+                if (__builtin_amdgcn_readfirstlane(length()) != 0) fault = kFaultBadPage;
+            } else {
+                int mine = 0;
+                if (l == 0) mine = atomicExch(&a.length[row], 0) != 0;
+                mine = __builtin_amdgcn_readfirstlane(mine);
+                __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
+                for (int c = l; mine && c < a.width; c += 64) {
+                    if (c < used) atomicSub(&a.ref[t[c]], 1);
+                    t[c] = -1;
+                }
+            }
         }
     }
     if (l == 0 && a.status) a.status[r] = fault;

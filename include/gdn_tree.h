@@ -388,7 +388,8 @@ gdn_status gdn_tree_attention(const void *q, const void *k, const void *v,
  * served (GDN_FAULT_NO_PAGE).  Where fork or extend name a dst row twice,
  * the first request has it and the others fail (GDN_FAULT_BAD_SLOT).
  * gdn_page_free: the rows done[r] give their pages back and become empty; a
- * row that is named twice is freed once.
+ * row that is named twice is freed once.  A page whose ref is not positive is
+ * a fault like an id outside the pool.
  * gdn_page_compact: the used pages with ids >= (number of used pages) move,
  * in order, into the free ones below; table (entries of the lengths' tokens)
  * and ref follow.  copies [pool / 2][2] lists {from, to}, count[0] their

@@ -178,3 +178,51 @@ def test_strides_of_dimensions_of_one(gpu_lib, Hkv, page, dims):
     gpu_lib.kv_commit(odd["kc"], odd["vc"], *args)
     for a, b in zip(plain, (d["kc"], d["vc"])):
         assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+# ---------------------------------------------------------------------------
+# pages
+# ---------------------------------------------------------------------------
+def test_page_free_changes_nothing_for_a_bad_row(gpu_lib):
+    """an id outside the pool, or a page that nobody is counted for: the row,
+    its length and every count stay, and a repaired row is freed whole"""
+    rng = np.random.default_rng(5)
+    P = Pages(rng, 6, 4, 20, 4, {0: 10, 1: 16, 2: 3, 3: 9, 4: 8})
+    kept = P.table.copy()
+    P.table[1, 2] = 25                                   # outside the pool
+    P.table[3, 1] = -1
+    P.table[4, 1] = int(np.argmax(P.ref == 0))           # free
+    table, length, ref = P.up()
+    st = ints([-1] * 8)
+    done = [0, 1, 3, 1, 4, 0, 2, 5]
+    gpu_lib.page_free(table, length, ref, ints(done), 4, status=st)
+    P.release([0, 2])
+    torch.cuda.synchronize()
+    bad = gpu_lib.FAULT_BAD_PAGE
+    assert st.tolist() == [0, bad, bad, bad, bad, 0, 0, 0]
+    P.same(table, length, ref)
+    for r in (1, 3, 4):
+        P.table[r] = kept[r]
+    table.copy_(ints(P.table.tolist()))
+    gpu_lib.page_free(table, length, ref, ints(done), 4, status=st)
+    P.release([1, 3, 4])
+    torch.cuda.synchronize()
+    assert st.tolist() == [0] * 8 and not ref.any()
+    P.same(table, length, ref)
+
+
+def test_page_free_many_named_twice(gpu_lib):
+    """rows that share pages, each named twice: every count goes down once"""
+    rng = np.random.default_rng(6)
+    P = Pages(rng, 600, 30, 100, 4, {s: 100 for s in range(3)})
+    table, length, ref = P.up()
+    src, dst = [i % 3 for i in range(3, 600)], list(range(3, 600))
+    gpu_lib.page_fork(table, length, ref, ints(src), ints(dst), 4)
+    P.fork(src, dst)
+    P.same(table, length, ref)
+    done = [int(x) for x in rng.permutation(600)[:500]]
+    st = ints([-1] * 1000)
+    gpu_lib.page_free(table, length, ref, ints(done + done[::-1]), 4, status=st)
+    P.release(done)
+    assert st.tolist() == [0] * 1000
+    P.same(table, length, ref)
