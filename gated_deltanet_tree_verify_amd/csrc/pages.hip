@@ -191,6 +191,23 @@ __global__ __launch_bounds__(kThreads) void page_fork_kernel(PageArgs a, const i
             if (__any(bad[k]) && l == 0) q.fault[r0 + k * kWaves] = kFaultBadPage;
     }
     claim_rows(a, dst, m, q);
+    // A source that an earlier request writes: what that row will hold is not
+    // known here (it may stay empty for want of a page), so the request fails.
+    // A claimed row's length is its request less m.
+    constexpr int kLate = -2;
+    for (int r = tid; r < m; r += kThreads)
+        if (q.fault[r] == 0) {
+            const int x = __hip_atomic_load(&a.length[q.src[r]], __ATOMIC_RELAXED,
+                                            __HIP_MEMORY_SCOPE_AGENT);
+            if (x < 0 && x + m < r) q.last[r] = kLate;
+        }
+    __syncthreads();
+    for (int r = tid; r < m; r += kThreads)
+        if (q.last[r] == kLate) {
+            q.last[r] = -1;
+            q.fault[r] = kFaultBadSlot;
+            a.length[q.dst[r]] = 0;
+        }
 
     const int sum = running_totals(q.upto, m, q.part, [&](int r) {
         return q.fault[r] == 0 && (q.len[r] & (page - 1)) != 0 ? 1 : 0;

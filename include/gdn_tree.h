@@ -381,7 +381,9 @@ gdn_status gdn_tree_attention(const void *q, const void *k, const void *v,
  * src[r]: its whole pages are shared (ref + 1), a last partial page gets a
  * page of its own.  copies[r] = {from, to} of that page, {-1, -1} where
  * there is none; gdn_page_copy moves the bytes.  Without a free page the row
- * stays empty (GDN_FAULT_NO_PAGE).
+ * stays empty (GDN_FAULT_NO_PAGE).  A row that an earlier request of the call
+ * names as dst cannot be a src (GDN_FAULT_BAD_SLOT): fork it in a call of its
+ * own, after its pages have been copied.
  * gdn_page_extend: room for add[r] more tokens in row dst[r]; begin[r] is
  * its length before, or -1 where the pages did not suffice: from the first
  * request on whose pages, with those before it, pass the free ones, none is

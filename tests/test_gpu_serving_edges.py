@@ -226,3 +226,20 @@ def test_page_free_many_named_twice(gpu_lib):
     P.release(done)
     assert st.tolist() == [0] * 1000
     P.same(table, length, ref)
+
+
+def test_page_fork_from_a_row_of_the_same_call(gpu_lib):
+    """a row that an earlier request of the call writes cannot be read; one
+    that a later request writes is read as it was, empty"""
+    rng = np.random.default_rng(8)
+    P = Pages(rng, 10, 4, 20, 4, {0: 10, 1: 16})
+    table, length, ref = P.up()
+    src, dst = [0, 4, 7, 1, 5], [4, 5, 6, 7, 8]
+    st = ints([-1] * 5)
+    copies = gpu_lib.page_fork(table, length, ref, ints(src), ints(dst), 4, status=st)
+    want = P.fork([0, 1], [4, 7])
+    torch.cuda.synchronize()
+    bad = gpu_lib.FAULT_BAD_SLOT
+    assert st.tolist() == [0, bad, 0, 0, bad]
+    assert copies.tolist() == [want[0], [-1, -1], [-1, -1], want[1], [-1, -1]]
+    P.same(table, length, ref)
