@@ -377,6 +377,7 @@ gdn_status gdn_page_free(int32_t *table, int32_t *length, int32_t *ref, const in
     if (st != GDN_OK) return st;
     if (m == 0) return GDN_OK;
     if (!done || !all_aligned(done)) return GDN_ERR_INVALID_ARG;
+    if (!grid_ok(m, gdn::kRowThreads)) return GDN_ERR_UNSUPPORTED;
     return from_hip(gdn::launch_page_free(a, done, m, static_cast<hipStream_t>(stream)));
 }
 
@@ -389,6 +390,7 @@ gdn_status gdn_page_compact(int32_t *table, const int32_t *length, int32_t *ref,
     if (st != GDN_OK) return st;
     if ((pool > 1 && !copies) || !count || !workspace) return GDN_ERR_INVALID_ARG;
     if (!all_aligned(copies, count, workspace)) return GDN_ERR_INVALID_ARG;
+    if (!grid_ok(seqs, gdn::kRowThreads)) return GDN_ERR_UNSUPPORTED;
     return from_hip(
         gdn::launch_page_compact(a, copies, count, workspace, static_cast<hipStream_t>(stream)));
 }
@@ -400,7 +402,9 @@ gdn_status gdn_page_copy(void *cache, const int32_t *copies, const int32_t *coun
     if (!cache || !copies || !all_aligned((const char *)cache, copies, count) ||
         page_bytes % 16 != 0)
         return GDN_ERR_INVALID_ARG;
-    if (planes > 65535) return GDN_ERR_UNSUPPORTED;
+    const int64_t parts = gdn::page_copy_parts(page_bytes);
+    if (planes > 65535 || parts > 0xffffffffLL || !grid_ok(parts * m, gdn::kCopyThreads))
+        return GDN_ERR_UNSUPPORTED;
     return from_hip(gdn::launch_page_copy(cache, copies, count, m, planes, pool, page_bytes,
                                           static_cast<hipStream_t>(stream)));
 }
@@ -424,6 +428,8 @@ gdn_status gdn_kv_commit(void *k_cache, void *v_cache, int64_t page_stride, cons
     if (page_log < 0 || d % 8 != 0 || (long long)max_pages * page > 0x7fffffffLL)
         return GDN_ERR_UNSUPPORTED;
     if (page_stride % 8 != 0 || page_stride < (int64_t)Hkv * page * d) return GDN_ERR_INVALID_ARG;
+    if (!grid_ok(gdn::kv_commit_parts(max_path) * m, gdn::kCommitThreads))
+        return GDN_ERR_UNSUPPORTED;
     const gdn::KvCommitArgs a{k_cache, v_cache, page_stride, table, dst,        begin, k,
                               v,       path,    add,         m,     n,          max_path, Hkv,
                               d,       elem_bytes, seqs,     max_pages, pool,   page_log, status};

@@ -319,7 +319,7 @@ __global__ __launch_bounds__(kThreads) void page_extend_kernel(PageArgs a, const
 // that cannot be freed looks at the length again: it is 0 where another wave
 // has just freed the row (the claim is visible before that wave's writes), and
 // only otherwise the ids are at fault.
-__global__ __launch_bounds__(64) void page_free_kernel(PageArgs a,
+__global__ __launch_bounds__(kRowThreads) void page_free_kernel(PageArgs a,
                                                        const int32_t *__restrict__ done) {
     const int r = blockIdx.x, l = threadIdx.x;
     const int row = done[r];
@@ -394,7 +394,7 @@ __global__ __launch_bounds__(kThreads) void page_compact_kernel(PageArgs a, int2
     if (tid == 0) count[0] = moves;
 }
 
-__global__ __launch_bounds__(64) void page_remap_kernel(PageArgs a,
+__global__ __launch_bounds__(kRowThreads) void page_remap_kernel(PageArgs a,
                                                         const int32_t *__restrict__ to) {
     const int row = blockIdx.x;
     const int len = a.length[row];
@@ -407,11 +407,7 @@ __global__ __launch_bounds__(64) void page_remap_kernel(PageArgs a,
     }
 }
 
-// 16 KiB per workgroup: four 16-byte pieces per thread, loaded before any is
-// stored
-constexpr int kCopyThreads = 256;
-constexpr int kCopyPieces = 4;
-
+// a thread's pieces are loaded before any is stored
 __global__ __launch_bounds__(kCopyThreads) void page_copy_kernel(
     uint4 *cache, const int2 *__restrict__ copies, const int32_t *__restrict__ count, int pool,
     int64_t pieces, int parts) {
@@ -433,9 +429,7 @@ __global__ __launch_bounds__(kCopyThreads) void page_copy_kernel(
 }
 
 // one workgroup per (request, 8 tokens)
-constexpr int kTokens = 8;
-
-__global__ __launch_bounds__(256) void kv_commit_kernel(KvCommitArgs a, int parts) {
+__global__ __launch_bounds__(kCommitThreads) void kv_commit_kernel(KvCommitArgs a, int parts) {
     const int r = blockIdx.x / parts, part = blockIdx.x % parts;
     const int row = a.dst[r], at = a.begin[r], add = a.add[r];
     int fault = 0;
@@ -447,7 +441,7 @@ __global__ __launch_bounds__(256) void kv_commit_kernel(KvCommitArgs a, int part
     // of its rows or none
     if (!fault && at >= 0) {
         int f = 0;
-        for (int j = threadIdx.x; j < add; j += 256) {
+        for (int j = threadIdx.x; j < add; j += kCommitThreads) {
             const int node = a.path[(size_t)r * a.max_path + j];
             if (node < 0 || node >= a.n) f |= kFaultBadPath;
             const int p = a.table[(size_t)row * a.width + ((at + j) >> a.page_log)];
@@ -462,11 +456,11 @@ __global__ __launch_bounds__(256) void kv_commit_kernel(KvCommitArgs a, int part
     const int per = a.d * a.elem_bytes / 16;              // pieces of one head's row
     const int rowp = a.Hkv * per;
     const size_t pstride = (size_t)a.page_stride * a.elem_bytes / 16;
-    const int n = min(kTokens, add - part * kTokens);
+    const int n = min(kCommitTokens, add - part * kCommitTokens);
     const uint4 *k = static_cast<const uint4 *>(a.k) + (size_t)r * a.n * rowp;
     const uint4 *v = static_cast<const uint4 *>(a.v) + (size_t)r * a.n * rowp;
-    for (int i = threadIdx.x; i < n * rowp; i += 256) {
-        const int j = part * kTokens + i / rowp, x = i % rowp, h = x / per;
+    for (int i = threadIdx.x; i < n * rowp; i += kCommitThreads) {
+        const int j = part * kCommitTokens + i / rowp, x = i % rowp, h = x / per;
         const int node = a.path[(size_t)r * a.max_path + j], pos = at + j;
         const int p = a.table[(size_t)row * a.width + (pos >> a.page_log)];
         const size_t to = (size_t)p * pstride +
@@ -493,7 +487,7 @@ hipError_t launch_page_extend(const PageArgs &a, const int32_t *dst, const int32
 }
 
 hipError_t launch_page_free(const PageArgs &a, const int32_t *done, int m, hipStream_t s) {
-    hipLaunchKernelGGL(page_free_kernel, dim3((unsigned)m), dim3(64), 0, s, a, done);
+    hipLaunchKernelGGL(page_free_kernel, dim3((unsigned)m), dim3(kRowThreads), 0, s, a, done);
     return hipGetLastError();
 }
 
@@ -503,15 +497,15 @@ hipError_t launch_page_compact(const PageArgs &a, int32_t *copies, int32_t *coun
                        reinterpret_cast<int2 *>(copies), count, workspace);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(page_remap_kernel, dim3((unsigned)a.seqs), dim3(64), 0, s, a, workspace);
+    hipLaunchKernelGGL(page_remap_kernel, dim3((unsigned)a.seqs), dim3(kRowThreads), 0, s, a,
+                       workspace);
     return hipGetLastError();
 }
 
 hipError_t launch_page_copy(void *cache, const int32_t *copies, const int32_t *count, int m,
                             int planes, int pool, int64_t page_bytes, hipStream_t s) {
     const int64_t pieces = page_bytes / 16;
-    const int64_t parts = (pieces + kCopyThreads * kCopyPieces - 1) / (kCopyThreads * kCopyPieces);
-    if (parts * m > 0x7fffffffLL) return hipErrorInvalidValue;
+    const int64_t parts = page_copy_parts(page_bytes);
     hipLaunchKernelGGL(page_copy_kernel, dim3((unsigned)(parts * m), (unsigned)planes),
                        dim3(kCopyThreads), 0, s, static_cast<uint4 *>(cache),
                        reinterpret_cast<const int2 *>(copies), count, pool, pieces, (int)parts);
@@ -519,9 +513,9 @@ hipError_t launch_page_copy(void *cache, const int32_t *copies, const int32_t *c
 }
 
 hipError_t launch_kv_commit(const KvCommitArgs &a, hipStream_t s) {
-    const int parts = (a.max_path + kTokens - 1) / kTokens;
-    if ((long long)parts * a.m > 0x7fffffffLL) return hipErrorInvalidValue;
-    hipLaunchKernelGGL(kv_commit_kernel, dim3((unsigned)(parts * a.m)), dim3(256), 0, s, a, parts);
+    const int64_t parts = kv_commit_parts(a.max_path);
+    hipLaunchKernelGGL(kv_commit_kernel, dim3((unsigned)(parts * a.m)), dim3(kCommitThreads), 0, s,
+                       a, (int)parts);
     return hipGetLastError();
 }
 

@@ -60,6 +60,20 @@ struct KvCommitArgs {
     int32_t *status;
 };
 
+// workgroups of 256 threads: page_copy moves 16 KiB of a page in each (four
+// 16-byte pieces a thread), kv_commit 8 tokens of a request
+constexpr int kCopyThreads = 256, kCopyPieces = 4;
+constexpr int64_t page_copy_parts(int64_t page_bytes) {
+    constexpr int64_t kBytes = 16 * kCopyThreads * kCopyPieces;
+    return page_bytes / kBytes + (page_bytes % kBytes != 0);
+}
+constexpr int kCommitThreads = 256, kCommitTokens = 8;
+constexpr int64_t kv_commit_parts(int max_path) {
+    return ((int64_t)max_path + kCommitTokens - 1) / kCommitTokens;
+}
+// page_free and the second kernel of page_compact: a wave a row
+constexpr int kRowThreads = 64;
+
 int64_t prefill_workspace(const RuleArgs &a);
 hipError_t launch_prefill(const RuleArgs &a, hipStream_t s);
 hipError_t launch_step(const RuleArgs &a, hipStream_t s);

@@ -282,3 +282,22 @@ def test_cache_strides_that_say_nothing():
             assert native.cache(u, bf16, heads, 64) is None
             with pytest.raises(ValueError, match="the pages of k_cache must be contiguous"):
                 g._need_cache(u, u, bf16, heads, 64)
+
+
+def test_pages_refuse_more_threads_than_a_launch_has(lib):
+    """before anything is launched: page_compact changes the counts in its
+    first kernel, and the second is the one that would not fit"""
+    P = FAKE
+    free = lambda m: lib.gdn_page_free(P, P, P, P, m, 4, 4, 8, 16, None, None)
+    assert free(1 << 26) == -2                              # workgroups of 64
+    pack = lambda seqs: lib.gdn_page_compact(P, P, P, P, P, P, seqs, 1, 8, 16, None)
+    assert pack(1 << 26) == -2
+    copy = lambda m, size: lib.gdn_page_copy(P, P, None, m, 2, 8, size, None)
+    assert copy(1 << 24, 16) == -2                          # workgroups of 256, 16 KiB each
+    assert copy(1 << 14, 1 << 24) == -2 and copy(1 << 14, (1 << 24) - 16) == -2
+    assert copy(1, 1 << 38) == -2 and copy(0x7fffffff, 0x7ffffffffffffff0) == -2
+    rows = lambda m, max_path: lib.gdn_kv_commit(P, P, 2048, P, P, P, P, P, P, P, m, 4, max_path, 2,
+                                                 64, 2, 4, 4, 8, 16, None, None)
+    assert rows(1 << 24, 1) == -2                           # workgroups of 256, 8 tokens each
+    assert rows(1 << 20, 128) == -2 and rows(1 << 20, 121) == -2
+    assert rows(0x7fffffff, 0x7fffffff) == -2 and rows(1, 0x7fffffff) == -2
