@@ -90,17 +90,34 @@ __device__ __forceinline__ int pages_of(int tokens, int page_log) {
     return (int)(((long long)tokens + (1LL << page_log) - 1) >> page_log);
 }
 
-// running totals of need(r) over the requests, in upto[]; returns the last
+// a + b for numbers that are not negative; kMany stands for all that do not
+// fit (there are fewer pages than that)
+constexpr int kMany = 0x7fffffff;
+__device__ __forceinline__ int add_up(int a, int b) {
+    return (int)min((unsigned)a + (unsigned)b, (unsigned)kMany);
+}
+
+// running totals of need(r) over the requests, in upto[]; returns the last.
+// Thousands of requests for whole rows pass 32 bits: the totals stop at kMany.
 template <typename F>
 __device__ int running_totals(int *upto, int m, int *s_part, F need) {
+    const int w = threadIdx.x >> 6, l = threadIdx.x & 63;
     int sum = 0;
     for (int r0 = 0; r0 < m; r0 += kThreads) {
         const int r = r0 + threadIdx.x;
-        const int x = r < m ? need(r) : 0;
-        int total;
-        const int before = block_exclusive(x, s_part, total);
-        if (r < m) upto[r] = sum + before + x;
-        sum += total;
+        int x = r < m ? need(r) : 0;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int up = __shfl_up(x, o);
+            if (l >= o) x = add_up(x, up);
+        }
+        __syncthreads();
+        if (l == 63) s_part[w] = x;
+        __syncthreads();
+        for (int i = 0; i < kWaves; ++i) {
+            if (i == w && r < m) upto[r] = add_up(sum, x);
+            sum = add_up(sum, s_part[i]);
+        }
     }
     __syncthreads();
     return sum;

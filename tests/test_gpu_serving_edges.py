@@ -243,3 +243,26 @@ def test_page_fork_from_a_row_of_the_same_call(gpu_lib):
     assert st.tolist() == [0, bad, 0, 0, bad]
     assert copies.tolist() == [want[0], [-1, -1], [-1, -1], want[1], [-1, -1]]
     P.same(table, length, ref)
+
+
+def test_page_extend_totals_past_32_bits(gpu_lib):
+    """requests for whole rows of half a million pages: more than 2^31 pages
+    are asked for, 100 are there"""
+    seqs, width = 4096, (1 << 19) + 1
+    table = torch.empty(seqs, width, dtype=torch.int32, device="cuda")      # 8 GiB
+    table[:3] = -1
+    length = torch.zeros(seqs, dtype=torch.int32, device="cuda")
+    ref = ints([0] * 100)
+    add = torch.full((seqs,), width, dtype=torch.int32, device="cuda")
+    add[0], add[1] = 50, 30
+    st = torch.full((seqs,), -1, dtype=torch.int32, device="cuda")
+    begin = gpu_lib.page_extend(table, length, ref, torch.arange(seqs, dtype=torch.int32,
+                                                                 device="cuda"), add, 1, status=st)
+    torch.cuda.synchronize()
+    none = gpu_lib.FAULT_NO_PAGE
+    assert st.tolist() == [0, 0] + [none] * (seqs - 2)
+    assert begin.tolist() == [0, 0] + [-1] * (seqs - 2)
+    assert length.tolist() == [50, 30] + [0] * (seqs - 2)
+    assert table[0, :51].tolist() == list(range(50)) + [-1]
+    assert table[1, :31].tolist() == list(range(50, 80)) + [-1]
+    assert (table[2] == -1).all() and ref.tolist() == [1] * 80 + [0] * 20
