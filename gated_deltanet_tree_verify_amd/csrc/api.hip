@@ -56,8 +56,9 @@ gdn_status page_status(const gdn::PageArgs &a, int m, int page) {
     if (!a.table || !a.length || !a.ref) return GDN_ERR_INVALID_ARG;
     if (!all_aligned(a.table, a.length, a.ref, a.status)) return GDN_ERR_INVALID_ARG;
     if (m < 0 || a.seqs < 1 || a.width < 1 || a.pool < 1 || page < 1) return GDN_ERR_INVALID_ARG;
-    // a row's tokens are counted in 32 bits
-    if (a.page_log < 0 || (long long)a.width * page > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
+    // tokens and pages are counted in 32 bits, by loops that step past their end
+    if (a.page_log < 0 || (long long)a.width * page > GDN_MAX_TOKENS || a.pool > GDN_MAX_PAGES)
+        return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }
 
@@ -327,7 +328,7 @@ gdn_status gdn_tree_attention(const void *q, const void *k, const void *v, gdn_d
         batch > GDN_MAX_SEQUENCES || groups > GDN_MAX_SEQUENCES)
         return GDN_ERR_UNSUPPORTED;
     // tokens, and the query rows of a group, are counted in 32 bits
-    if ((long long)max_pages * page > 0x3fffffffLL ||
+    if ((long long)max_pages * page > GDN_MAX_TOKENS ||
         (long long)batch * n * Hq > 0x3fffffffLL)
         return GDN_ERR_UNSUPPORTED;
     // the joining kernel: a workgroup of 256 for every 4 rows (d > 128) to 16 (d <= 64)
@@ -424,8 +425,10 @@ gdn_status gdn_kv_commit(void *k_cache, void *v_cache, int64_t page_stride, cons
                      (const char *)k, (const char *)v, path, add, status))
         return GDN_ERR_INVALID_ARG;
     const int page_log = log2_exact(page);
-    // rows are moved in 16-byte pieces; a row's tokens are counted in 32 bits
-    if (page_log < 0 || d % 8 != 0 || (long long)max_pages * page > 0x7fffffffLL)
+    // rows are moved in 16-byte pieces; tokens and a token's pieces are counted
+    // in 32 bits
+    if (page_log < 0 || d % 8 != 0 || (long long)max_pages * page > GDN_MAX_TOKENS ||
+        (long long)Hkv * d > 0xffffffLL)
         return GDN_ERR_UNSUPPORTED;
     if (page_stride % 8 != 0 || page_stride < (int64_t)Hkv * page * d) return GDN_ERR_INVALID_ARG;
     if (!grid_ok(gdn::kv_commit_parts(max_path) * m, gdn::kCommitThreads))

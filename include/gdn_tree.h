@@ -60,6 +60,8 @@ extern "C" {
 #define GDN_MAX_HEAD_DIM 256    /* head size of gdn_tree_attention */
 #define GDN_MAX_SEQUENCES 512   /* batch and groups of gdn_tree_attention */
 #define GDN_MAX_REQUESTS 4096   /* requests of one page_fork / page_extend call */
+#define GDN_MAX_TOKENS 0x3fffffff /* max_pages * page: tokens of a cache row */
+#define GDN_MAX_PAGES 0x3fffffff  /* pool of the page calls */
 
 typedef enum {
     GDN_OK = 0,

@@ -301,3 +301,22 @@ def test_pages_refuse_more_threads_than_a_launch_has(lib):
     assert rows(1 << 24, 1) == -2                           # workgroups of 256, 8 tokens each
     assert rows(1 << 20, 128) == -2 and rows(1 << 20, 121) == -2
     assert rows(0x7fffffff, 0x7fffffff) == -2 and rows(1, 0x7fffffff) == -2
+
+
+def test_pages_refuse_counts_past_32_bits(lib):
+    """loops over tokens and pages step past their end: 2^30 and more of either
+    are refused before anything is launched"""
+    P, most = FAKE, (1 << 30) - 1
+    for fn in (lib.gdn_page_fork, lib.gdn_page_extend):
+        call = lambda m, width, pool, page: fn(P, P, P, P, P, P, m, 4, width, pool, page, None, None)
+        assert call(1, 4, most + 1, 16) == -2 and call(1, 1 << 26, 8, 16) == -2
+        assert call(0, 4, most, 16) == 0 and call(0, (1 << 26) - 1, 8, 16) == 0
+    free = lambda m, width, pool: lib.gdn_page_free(P, P, P, P, m, 4, width, pool, 1, None, None)
+    assert free(1, 1 << 30, 8) == -2 and free(1, 4, most + 1) == -2 and free(0, most, most) == 0
+    pack = lambda width, pool: lib.gdn_page_compact(P, P, P, P, P, P, 4, width, pool, 1, None)
+    assert pack(1 << 30, 8) == -2 and pack(4, 0x7fffffff) == -2
+
+    def rows(width=4, Hkv=2, d=64, page=16):
+        return lib.gdn_kv_commit(P, P, Hkv * page * d, P, P, P, P, P, P, P, 1, 4, 4, Hkv, d, 2, 4,
+                                 width, 8, page, None, None)
+    assert rows(width=1 << 26) == -2 and rows(Hkv=1 << 18) == -2 and rows(Hkv=1 << 21, d=1024) == -2
