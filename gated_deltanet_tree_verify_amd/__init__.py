@@ -179,6 +179,11 @@ def _native():
         except ImportError as e:
             raise RuntimeError("the binding's native part cannot be loaded; run "
                                "gated_deltanet_tree_verify_amd.build()") from e
+        got = getattr(_binding, "ABI_VERSION", None)
+        if got != ABI_VERSION:
+            raise RuntimeError(f"the binding's native part has ABI version {got}, this package "
+                               f"expects {ABI_VERSION}; rebuild with "
+                               "gated_deltanet_tree_verify_amd.build()")
         _binding.explain(_explain)
         _native_module = _binding
     return _native_module
@@ -245,9 +250,15 @@ def _explain(t, name, dtypes, shape=None):
 
 def _need(t, name, dtypes, shape=None):
     """a contiguous GPU tensor of one of the dtypes, of this shape if given;
-    from the first call on this name is the native check itself"""
+    from the first call on this name is the native check itself.  The tree
+    calls need libgdntree.so alone: without the native part they are checked
+    in Python (the serving operators ask for it first, and raise)."""
     global _need
-    _need = _native().need
+    try:
+        _need = _native().need
+    except RuntimeError:
+        load()
+        _need = _explain
     _need(t, name, dtypes, shape)
 
 

@@ -71,7 +71,8 @@ def build_binding(verbose: bool = False) -> str:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
-        raise RuntimeError(f"{cmd[0]} failed ({res.returncode}):\n{res.stderr}")
+        raise RuntimeError(f"{cmd[0]} failed ({res.returncode}) on the binding's native part, which "
+                           f"the serving operators need; {LIB} is built:\n{res.stderr}")
     os.replace(tmp, BINDING)
     return BINDING
 

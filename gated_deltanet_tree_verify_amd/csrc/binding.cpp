@@ -198,4 +198,9 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, g_method
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&g_module); }
+PyMODINIT_FUNC PyInit__binding() {
+    PyObject *m = PyModule_Create(&g_module);
+    // the header that the calls above were compiled with
+    if (m && PyModule_AddIntConstant(m, "ABI_VERSION", GDN_TREE_ABI_VERSION) < 0) Py_CLEAR(m);
+    return m;
+}

@@ -320,3 +320,54 @@ def test_pages_refuse_counts_past_32_bits(lib):
         return lib.gdn_kv_commit(P, P, Hkv * page * d, P, P, P, P, P, P, P, 1, 4, 4, Hkv, d, 2, 4,
                                  width, 8, page, None, None)
     assert rows(width=1 << 26) == -2 and rows(Hkv=1 << 18) == -2 and rows(Hkv=1 << 21, d=1024) == -2
+
+
+WITHOUT_NATIVE = r"""
+import sys, types
+import torch
+import gated_deltanet_tree_verify_amd as g
+name = "gated_deltanet_tree_verify_amd._binding"
+kind = sys.argv[1]
+if kind == "missing":
+    sys.modules[name] = None
+else:
+    sys.modules[name] = g._binding = types.ModuleType(name)
+    if kind == "older":
+        g._binding.ABI_VERSION = g.ABI_VERSION - 1
+    g._binding.need = g._binding.explain = None
+
+def tells(f, kind, text):
+    try:
+        f()
+    except kind as e:
+        assert text in str(e), e
+    else:
+        raise SystemExit("accepted")
+
+z = torch.zeros
+i = lambda *s: z(*s, dtype=torch.int32)
+for _ in range(2):
+    tells(lambda: g.verify(z(1, 2, 1, 64), z(1, 2, 1, 64), z(1, 2, 1, 64), z(1, 2, 1), z(1, 2, 1),
+                           i(1, 2), z(1, 1, 64, 64)), ValueError, "q must be a GPU tensor")
+    tells(lambda: g.accept([0], i(1, 2), i(1, 2)), TypeError, "parent must be a torch.Tensor")
+    tells(lambda: g.page_free(i(4, 4), i(4), i(8), i(1), 16), RuntimeError, "build()")
+    tells(lambda: g.step(z(1, 2, 64), z(1, 2, 64), z(1, 2, 64), z(1, 2), z(1, 2), z(2, 2, 64, 64),
+                         i(1), i(1)), RuntimeError, "native part")
+print("done")
+"""
+
+
+@pytest.mark.parametrize("kind", ["missing", "older", "unversioned"])
+def test_tree_calls_need_the_library_alone(lib, kind):
+    """without the binding's native part, or with one of another ABI version,
+    the tree calls check their arguments as ever and the serving operators raise"""
+    pytest.importorskip("torch")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", WITHOUT_NATIVE, kind], cwd=root, capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout == "done\n", (r.returncode, r.stdout, r.stderr)
+
+
+def test_native_part_has_the_headers_version(lib):
+    pytest.importorskip("torch")
+    assert g._native().ABI_VERSION == g.ABI_VERSION == lib.gdn_tree_abi_version()
