@@ -517,6 +517,8 @@ def _rule_shapes(q, k, v, alpha, beta, S, src, dst, out, batch, status, stream):
     if v.dim() != 3 or v.shape[0] != rows:
         raise ValueError("v must be [rows][heads][d_v]")
     H, dv = v.shape[1], v.shape[2]
+    if batch is None:
+        batch = rows
     _need(alpha, "alpha", (torch.float32,), (rows, H))
     _need(beta, "beta", (torch.float32,), (rows, H))
     _need(S, "S", (torch.float32,))
@@ -569,7 +571,7 @@ def step(q, k, v, alpha, beta, S, src, dst, out=None, status=None, stream=None, 
     """gdn_step: one token for every sequence (row i: sequence i); arguments
     as for prefill without cu.  Returns out; S is updated in place."""
     native = _native()
-    rows, Hk, dk, H, dv, out = _rule_shapes(q, k, v, alpha, beta, S, src, dst, out, q.shape[0],
+    rows, Hk, dk, H, dv, out = _rule_shapes(q, k, v, alpha, beta, S, src, dst, out, None,
                                             status, stream)
     args = (q, k, v, _qkv_dtype(q), alpha, beta, S, src,
             dst, out, _qkv_dtype(out), rows, S.shape[0], H, Hk, dk, dv, status,

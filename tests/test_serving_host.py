@@ -371,3 +371,13 @@ def test_tree_calls_need_the_library_alone(lib, kind):
 def test_native_part_has_the_headers_version(lib):
     pytest.importorskip("torch")
     assert g._native().ABI_VERSION == g.ABI_VERSION == lib.gdn_tree_abi_version()
+
+
+def test_step_says_what_is_wrong_with_q():
+    torch = pytest.importorskip("torch")
+    i = torch.zeros(1, dtype=torch.int32)
+    for q in (None, [0.0], 1):
+        with pytest.raises(TypeError, match="q must be a torch.Tensor"):
+            g.step(q, q, q, q, q, q, i, i)
+    with pytest.raises(ValueError, match="q must be a GPU tensor"):
+        g.step(torch.tensor(1.0), i, i, i, i, i, i, i)
