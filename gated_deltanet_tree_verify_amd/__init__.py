@@ -775,7 +775,9 @@ def page_copy(cache, copies, count=None, stream=None, prepare=False):
         if count.numel() != 1:
             raise ValueError("count must hold one number")
     planes, pool = cache.shape[0], cache.shape[1]
-    nbytes = cache.stride(1) * cache.element_size()
+    nbytes = cache.element_size()              # of a page; a pool of one may have any stride
+    for n in cache.shape[2:]:
+        nbytes *= n
     args = (cache, copies, count, copies.shape[0], planes, pool, nbytes,
             _stream(stream))
     return _issue("gdn_page_copy", native.gdn_page_copy, args, (cache, copies, count), cache, prepare)

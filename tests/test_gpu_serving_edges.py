@@ -266,3 +266,14 @@ def test_page_extend_totals_past_32_bits(gpu_lib):
     assert table[0, :51].tolist() == list(range(50)) + [-1]
     assert table[1, :31].tolist() == list(range(50, 80)) + [-1]
     assert (table[2] == -1).all() and ref.tolist() == [1] * 80 + [0] * 20
+
+
+def test_page_copy_of_a_single_page(gpu_lib):
+    """a pool of one page, whose stride says nothing: nothing to copy"""
+    cache = torch.randn(2, 1, 4, 8, device="cuda")
+    odd = cache.as_strided(cache.shape, (32, 3, 8, 1))
+    assert odd.is_contiguous()
+    want = cache.clone()
+    assert gpu_lib.page_copy(odd, ints([[0, 0], [-1, -1]])) is odd
+    torch.cuda.synchronize()
+    assert torch.equal(cache, want)
