@@ -14,10 +14,14 @@ struct Sequence {
     int fault;
 };
 
+__device__ __forceinline__ bool slots_ok(const RuleArgs &a, int src, int dst) {
+    return src >= -1 && src < a.slots && dst >= 0 && dst < a.slots;
+}
+
 __device__ __forceinline__ Sequence sequence(const RuleArgs &a, int b) {
     Sequence s;
-    s.first = a.cu ? a.cu[b] : b;
-    const int end = a.cu ? a.cu[b + 1] : b + 1;
+    s.first = a.cu[b];
+    const int end = a.cu[b + 1];
     s.src = a.src[b], s.dst = a.dst[b];
     s.fault = 0;
     if (s.first < 0 || end < s.first || end > a.rows) {
@@ -26,7 +30,7 @@ __device__ __forceinline__ Sequence sequence(const RuleArgs &a, int b) {
         return s;
     }
     s.len = end - s.first;
-    if (s.src < -1 || s.src >= a.slots || s.dst < 0 || s.dst >= a.slots) s.fault = kFaultBadSlot;
+    if (!slots_ok(a, s.src, s.dst)) s.fault = kFaultBadSlot;
     return s;
 }
 

@@ -1,4 +1,4 @@
-// The gated delta rule token by token: the single-token step of decoding.
+// One token of the gated delta rule for every sequence: the step of decoding.
 //
 // For one (sequence, head), with M = alpha S (S of shape d_k x d_v, fp32):
 //     u = beta (v - M^T k),   S' = M + k u^T,   o = S'^T q = M^T q + (k . q) u,
@@ -24,7 +24,7 @@ constexpr int kSums = 12;      // M^T k (4), M^T q (4), k . q (1) of a column gr
 
 template <typename T, typename OT, int kR>
 __global__ __launch_bounds__(kThreads) void rule_recurrent_kernel(RuleArgs a, int tiles) {
-    __shared__ float red[2][kThreads / 64][8][kSums];
+    __shared__ float red[kThreads / 64][8][kSums];
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63;
     const int cg = tid & 7, rg = tid >> 3;
     const int tile = blockIdx.x % tiles, bh = blockIdx.x / tiles;
@@ -32,15 +32,13 @@ __global__ __launch_bounds__(kThreads) void rule_recurrent_kernel(RuleArgs a, in
     const int c0 = tile * kTile + 4 * cg, r0 = rg * kR;
     const bool live = c0 < a.dv && r0 < a.dk;
 
-    const rule::Sequence sq = rule::sequence(a, b);
-    if (a.status && h == 0 && tile == 0 && tid == 0) a.status[b] = sq.fault;
-    OT *out = static_cast<OT *>(a.out) + (size_t)h * a.dv;
-    const size_t ostride = (size_t)a.H * a.dv;
-    if (sq.fault) {
+    const int src = a.src[b], dst = a.dst[b];
+    const int fault = rule::slots_ok(a, src, dst) ? 0 : kFaultBadSlot;
+    if (a.status && h == 0 && tile == 0 && tid == 0) a.status[b] = fault;
+    OT *out = static_cast<OT *>(a.out) + ((size_t)b * a.H + h) * a.dv + c0;
+    if (fault) {
         if (c0 < a.dv && rg == 0)
-            for (int t = 0; t < sq.len; ++t)
-                for (int e = 0; e < 4; ++e)
-                    rule::put(&out[(sq.first + t) * ostride + c0 + e], __builtin_nanf(""));
+            for (int e = 0; e < 4; ++e) rule::put(&out[e], __builtin_nanf(""));
         return;
     }
 
@@ -50,69 +48,58 @@ __global__ __launch_bounds__(kThreads) void rule_recurrent_kernel(RuleArgs a, in
 #pragma unroll
     for (int i = 0; i < kR; ++i) {
         S[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (live && sq.src >= 0)
-            S[i] = *reinterpret_cast<const float4 *>(a.S + sq.src * slab + at + (size_t)i * a.dv);
+        if (live && src >= 0)
+            S[i] = *reinterpret_cast<const float4 *>(a.S + src * slab + at + (size_t)i * a.dv);
     }
 
-    const T *q = static_cast<const T *>(a.q) + (size_t)hk * a.dk + r0;
-    const T *k = static_cast<const T *>(a.k) + (size_t)hk * a.dk + r0;
-    const T *v = static_cast<const T *>(a.v) + (size_t)h * a.dv + c0;
-    const size_t kstride = (size_t)a.Hk * a.dk;
-    for (int t = 0; t < sq.len; ++t) {
-        const size_t row = (size_t)sq.first + t;
-        float kr[kR], qr[kR], vv[4] = {0.f, 0.f, 0.f, 0.f};
+    const T *q = static_cast<const T *>(a.q) + ((size_t)b * a.Hk + hk) * a.dk + r0;
+    const T *k = static_cast<const T *>(a.k) + ((size_t)b * a.Hk + hk) * a.dk + r0;
+    const T *v = static_cast<const T *>(a.v) + ((size_t)b * a.H + h) * a.dv + c0;
+    float kr[kR], qr[kR], vv[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < kR; ++i) {
-            kr[i] = r0 < a.dk ? to_f32(k[row * kstride + i]) : 0.f;
-            qr[i] = r0 < a.dk ? to_f32(q[row * kstride + i]) : 0.f;
-        }
-        if (c0 < a.dv)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) vv[e] = to_f32(v[row * ostride + e]);
-        const float al = a.alpha[row * a.H + h], be = a.beta[row * a.H + h];
-
-        float s[9] = {};
-#pragma unroll
-        for (int i = 0; i < kR; ++i) {
-            S[i].x *= al, S[i].y *= al, S[i].z *= al, S[i].w *= al;
-            s[0] = fmaf(S[i].x, kr[i], s[0]), s[1] = fmaf(S[i].y, kr[i], s[1]);
-            s[2] = fmaf(S[i].z, kr[i], s[2]), s[3] = fmaf(S[i].w, kr[i], s[3]);
-            s[4] = fmaf(S[i].x, qr[i], s[4]), s[5] = fmaf(S[i].y, qr[i], s[5]);
-            s[6] = fmaf(S[i].z, qr[i], s[6]), s[7] = fmaf(S[i].w, qr[i], s[7]);
-            s[8] = fmaf(kr[i], qr[i], s[8]);
-        }
-#pragma unroll
-        for (int x = 8; x < 64; x <<= 1)
-#pragma unroll
-            for (int j = 0; j < 9; ++j) s[j] += __shfl_xor(s[j], x);
-        float(*buf)[8][kSums] = red[t & 1];
-        if (l < 8) {
-#pragma unroll
-            for (int j = 0; j < 9; ++j) buf[w][l][j] = s[j];
-        }
-        // one barrier a token: the other buffer's readers have all passed it
-        // before this one is written again
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < 9; ++j)
-            s[j] = (buf[0][cg][j] + buf[1][cg][j]) + (buf[2][cg][j] + buf[3][cg][j]);
-        float u[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) u[e] = be * (vv[e] - s[e]);
-#pragma unroll
-        for (int i = 0; i < kR; ++i) {
-            S[i].x = fmaf(kr[i], u[0], S[i].x), S[i].y = fmaf(kr[i], u[1], S[i].y);
-            S[i].z = fmaf(kr[i], u[2], S[i].z), S[i].w = fmaf(kr[i], u[3], S[i].w);
-        }
-        if (rg == 0 && c0 < a.dv)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                rule::put(&out[row * ostride + c0 + e], fmaf(s[8], u[e], s[4 + e]));
+    for (int i = 0; i < kR; ++i) {
+        kr[i] = r0 < a.dk ? to_f32(k[i]) : 0.f;
+        qr[i] = r0 < a.dk ? to_f32(q[i]) : 0.f;
     }
+    if (c0 < a.dv)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) vv[e] = to_f32(v[e]);
+    const float al = a.alpha[(size_t)b * a.H + h], be = a.beta[(size_t)b * a.H + h];
+
+    float s[9] = {};
+#pragma unroll
+    for (int i = 0; i < kR; ++i) {
+        S[i].x *= al, S[i].y *= al, S[i].z *= al, S[i].w *= al;
+        s[0] = fmaf(S[i].x, kr[i], s[0]), s[1] = fmaf(S[i].y, kr[i], s[1]);
+        s[2] = fmaf(S[i].z, kr[i], s[2]), s[3] = fmaf(S[i].w, kr[i], s[3]);
+        s[4] = fmaf(S[i].x, qr[i], s[4]), s[5] = fmaf(S[i].y, qr[i], s[5]);
+        s[6] = fmaf(S[i].z, qr[i], s[6]), s[7] = fmaf(S[i].w, qr[i], s[7]);
+        s[8] = fmaf(kr[i], qr[i], s[8]);
+    }
+#pragma unroll
+    for (int x = 8; x < 64; x <<= 1)
+#pragma unroll
+        for (int j = 0; j < 9; ++j) s[j] += __shfl_xor(s[j], x);
+    if (l < 8) {
+#pragma unroll
+        for (int j = 0; j < 9; ++j) red[w][l][j] = s[j];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 9; ++j)
+        s[j] = (red[0][cg][j] + red[1][cg][j]) + (red[2][cg][j] + red[3][cg][j]);
+    float u[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) u[e] = be * (vv[e] - s[e]);
+    if (rg == 0 && c0 < a.dv)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) rule::put(&out[e], fmaf(s[8], u[e], s[4 + e]));
     if (live)
 #pragma unroll
         for (int i = 0; i < kR; ++i)
-            *reinterpret_cast<float4 *>(a.S + sq.dst * slab + at + (size_t)i * a.dv) = S[i];
+            *reinterpret_cast<float4 *>(a.S + dst * slab + at + (size_t)i * a.dv) =
+                make_float4(fmaf(kr[i], u[0], S[i].x), fmaf(kr[i], u[1], S[i].y),
+                            fmaf(kr[i], u[2], S[i].z), fmaf(kr[i], u[3], S[i].w));
 }
 
 template <typename T, typename OT>

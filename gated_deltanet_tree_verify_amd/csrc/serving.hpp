@@ -13,7 +13,7 @@ constexpr int kFaultBadPage = 16;
 constexpr int kFaultBadGroup = 32;
 constexpr int kFaultNoPage = 64;
 
-// the gated delta rule over ragged sequences (cu null: one token each)
+// the gated delta rule over ragged sequences; the step has no cu: row b is sequence b's
 struct RuleArgs {
     const void *q, *k, *v;
     gdn_dtype dtype;
