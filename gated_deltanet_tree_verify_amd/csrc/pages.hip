@@ -114,10 +114,15 @@ __device__ int running_totals(int *upto, int m, int *s_part, F need) {
         __syncthreads();
         if (l == 63) s_part[w] = x;
         __syncthreads();
+        long long before = sum, all = sum;
+#pragma unroll
         for (int i = 0; i < kWaves; ++i) {
-            if (i == w && r < m) upto[r] = add_up(sum, x);
-            sum = add_up(sum, s_part[i]);
+            const int p = s_part[i];
+            before += i < w ? p : 0;
+            all += p;
         }
+        if (r < m) upto[r] = (int)min(before + x, (long long)kMany);
+        sum = (int)min(all, (long long)kMany);
     }
     __syncthreads();
     return sum;
