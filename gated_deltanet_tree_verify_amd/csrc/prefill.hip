@@ -47,7 +47,10 @@
 // 2^-23): the result is that of fp32 products.  Two parts were off by 2e-6 each (measured: 4.6e-6 in the
 // output's 2-norm), more than fp32 sums are.  fp32 q, k take the fp32 matrix
 // instruction.  g is summed in 64 bits: decays of late tokens are differences
-// of large sums.
+// of large sums.  The logarithms themselves are fp32's: one is off by 2^-23 of
+// itself at most, so a decay 2^-x by ln 2 2^-23 x 2^-x <= 2^-24.4, less than a
+// rounding of what it multiplies.  (In 64 bits the outputs' error was 1.38e-7
+// instead of 1.40e-7, and the chunk kernel 3 us slower.)
 #include "mfma_tile.hpp"
 #include "rule_common.hpp"
 
@@ -856,12 +859,15 @@ Layout layout(const RuleArgs &a) {
 // Four column groups a wave load a chunk's operands once for 64 columns; one
 // group gives four times the workgroups.  A chunk takes 3.9 us with four, 1.9
 // us with one, and a compute unit holds one workgroup of either.  32 heads of
-// d_v = 128, whole calls: 1 prompt of 2048 tokens 82 us with one group (152
-// with four), 2 prompts 160 (170), 3 prompts 236 (194), 4 prompts 312 (229);
-// sixteen prompts of 1 to 2049 tokens: scan 199 us with four groups, 323 with
-// one.  Lengths are device data: where one prompt is much longer than the
-// others (4096, 512, 512), one group is better (179, 292), and so four are
-// taken only from as many workgroups as there are compute units.
+// d_v = 128, whole calls, one group and four: 1 prompt of 2048 tokens 84 and
+// 149 us, 2 prompts 162 and 173, 3 prompts 263 and 207, 4 prompts 343 and 237,
+// 16 of 512 tokens 366 and 249.  Where one prompt is much longer than the
+// others, its own chain counts, and one group is better: 4096, 512, 512: 204
+// and 301; 8192 and three of one token: 355 and 587; 4096 and fifteen of 64:
+// 228 and 308.  Lengths are device data, so a rule on the batch cannot have all
+// of these right.  Four are taken from as many workgroups as there are compute
+// units, where equal prompts gain most: of the above, the three equal prompts
+// and the long ones beside three or more short ones get the slower form.
 bool wide_scan(const RuleArgs &a) {
     const long long wide = (long long)a.batch * a.H * ((a.dv + 4 * kCols - 1) / (4 * kCols));
     return wide >= device_cu_count();

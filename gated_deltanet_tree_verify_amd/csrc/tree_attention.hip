@@ -13,8 +13,14 @@
 // Work: a unit is (group, key head, 128 rows) over the shared tokens or
 // (sequence, key head, 128 rows) over its own tokens and tree nodes, cut into
 // tiles of 64 keys.  All units' tiles form one line, and workgroup i takes
-// the places [i c, (i + 1) c) of it, whatever units they belong to: every
-// workgroup has the same work for any mix of lengths.  Lengths are
+// the places [i c, (i + 1) c) of it, whatever units they belong to: workgroups
+// have the same work as long as no unit is cut into more parts than there is
+// room for partials (Layout: grid / units + 2 a row).  One context that is much
+// longer than the others of a batch with many rows passes that: c grows until
+// it fits, and the line ends before the last workgroups (64-node trees, 43000
+// tokens in all: 16 equal contexts 108 us, one of 32768 and 15 of 700 505 us;
+// 77000 tokens: 64 equal ones 229 us, one of 32768 and 63 of 700 1525 us; with
+// one token a sequence 69 and 86 us).  Lengths are
 // device data, so every workgroup forms the line's prefix sums by itself (a
 // scan over the batch).  Each unit a workgroup meets leaves one partial
 // (m, l, o) in the workspace; a second kernel joins a row's partials.
@@ -790,7 +796,12 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
                 }
                 // weights rounded to the operand type: half a step each
                 // (2^-8 or 2^-11 of a weight at most, and for fp16 2^-37 of the
-                // largest), independent over the keys
+                // largest), independent over the keys.  That is as much as
+                // the rounding of the outputs again: 0.0020 to 0.0023 of them
+                // in the 2-norm, 0.0017 without.  Two parts a weight would
+                // take it away for half as many products again (draft trees
+                // 126 -> 152 us, a shared prompt 63 -> 71 us), and where the
+                // second part is not positive, inf * weight would be NaN.
                 const vec p0 = E::round8(p), p1 = E::round8(p + 8);
                 auto times = [&](const uint32_t *y, f32x16 o) {
                     o = E::mma(__builtin_bit_cast(vec, make_uint4(y[0], y[1], y[2], y[3])), p0, o);

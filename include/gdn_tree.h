@@ -306,7 +306,7 @@ gdn_status gdn_tree_index(const int32_t *parent, int32_t *depth,
  * contents ignored; one call at a time may use it.
  * Arithmetic: products, sums and the state to fp32's precision (on the bf16
  * matrix unit the fp32 factors enter as three bf16 parts); decays from a
- * 64-bit sum of logarithms.
+ * 64-bit sum of fp32 logarithms.
  */
 int64_t gdn_prefill_workspace(gdn_dtype qkv_dtype, int batch, int rows, int H,
                               int Hk, int d_k, int d_v);
@@ -345,11 +345,11 @@ gdn_status gdn_step(const void *q, const void *k, const void *v,
  *   length [batch] int32, 0 <= length <= max_pages * page
  * Groups (optional, groups = 0 for none): sequences group_start[g] ..
  * group_start[g+1]-1 have their first group_shared[g] tokens in the same
- * pages; that part of the cache is read once for all of them.  The result
- * does not depend on the grouping.  Sequences before group_start[0] and from
- * group_start[groups] on share nothing; members shorter than the shared part
- * use what they have, and every member's entries are those of the group's
- * longest one within its own tokens.
+ * pages; that part of the cache is read once for all of them.  Groups change
+ * the result by roundings only (the softmax is split in other places).
+ * Sequences before group_start[0] and from group_start[groups] on share
+ * nothing; members shorter than the shared part use what they have, and every
+ * member's entries are those of the group's longest one within its own tokens.
  * Faults, per sequence (its out rows are NaN): GDN_FAULT_BAD_PARENT,
  * _BAD_LENGTH, _BAD_PAGE, _BAD_GROUP.
  * page is a power of two, d a multiple of 8 up to GDN_MAX_HEAD_DIM,
@@ -377,7 +377,9 @@ gdn_status gdn_tree_attention(const void *q, const void *k, const void *v,
  * Pages of a cache.  table [seqs][max_pages] int32 (page ids, -1 where
  * none), length [seqs] int32 tokens, ref [pool] int32: rows that hold a page,
  * 0 = free.  page (a power of two) tokens per page.  Free pages are handed
- * out lowest id first, requests are served in order.
+ * out lowest id first, requests are served in order.  fork, extend and compact
+ * read ref from id 0 up to the last free page that they need, compact all of it
+ * (1.5 to 2 us a thousand ids).
  *
  * gdn_page_fork: row dst[r] (empty: length 0) becomes a continuation of row
  * src[r]: its whole pages are shared (ref + 1), a last partial page gets a
