@@ -104,7 +104,6 @@ struct F16 {
 // one entry of the line: a group's shared tokens or a sequence's own
 struct Entry {
     int first;       // first sequence of its rows
-    int paged;       // sequence whose page row names its cached keys
     int rows;        // query rows per key head
     int pos0;        // cache position of key 0
     int cached;      // keys that are cached tokens
@@ -181,7 +180,6 @@ __device__ __forceinline__ Entry entry(const AttentionArgs &a, const Batch &y, i
     const int heads = a.Hq / a.Hkv;
     if (e < groups) {
         x.first = y.start[e];
-        x.paged = y.whole[e];
         x.rows = (y.start[e + 1] - y.start[e]) * a.n * heads;
         x.pos0 = 0;
         x.cached = y.shared[e];
@@ -190,7 +188,6 @@ __device__ __forceinline__ Entry entry(const AttentionArgs &a, const Batch &y, i
         const int b = e - groups, g = group_of(y.start, groups, b);
         const int len = y.length[b];
         x.first = b;
-        x.paged = b;
         x.rows = a.n * heads;
         x.pos0 = g < 0 ? 0 : min(len, y.shared[g]);
         x.cached = len - x.pos0;
@@ -304,26 +301,31 @@ __device__ __forceinline__ long long uniform(long long x) {
 }
 
 // a tile of the line
+template <bool kLooks>
 struct Cursor {
+    // looks the keys up: x.first is the sequence whose page row names them
+    static constexpr bool looks = kLooks;
     int e;               // entry
     int tile, rt, hk;    // tile of the unit, unit of the entry
     Entry x;
 };
 
+template <bool kLooks>
 __device__ __forceinline__ void seek(const AttentionArgs &a, const Batch &y, int groups,
-                                     int entries, Cursor &c, int e) {
+                                     int entries, Cursor<kLooks> &c, int e) {
     c.tile = c.rt = c.hk = 0;
     for (c.e = e; c.e < entries; ++c.e) {
         const Entry x = entry(a, y, groups, c.e);
-        c.x = {uniform(x.first), uniform(x.paged), uniform(x.rows),
-               uniform(x.pos0),  uniform(x.cached), uniform(x.keys),
-               uniform(x.tiles), uniform(x.row_tiles), uniform(x.weight)};
+        const int first = c.looks && c.e < groups ? y.whole[c.e] : x.first;
+        c.x = {uniform(first),   uniform(x.rows),  uniform(x.pos0),     uniform(x.cached),
+               uniform(x.keys),  uniform(x.tiles), uniform(x.row_tiles), uniform(x.weight)};
         if (c.x.tiles > 0 && c.x.row_tiles > 0) return;
     }
 }
 
+template <bool kLooks>
 __device__ __forceinline__ void advance(const AttentionArgs &a, const Batch &y, int groups,
-                                        int entries, Cursor &c) {
+                                        int entries, Cursor<kLooks> &c) {
     if (c.e >= entries || ++c.tile < c.x.tiles) return;
     c.tile = 0;
     if (++c.rt < c.x.row_tiles) return;
@@ -355,16 +357,16 @@ __device__ __forceinline__ unsigned long long address(const void *p) {
     return reinterpret_cast<unsigned long long>(p);
 }
 
-__device__ __forceinline__ void load_pages(const AttentionArgs &a, const Cursor &c, int key,
+__device__ __forceinline__ void load_pages(const AttentionArgs &a, const Cursor<true> &c, int key,
                                            int *to) {
     const int pos = c.x.pos0 + c.tile * kKeys + key;
-    const int32_t *from = a.pages + (size_t)c.x.paged * a.max_pages +
+    const int32_t *from = a.pages + (size_t)c.x.first * a.max_pages +
                           min(pos >> a.page_log, a.max_pages - 1);
     __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
                                      (__attribute__((address_space(3))) void *)to, 4, 0, 0);
 }
 
-__device__ __forceinline__ void put_rows(const AttentionArgs &a, const Bases &y, const Cursor &c,
+__device__ __forceinline__ void put_rows(const AttentionArgs &a, const Bases &y, const Cursor<true> &c,
                                          int key, const int *pages, Rows &rows) {
     const int j = c.tile * kKeys + key, pos = c.x.pos0 + j, tj = j - c.x.cached;
     const int page = pages[key];
@@ -534,7 +536,8 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
 
     // the tile that is computed (its place on the line and its unit's, its
     // number in this workgroup), and the one whose rows this wave looks up
-    Cursor cur, ahead;
+    Cursor<false> cur;
+    Cursor<true> ahead;
     long long t, v0;
     int ti = 0;
     {
@@ -551,7 +554,8 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
             cur.tile = cur.x.tiles - 1;
             advance(a, bat, groups, entries, cur);
         }
-        ahead = cur;
+        ahead = {cur.e, cur.tile, cur.rt, cur.hk, cur.x};
+        if (cur.e < groups) ahead.x.first = uniform((int)bat.whole[cur.e]);
         t = cur.e < entries ? v0 + cur.x.weight * (kUnit + cur.tile) : t1;
     }
     if (t >= t1) return;               // places without a tile
