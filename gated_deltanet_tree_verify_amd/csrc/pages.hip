@@ -143,8 +143,9 @@ struct Forks : Requests {
     int last[GDN_MAX_REQUESTS];       // the page of its own, -1: none
 };
 // Rows that a wave takes at once: their loads do not wait for each other (64
-// forks of 1000 to 2000 tokens: 11 to 12 us, one row at a time 13 to 15; 4 forks: 7
-// and 6.4 us, below the host's time for the calls around it).
+// forks of 1000 to 2000 tokens, medians of a kernel: 11.5 us, one row at a time
+// 14; 4 forks: 7 and 6.4 us, below the host's time for the calls around it; with
+// the check of sources 12 to 13.5 and 7.7 us).
 constexpr int kRowsAtOnce = 4;
 
 // A row that several requests would write goes to the first of them: each

@@ -18,9 +18,9 @@
 // room for partials (Layout: grid / units + 2 a row).  One context that is much
 // longer than the others of a batch with many rows passes that: c grows until
 // it fits, and the line ends before the last workgroups (64-node trees, 43000
-// tokens in all: 16 equal contexts 108 us, one of 32768 and 15 of 700 505 us;
-// 77000 tokens: 64 equal ones 229 us, one of 32768 and 63 of 700 1525 us; with
-// one token a sequence 69 and 86 us).  Lengths are
+// tokens in all, medians of whole calls: 16 equal contexts 108 us, one of 32768
+// and 15 of 700 505 us; 77000 tokens: 64 equal ones 229 us, one of 32768 and 63
+// of 700 1525 us; with one token a sequence 69 and 86 us).  Lengths are
 // device data, so every workgroup forms the line's prefix sums by itself (a
 // scan over the batch).  Each unit a workgroup meets leaves one partial
 // (m, l, o) in the workspace; a second kernel joins a row's partials.
@@ -35,6 +35,9 @@
 // rows, two waves and half the keys each; up to 32 rows (decoding), a wave has
 // half the keys and half the value columns, and the halves merge through LDS
 // at the unit's end.
+//
+// Times here are of this kernel, the shortest of 20 dispatches unless called
+// medians: those are 2 to 7 % above (draft trees 116 to 120, median 121 to 130).
 #include <type_traits>
 
 #include "device_common.hpp"
@@ -803,8 +806,8 @@ __global__ __launch_bounds__(kThreads, D > 128 ? 1 : 2) void attention_kernel(At
                 // largest), independent over the keys.  That is as much as
                 // the rounding of the outputs again: 0.0020 to 0.0023 of them
                 // in the 2-norm, 0.0017 without.  Two parts a weight would
-                // take it away for half as many products again (draft trees
-                // 126 -> 152 us, a shared prompt 63 -> 71 us), and where the
+                // take it away for half as many products again (medians: draft
+                // trees 126 -> 152 us, a shared prompt 63 -> 71 us), and where the
                 // second part is not positive, inf * weight would be NaN.
                 const vec p0 = E::round8(p), p1 = E::round8(p + 8);
                 auto times = [&](const uint32_t *y, f32x16 o) {
