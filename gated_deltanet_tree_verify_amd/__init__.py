@@ -29,6 +29,18 @@ Serving operators next to the tree calls:
     page_compact(table, length, ref, page)          -> (copies, count)
     page_copy(cache, copies, count)
     kv_commit(k_cache, v_cache, table, dst, begin, k, v, path, add)
+
+Between a model's projections and those:
+
+    rope_frequencies(rot, base, scaling)            -> (inv_freq, magnitude)
+    rope(q, k, pos, inv_freq)                       -> (q_out, k_out)   (gdn_rope)
+    qk_norm_rope(q, k, q_weight, k_weight, pos, inv_freq)
+                                                    -> (q_out, k_out)   (gdn_qk_norm_rope)
+    kv_append(k_cache, v_cache, table, dst, begin, k, v, cu)
+                                                    -> (q_out, k_out)   (gdn_kv_append)
+    count_prompt(counts, slot, cu, tokens)          -> counts
+    count_commit(counts, slot, tokens, path, add)   -> counts
+    adjust_logits(logits, counts, ...)              -> best  (gdn_adjust_logits)
 """
 from __future__ import annotations
 
@@ -40,6 +52,8 @@ import threading
 __all__ = ["load", "lib_path", "verify", "branch_verify", "commit", "commit_verify", "build_tree", "accept", "path", "Launch", "index", "status_string",
            "prefill", "step", "tree_attention", "page_fork", "page_extend", "page_free",
            "page_compact", "page_copy", "kv_commit",
+           "rope_frequencies", "rope", "qk_norm_rope", "kv_append", "count_prompt",
+           "count_commit", "adjust_logits",
            "FAULT_BAD_SLOT", "FAULT_BAD_LENGTH", "FAULT_BAD_PAGE", "FAULT_BAD_GROUP",
            "FAULT_NO_PAGE",
            "GdnError", "FAULT_BAD_PARENT", "FAULT_BAD_PATH", "DTYPE_F32", "DTYPE_BF16",
@@ -57,12 +71,12 @@ FAULT_BAD_GROUP = 32
 FAULT_NO_PAGE = 64
 DTYPE_F32 = 0
 DTYPE_BF16 = 1
-DTYPE_F16 = 2     # pseudo-values of commit_verify, tree_attention
+DTYPE_F16 = 2     # pseudo-values of commit_verify, tree_attention, rope and after
 MAX_NODES = 128
 MAX_DIM = 128
 MAX_CANDIDATES = 32
 # GDN_TREE_ABI_VERSION of include/gdn_tree.h that the signatures below follow
-ABI_VERSION = 9
+ABI_VERSION = 10
 
 _lock = threading.Lock()
 _lib = None
@@ -131,6 +145,24 @@ def load() -> ctypes.CDLL:
         lib.gdn_page_copy.argtypes = [P, P, P, I, I, I, L, P]
         lib.gdn_kv_commit.argtypes = [P, P, L, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I,
                                       P, P]
+        D = ctypes.c_double
+        lib.gdn_rope_frequencies.argtypes = [I, D, I, D, D, D, D, P, P]
+        lib.gdn_rope.argtypes = [P, L, L, P, L, L, I, P, P, I, P, I, I, F, P, L, L, P, L, L, I, I,
+                                 I, I, P]
+        lib.gdn_qk_norm_rope.argtypes = [P, L, L, P, L, L, I, I, F, F, P, L, P, L, I, P, P, I, P, I,
+                                         I, F, P, L, L, P, L, L, I, I, I, I, P]
+        lib.gdn_kv_append.argtypes = [P, P, L, P, P, P, P, P, L, L, P, L, L, P, L, L, I, I, F, F,
+                                      P, L, P, L, I, P, P, I, I, F, P, L, L, P, L, L, I, I, I, I,
+                                      I, I, I, I, I, P, P]
+        lib.gdn_count_prompt.argtypes = [P, L, P, P, P, I, I, I, I, P, P]
+        lib.gdn_count_commit.argtypes = [P, L, P, P, P, P, I, I, I, I, I, P, P]
+        lib.gdn_adjust_logits_workspace.argtypes = [I] * 3
+        lib.gdn_adjust_logits_workspace.restype = L
+        lib.gdn_adjust_logits.argtypes = [P, I, L, P, L, P, I, P, P, P, P, P, P, P, I, P, I, P, I,
+                                          L, P, I, I, I, P, L, P, P]
+        for fn in (lib.gdn_rope_frequencies, lib.gdn_rope, lib.gdn_qk_norm_rope, lib.gdn_kv_append,
+                   lib.gdn_count_prompt, lib.gdn_count_commit, lib.gdn_adjust_logits):
+            fn.restype = I
         for fn in (lib.gdn_prefill, lib.gdn_step, lib.gdn_tree_attention, lib.gdn_page_fork,
                    lib.gdn_page_extend, lib.gdn_page_free, lib.gdn_page_compact,
                    lib.gdn_page_copy, lib.gdn_kv_commit):
@@ -813,3 +845,391 @@ def kv_commit(k_cache, v_cache, table, dst, begin, k, v, path, add, status=None,
             table.shape[0], table.shape[1], num, page, status, _stream(stream))
     return _issue("gdn_kv_commit", native.gdn_kv_commit, args,
                   (k_cache, v_cache, table, dst, begin, k, v, path, add, status), None, prepare)
+
+
+# ---------------------------------------------------------------------------
+# between projections and attention, cache and acceptance
+# ---------------------------------------------------------------------------
+_SCALINGS = {None: 0, "linear": 1, "ntk": 2, "parts": 3, "yarn": 4}
+_NORMS = {None: 0, "rms": 1, "l2": 2}
+_LAYOUTS = {"half": 0, "interleaved": 1}
+
+
+def _choice(value, name, choices):
+    try:
+        return choices[value]
+    except (KeyError, TypeError):
+        raise ValueError(f"{name} must be one of {tuple(choices)}, not {value!r}") from None
+
+
+def rope_frequencies(rot, base=10000.0, scaling=None, factor=1.0, original=0, low=1.0, high=32.0,
+                     device="cuda"):
+    """gdn_rope_frequencies: (inv_freq, magnitude) of rotary positions over rot
+    elements of a head: an fp32 tensor [rot / 2] on the device, and the number
+    that rope's scale takes.  scaling: None, "linear", "ntk", "parts" or "yarn",
+    by `factor`; the last two leave pairs alone that turn `high` times or more
+    within the `original` context, and divide those that turn `low` times or
+    less.  Computed on the host: made once, kept by the program."""
+    torch = _torch()
+    kind = _choice(scaling, "scaling", _SCALINGS)
+    host = torch.empty(max(1, int(rot) // 2), dtype=torch.float32)
+    magnitude = ctypes.c_float()
+    _check("gdn_rope_frequencies", load().gdn_rope_frequencies(
+        int(rot), float(base), kind, float(factor), float(original), float(low), float(high),
+        host.data_ptr(), ctypes.addressof(magnitude)))
+    return host.to(device), magnitude.value
+
+
+def _dtype(t):
+    torch = _torch()
+    return {torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16}[t.dtype]
+
+
+def _rows(t, name, dtypes, tail):
+    """rows(t, dtypes, tail) of the native part, or what is wrong with t"""
+    got = _native_module.rows(t, dtypes, tail)
+    if got is None:
+        _explain_rows(t, name, dtypes, tail)
+    return got
+
+
+def _explain_rows(t, name, dtypes, tail):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if t.dim() < tail:
+        raise ValueError(f"{name} must have {tail} dimensions or more")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    raise ValueError(f"the leading dimensions of {name} must be one (a view with a single stride)")
+
+
+def _here(*tensors):
+    """the calls run on the current device: tensors of another are refused"""
+    device = _torch()._C._cuda_getDevice()
+    if not _native_module.on_device(device, *tensors):
+        raise ValueError(f"all tensors must be on the current device, cuda:{device}")
+
+
+def _out_like(out, t, name, stream):
+    """an output of t's shape: (tensor, row stride, head stride)"""
+    if out is None:
+        out = _empty(t.shape, t.dtype, t.device, stream)
+    got = _rows(out, name, (t.dtype,), 2)
+    if out.shape != t.shape:
+        raise ValueError(f"{name} has shape {tuple(out.shape)}, expected {tuple(t.shape)}")
+    return out, got[1], got[3]
+
+
+def _norm_weight(w, name, dtype, heads, d):
+    """(weight, head stride) of weights [d] or [heads][d]"""
+    torch = _torch()
+    if w is None:
+        return None, 0
+    _need(w, name, (dtype, torch.float32))
+    if w.shape == (d,):
+        return w, 0
+    if w.shape == (heads, d):
+        return w, d
+    raise ValueError(f"{name} has shape {tuple(w.shape)}, expected [{d}] or [{heads}][{d}]")
+
+
+def _weights(q_weight, k_weight, norm, q, Hq, Hk, d):
+    torch = _torch()
+    if norm == 0 and (q_weight is not None or k_weight is not None):
+        raise ValueError("weights belong to a norm")
+    wq, wq_head = _norm_weight(q_weight, "q_weight", q.dtype, Hq, d)
+    wk, wk_head = _norm_weight(k_weight, "k_weight", q.dtype, Hk, d)
+    given = wq if wq is not None else wk
+    if wq is not None and wk is not None and wq.dtype != wk.dtype:
+        raise TypeError("q_weight and k_weight must share a dtype")
+    kind = DTYPE_F32 if given is None or given.dtype == torch.float32 else _dtype(given)
+    return wq, wq_head, wk, wk_head, kind
+
+
+def _rotation(inv_freq, d):
+    torch = _torch()
+    if inv_freq is None:
+        return 0
+    _need(inv_freq, "inv_freq", (torch.float32,))
+    if inv_freq.dim() != 1 or 2 * inv_freq.shape[0] > d:
+        raise ValueError("inv_freq must be [rot / 2] with rot at most the head size")
+    return 2 * inv_freq.shape[0]
+
+
+def _heads_call(name, q, k, norm, eps, offset, q_weight, k_weight, pos, base, inv_freq, layout,
+                scale, q_out, k_out, stream, prepare):
+    torch = _torch()
+    native = _native()
+    kinds = (torch.bfloat16, torch.float16, torch.float32)
+    rows, q_row, Hq, q_head, d = _rows(q, "q", kinds, 2)
+    lead = q.shape[:-2]
+    k_row = k_head = Hk = k_out_row = k_out_head = 0
+    if k is not None:
+        _, k_row, Hk, k_head, dk = _rows(k, "k", (q.dtype,), 2)
+        if k.shape[:-2] != lead or dk != d:
+            raise ValueError("k must be [...][key heads][d] with q's leading dimensions and d")
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    rot = _rotation(inv_freq, d)
+    lay = _choice(layout, "layout", _LAYOUTS)
+    base_rows = 1
+    if rot > 0 or name == "gdn_rope":
+        _need(pos, "pos", (torch.int32,), lead)
+        if base is not None:
+            _need(base, "base", (torch.int32,), lead[:1])
+            base_rows = max(1, rows // max(1, base.numel()))
+    elif pos is not None or base is not None:
+        raise ValueError("positions without inv_freq")
+    q_out, q_out_row, q_out_head = _out_like(q_out, q, "q_out", stream)
+    if k is not None:
+        k_out, k_out_row, k_out_head = _out_like(k_out, k, "k_out", stream)
+    wq, wq_head, wk, wk_head, w_dtype = _weights(q_weight, k_weight, norm, q, Hq, Hk, d)
+    _here(q, k, pos, base, inv_freq, wq, wk, q_out, k_out)
+    if name == "gdn_rope":
+        args = (q, q_row, q_head, k, k_row, k_head, _dtype(q), pos, base, base_rows, inv_freq, rot,
+                lay, float(scale), q_out, q_out_row, q_out_head, k_out, k_out_row, k_out_head, rows,
+                Hq, Hk, d, _stream(stream))
+    else:
+        args = (q, q_row, q_head, k, k_row, k_head, _dtype(q), norm, float(eps), float(offset), wq,
+                wq_head, wk, wk_head, w_dtype, pos, base, base_rows, inv_freq, rot, lay,
+                float(scale), q_out, q_out_row, q_out_head, k_out, k_out_row, k_out_head, rows, Hq,
+                Hk, d, _stream(stream))
+    return _issue(name, getattr(native, name), args,
+                  (q, k, pos, base, inv_freq, wq, wk, q_out, k_out), (q_out, k_out), prepare)
+
+
+def rope(q, k, pos, inv_freq, layout="half", scale=1.0, base=None, q_out=None, k_out=None,
+         stream=None, prepare=False):
+    """gdn_rope: rotary positions of queries and keys.
+
+    q [...][Hq][d], k [...][Hk][d] or None (bf16, fp16 or fp32; views of one
+    projection, for instance); pos int32 [...], counted from base int32 [the
+    first of these dimensions] where given; inv_freq fp32 [rot / 2] as from
+    rope_frequencies.  layout: pairs (i, i + rot / 2), "half", or (2 i, 2 i + 1),
+    "interleaved"; scale: the magnitude.  Negative positions turn back.
+    Returns (q_out, k_out); q_out may be q, k_out may be k.
+    """
+    return _heads_call("gdn_rope", q, k, 0, 0.0, 0.0, None, None, pos, base, inv_freq, layout,
+                       scale, q_out, k_out, stream, prepare)
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, pos=None, inv_freq=None, norm="rms", eps=1e-6,
+                 offset=0.0, layout="half", scale=1.0, base=None, q_out=None, k_out=None,
+                 stream=None, prepare=False):
+    """gdn_qk_norm_rope: norms of queries and keys for each head, and rope of
+    the result in the same pass.
+
+    norm: "rms" or "l2"; weights [d] or [heads][d] (the heads' dtype or fp32),
+    multiplied as offset + weight, or None; without inv_freq the norm alone.
+    Everything else as for rope.  Returns (q_out, k_out).
+    """
+    return _heads_call("gdn_qk_norm_rope", q, k, _choice(norm, "norm", _NORMS), eps, offset,
+                       q_weight, k_weight, pos, base, inv_freq, layout, scale, q_out, k_out, stream,
+                       prepare)
+
+
+def kv_append(k_cache, v_cache, table, dst, begin, k, v, cu=None, inv_freq=None, layout="half",
+              scale=1.0, pos=None, norm=None, eps=1e-6, offset=0.0, k_weight=None, q=None,
+              q_weight=None, q_out=None, k_out=None, status=None, stream=None, prepare=False):
+    """gdn_kv_append: a ragged batch's keys and values become tokens begin[r] ..
+    of the table's rows dst[r], keys normalised and rotated on the way.
+
+    k, v [...][Hkv][d]; request r owns the rows cu[r] .. cu[r+1] (cu int32
+    [m + 1]; None: one row each).  Positions are the tokens' places in their
+    rows, or pos int32 [rows].  norm None, "rms" or "l2"; without inv_freq no
+    rotation.  q [...][Hq][d]: the queries of the same rows, into q_out.
+    k_out: the keys once more, as tree_attention takes them.  Returns
+    (q_out, k_out), None where not asked for.
+    """
+    torch = _torch()
+    native = _native()
+    kinds = (torch.bfloat16, torch.float16, torch.float32)
+    rows, k_row, Hkv, k_head, d = _rows(k, "k", kinds, 2)
+    lead = k.shape[:-2]
+    _, v_row, _, v_head, _ = _rows(v, "v", (k.dtype,), 2)
+    if v.shape != k.shape:
+        raise ValueError("v must have k's shape")
+    num, page, stride = _need_cache(k_cache, v_cache, (k.dtype,), Hkv, d)
+    _need(table, "table", (torch.int32,))
+    if table.dim() != 2:
+        raise ValueError("table must be [seqs][max_pages]")
+    if cu is None:
+        m = rows
+    else:
+        _need(cu, "cu", (torch.int32,))
+        if cu.dim() != 1 or cu.shape[0] < 1:
+            raise ValueError("cu must be [m + 1]")
+        m = cu.shape[0] - 1
+    _need(dst, "dst", (torch.int32,), (m,))
+    _need(begin, "begin", (torch.int32,), (m,))
+    q_row = q_head = Hq = q_out_row = q_out_head = k_out_row = k_out_head = 0
+    if q is not None:
+        _, q_row, Hq, q_head, dq = _rows(q, "q", (k.dtype,), 2)
+        if q.shape[:-2] != lead or dq != d:
+            raise ValueError("q must be [...][heads][d] with k's leading dimensions and d")
+        q_out, q_out_row, q_out_head = _out_like(q_out, q, "q_out", stream)
+    elif q_out is not None or q_weight is not None:
+        raise ValueError("q_out and q_weight without q")
+    if k_out is not None:
+        k_out, k_out_row, k_out_head = _out_like(k_out, k, "k_out", stream)
+    rot = _rotation(inv_freq, d)
+    if pos is not None:
+        if rot == 0:
+            raise ValueError("positions without inv_freq")
+        _need(pos, "pos", (torch.int32,), lead)
+    kind = _choice(norm, "norm", _NORMS)
+    wq, wq_head, wk, wk_head, w_dtype = _weights(q_weight, k_weight, kind, k, Hq, Hkv, d)
+    if status is not None:
+        _need(status, "status", (torch.int32,), (m,))
+    _here(k_cache, v_cache, table, dst, begin, k, v, cu, inv_freq, pos, wk, q, wq, q_out, k_out,
+          status)
+    args = (k_cache, v_cache, stride, table, dst, begin, cu, q, q_row, q_head, k, k_row, k_head, v,
+            v_row, v_head, _dtype(k), kind, float(eps), float(offset), wq, wq_head, wk, wk_head,
+            w_dtype, pos, inv_freq, rot, _choice(layout, "layout", _LAYOUTS), float(scale), q_out,
+            q_out_row, q_out_head, k_out, k_out_row, k_out_head, m, rows, Hq, Hkv, d,
+            table.shape[0], table.shape[1], num, page, status, _stream(stream))
+    return _issue("gdn_kv_append", native.gdn_kv_append, args,
+                  (k_cache, v_cache, table, dst, begin, k, v, cu, inv_freq, pos, wk, q, wq, q_out,
+                   k_out, status), (q_out, k_out), prepare)
+
+
+def _need_counts(counts, slot):
+    torch = _torch()
+    slots, stride, vocab = _rows(counts, "counts", (torch.int16,), 1)
+    if counts.dim() != 2:
+        raise ValueError("counts must be [slots][vocab]")
+    _need(slot, "slot", (torch.int32,))
+    if slot.dim() != 1:
+        raise ValueError("slot must be [m]")
+    return slots, stride, vocab, slot.shape[0]
+
+
+def count_prompt(counts, slot, cu, tokens, status=None, stream=None, prepare=False):
+    """gdn_count_prompt: the rows slot[r] of the table counts int16
+    [slots][vocab] made anew from the prompts tokens[cu[r]] .. (int32); an empty
+    prompt clears its row.  Returns counts."""
+    torch = _torch()
+    native = _native()
+    slots, stride, vocab, m = _need_counts(counts, slot)
+    _need(cu, "cu", (torch.int32,), (m + 1,))
+    _need(tokens, "tokens", (torch.int32,))
+    if status is not None:
+        _need(status, "status", (torch.int32,), (m,))
+    _here(counts, slot, cu, tokens, status)
+    args = (counts, stride, slot, cu, tokens, m, tokens.numel(), slots, vocab, status,
+            _stream(stream))
+    return _issue("gdn_count_prompt", native.gdn_count_prompt, args,
+                  (counts, slot, cu, tokens, status), counts, prepare)
+
+
+def count_commit(counts, slot, tokens, path, add, status=None, stream=None, prepare=False):
+    """gdn_count_commit: the tokens of the accepted branches, nodes
+    path[r][: add[r]] of tokens int32 [m][n], counted in the rows slot[r] of
+    the table counts int16 [slots][vocab].  Returns counts."""
+    torch = _torch()
+    native = _native()
+    slots, stride, vocab, m = _need_counts(counts, slot)
+    _need(tokens, "tokens", (torch.int32,))
+    if tokens.dim() != 2 or tokens.shape[0] != m:
+        raise ValueError("tokens must be [m][n]")
+    _need(path, "path", (torch.int32,))
+    if path.dim() != 2 or path.shape[0] != m:
+        raise ValueError("path must be [m][max_path]")
+    _need(add, "add", (torch.int32,), (m,))
+    if status is not None:
+        _need(status, "status", (torch.int32,), (m,))
+    _here(counts, slot, tokens, path, add, status)
+    args = (counts, stride, slot, tokens, path, add, m, tokens.shape[1], path.shape[1], slots,
+            vocab, status, _stream(stream))
+    return _issue("gdn_count_commit", native.gdn_count_commit, args,
+                  (counts, slot, tokens, path, add, status), counts, prepare)
+
+
+def adjust_logits(logits, counts=None, slot=None, tokens=None, parent=None, repetition=None,
+                  presence=None, frequency=None, bias=None, mask=None, out=None, best=None,
+                  status=None, stream=None, workspace=None, prepare=False):
+    """gdn_adjust_logits: penalties, biases and grammar masks on the logits
+    [batch][n][vocab] (bf16, fp16 or fp32) of a draft tree, and each node's
+    greedy token: returns best int32 [batch][n], as accept takes it (-1 where
+    the mask leaves nothing), or None for best=False.
+
+    counts int16 [slots][vocab] with slot int32 [batch] (None: row b), and the
+    tree's own tokens, parent int32 [batch][n], say what has occurred;
+    repetition, presence, frequency fp32 [batch]; bias = (tokens int32
+    [batch][m], values fp32 [batch][m]); mask int32 [batch][1 or n]
+    [ceil(vocab / 32)], a bit for every token that may follow.  out: receives
+    the adjusted logits (in the logits' dtype or fp32; may be logits itself).
+    """
+    torch = _torch()
+    native = _native()
+    kinds = (torch.bfloat16, torch.float16, torch.float32)
+    _, row, vocab = _rows(logits, "logits", kinds, 1)
+    if logits.dim() != 3:
+        raise ValueError("logits must be [batch][n][vocab]")
+    batch, n = logits.shape[0], logits.shape[1]
+    slots = counts_row = 0
+    if counts is not None:
+        slots, counts_row, width = _rows(counts, "counts", (torch.int16,), 1)
+        if counts.dim() != 2 or width != vocab:
+            raise ValueError(f"counts must be [slots][{vocab}]")
+        if slot is not None:
+            _need(slot, "slot", (torch.int32,), (batch,))
+    elif slot is not None:
+        raise ValueError("slot without counts")
+    if (tokens is None) != (parent is None):
+        raise ValueError("tokens and parent belong together")
+    if tokens is not None:
+        _need(tokens, "tokens", (torch.int32,), (batch, n))
+        _need(parent, "parent", (torch.int32,), (batch, n))
+    for t, name in ((repetition, "repetition"), (presence, "presence"), (frequency, "frequency")):
+        if t is not None:
+            _need(t, name, (torch.float32,), (batch,))
+    bias_tok = bias_val = None
+    biases = 0
+    if bias is not None:
+        bias_tok, bias_val = bias
+        _need(bias_tok, "bias tokens", (torch.int32,))
+        if bias_tok.dim() != 2 or bias_tok.shape[0] != batch:
+            raise ValueError("bias tokens must be [batch][m]")
+        _need(bias_val, "bias values", (torch.float32,), bias_tok.shape)
+        biases = bias_tok.shape[1]
+    mask_rows = 0
+    if mask is not None:
+        _need(mask, "mask", (torch.int32,))
+        mask_rows = mask.shape[1] if mask.dim() == 3 else -1
+        if mask_rows not in (1, n) or tuple(mask.shape) != (batch, mask_rows, (vocab + 31) // 32):
+            raise ValueError(f"mask must be [{batch}][1 or {n}][{(vocab + 31) // 32}]")
+    out_row, out_dtype = 0, _dtype(logits)
+    if out is not None:
+        if not isinstance(out, torch.Tensor) or out.shape != logits.shape:
+            raise ValueError("out must be a tensor of the logits' shape")
+        _, out_row, _ = _rows(out, "out", (logits.dtype, torch.float32), 1)
+        out_dtype = _dtype(out)
+    if best is False:
+        best = workspace = None
+        size = 0
+    else:
+        if best is None:
+            best = _empty((batch, n), torch.int32, logits.device, stream)
+        _need(best, "best", (torch.int32,), (batch, n))
+        if workspace is None:
+            workspace = _empty(_workspace_bytes("gdn_adjust_logits_workspace", batch, n, vocab),
+                               torch.uint8, logits.device, stream)
+        else:
+            _need(workspace, "workspace", (torch.uint8,))
+        size = workspace.numel()
+    if status is not None:
+        _need(status, "status", (torch.int32,), (batch,))
+    _here(logits, counts, slot, tokens, parent, repetition, presence, frequency, bias_tok, bias_val,
+          mask, out, best, workspace, status)
+    args = (logits, _dtype(logits), row, counts, counts_row, slot, slots, tokens, parent,
+            repetition, presence, frequency, bias_tok, bias_val, biases, mask, mask_rows, out,
+            out_dtype, out_row, best, batch, n, vocab, workspace, size, status, _stream(stream))
+    return _issue("gdn_adjust_logits", native.gdn_adjust_logits, args,
+                  (logits, counts, slot, tokens, parent, repetition, presence, frequency, bias_tok,
+                   bias_val, mask, out, best, workspace, status), best, prepare)

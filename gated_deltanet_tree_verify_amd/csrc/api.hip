@@ -1,9 +1,11 @@
 // C-ABI front end of libgdntree.so: host-side argument validation, kernel
 // selection and asynchronous launch on the caller's stream.  The declared
 // contract (layouts, ownership, errors) is in include/gdn_tree.h.
+#include <math.h>
 #include <stdint.h>
 
 #include <atomic>
+#include <cmath>
 
 #include "serving.hpp"
 
@@ -50,6 +52,85 @@ gdn_status rule_status(const gdn::RuleArgs &a) {
 // threads of a launch are counted in 32 bits
 bool grid_ok(long long workgroups, long long threads) {
     return workgroups <= 0xffffffffLL / threads;
+}
+
+// ---- heads of queries and keys
+int64_t element_bytes(gdn_dtype t) { return t == GDN_DTYPE_F32 ? 4 : 2; }
+
+bool dtype_ok(gdn_dtype t) {
+    return t == GDN_DTYPE_F32 || t == GDN_DTYPE_BF16 || t == GDN_DTYPE_F16;
+}
+
+bool aligned_to(const void *p, int64_t bytes) {
+    return reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes == 0;
+}
+
+template <typename... P>
+bool all_aligned4(const P *...p) {
+    return (... && (!p || aligned_to(p, 4)));
+}
+
+// rows [rows][heads][d] to read: strides not negative, offsets in 63 bits
+bool strides_ok(int64_t row, int64_t head) {
+    return row >= 0 && head >= 0 && row <= (1LL << 40) && head <= (1LL << 40);
+}
+
+// and to write: no two elements in one place
+bool apart(int rows, int64_t row, int heads, int64_t head, int d) {
+    if (rows <= 1) return heads <= 1 || head >= d;
+    if (heads <= 1) return row >= d;
+    return (head >= d && row >= (heads - 1) * head + d) ||
+           (row >= d && head >= (rows - 1) * row + d);
+}
+
+gdn_status part_status(const gdn::HeadsPart &x, const gdn::HeadsArgs &a, bool out_needed) {
+    if (x.heads == 0) return GDN_OK;
+    if (!x.in || (out_needed && !x.out)) return GDN_ERR_INVALID_ARG;
+    const int64_t e = element_bytes(a.dtype);
+    if (!aligned_to(x.in, e) || !aligned_to(x.out, e) ||
+        !aligned_to(x.weight, a.wide_weight ? 4 : e))
+        return GDN_ERR_INVALID_ARG;
+    if (!strides_ok(x.in_row, x.in_head)) return GDN_ERR_INVALID_ARG;
+    if (x.out && (!strides_ok(x.out_row, x.out_head) ||
+                  !apart(a.rows, x.out_row, x.heads, x.out_head, a.d)))
+        return GDN_ERR_INVALID_ARG;
+    if (x.weight && x.weight_head != 0 && x.weight_head != a.d) return GDN_ERR_INVALID_ARG;
+    return GDN_OK;
+}
+
+// pointers are of no interest where there are no rows; `weight_dtype` as the caller gave it
+gdn_status heads_status(const gdn::HeadsArgs &a, gdn_dtype weight_dtype, bool own_positions,
+                        bool k_out_needed) {
+    if (!dtype_ok(a.dtype)) return GDN_ERR_INVALID_ARG;
+    if (a.norm != GDN_NORM_NONE && a.norm != GDN_NORM_RMS && a.norm != GDN_NORM_L2)
+        return GDN_ERR_INVALID_ARG;
+    if (a.layout != GDN_ROPE_HALF && a.layout != GDN_ROPE_INTERLEAVED) return GDN_ERR_INVALID_ARG;
+    if (a.norm != GDN_NORM_NONE && (a.q.weight || a.k.weight) && weight_dtype != a.dtype &&
+        weight_dtype != GDN_DTYPE_F32)
+        return GDN_ERR_INVALID_ARG;
+    if (a.rows < 0 || a.q.heads < 0 || a.k.heads < 0 || a.q.heads + (int64_t)a.k.heads < 1 ||
+        a.d < 1 || a.rot < 0 || a.rot > a.d || a.rot % 2 != 0)
+        return GDN_ERR_INVALID_ARG;
+    if (a.d > GDN_MAX_HEAD_DIM || a.q.heads > 65535 || a.k.heads > 65535)
+        return GDN_ERR_UNSUPPORTED;
+    if (a.base && a.base_rows < 1) return GDN_ERR_INVALID_ARG;
+    if (a.rows == 0) return GDN_OK;
+    if (a.rot > 0 && (!a.inv_freq || (own_positions && !a.pos))) return GDN_ERR_INVALID_ARG;
+    if (!all_aligned4(a.pos, a.base, a.inv_freq)) return GDN_ERR_INVALID_ARG;
+    gdn_status st = part_status(a.q, a, true);
+    if (st == GDN_OK) st = part_status(a.k, a, k_out_needed);
+    return st;
+}
+
+// pointers are of no interest where there are no requests
+gdn_status count_status(const gdn::CountArgs &a) {
+    if (a.m < 0 || a.slots < 1 || a.vocab < 1 || a.stride < a.vocab) return GDN_ERR_INVALID_ARG;
+    if (a.vocab > GDN_MAX_VOCAB || a.m > GDN_MAX_REQUESTS || a.stride > (1LL << 40))
+        return GDN_ERR_UNSUPPORTED;
+    if (a.m > 0 && (!a.counts || !a.slot || !aligned_to(a.counts, 2) ||
+                    !all_aligned4(a.slot, a.status)))
+        return GDN_ERR_INVALID_ARG;
+    return GDN_OK;
 }
 
 gdn_status page_status(const gdn::PageArgs &a, int m, int page) {
@@ -437,6 +518,184 @@ gdn_status gdn_kv_commit(void *k_cache, void *v_cache, int64_t page_stride, cons
                               v,       path,    add,         m,     n,          max_path, Hkv,
                               d,       elem_bytes, seqs,     max_pages, pool,   page_log, status};
     return from_hip(gdn::launch_kv_commit(a, static_cast<hipStream_t>(stream)));
+}
+
+gdn_status gdn_rope_frequencies(int rot, double base, gdn_rope_scaling scaling, double factor,
+                                double original, double low, double high, float *inv_freq,
+                                float *magnitude) {
+    if (!inv_freq || !magnitude || !all_aligned4(inv_freq, magnitude)) return GDN_ERR_INVALID_ARG;
+    if (rot < 2 || rot % 2 != 0 || !(base > 1.0) || !std::isfinite(base))
+        return GDN_ERR_INVALID_ARG;
+    if (rot > GDN_MAX_HEAD_DIM) return GDN_ERR_UNSUPPORTED;
+    if (scaling < GDN_ROPE_PLAIN || scaling > GDN_ROPE_YARN) return GDN_ERR_INVALID_ARG;
+    const bool parts = scaling == GDN_ROPE_PARTS || scaling == GDN_ROPE_YARN;
+    if (scaling != GDN_ROPE_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor)))
+        return GDN_ERR_INVALID_ARG;
+    if (scaling == GDN_ROPE_NTK && rot <= 2) return GDN_ERR_INVALID_ARG;
+    if (parts && (!(original > 0.0) || !std::isfinite(original) || !(low < high) ||
+                  !std::isfinite(high - low)))
+        return GDN_ERR_INVALID_ARG;
+    if (scaling == GDN_ROPE_NTK) base *= std::pow(factor, rot / (rot - 2.0));
+    for (int i = 0; i < rot / 2; ++i) {
+        double t = std::pow(base, -2.0 * i / rot);
+        if (scaling == GDN_ROPE_LINEAR) t /= factor;
+        if (parts) {
+            const double turns = original * t / (2 * M_PI);
+            const double g = std::fmin(std::fmax((turns - low) / (high - low), 0.0), 1.0);
+            t = g * t + (1 - g) * t / factor;
+        }
+        inv_freq[i] = static_cast<float>(t);
+    }
+    *magnitude = scaling == GDN_ROPE_YARN ? static_cast<float>(0.1 * std::log(factor) + 1) : 1.f;
+    return GDN_OK;
+}
+
+gdn_status gdn_qk_norm_rope(const void *q, int64_t q_row, int64_t q_head, const void *k,
+                            int64_t k_row, int64_t k_head, gdn_dtype dtype, gdn_norm norm,
+                            float eps, float offset, const void *q_weight, int64_t q_weight_head,
+                            const void *k_weight, int64_t k_weight_head, gdn_dtype weight_dtype,
+                            const int32_t *pos, const int32_t *base, int base_rows,
+                            const float *inv_freq, int rot, gdn_rope_layout layout, float scale,
+                            void *q_out, int64_t q_out_row, int64_t q_out_head, void *k_out,
+                            int64_t k_out_row, int64_t k_out_head, int rows, int Hq, int Hk, int d,
+                            void *stream) {
+    const gdn::HeadsArgs a{
+        {q, q_row, q_head, q_out, q_out_row, q_out_head, q_weight, q_weight_head, Hq},
+        {k, k_row, k_head, k_out, k_out_row, k_out_head, k_weight, k_weight_head, Hk},
+        dtype, weight_dtype == GDN_DTYPE_F32, norm, eps, offset, pos, base, base_rows, inv_freq,
+        rot, layout, scale, rows, d};
+    const gdn_status st = heads_status(a, weight_dtype, true, true);
+    if (st != GDN_OK || rows == 0) return st;
+    // a wave a row, or as many as share its heads
+    if (!grid_ok((long long)rows * gdn::heads_splits(rows, Hq + Hk), 64))
+        return GDN_ERR_UNSUPPORTED;
+    return from_hip(gdn::launch_heads(a, static_cast<hipStream_t>(stream)));
+}
+
+gdn_status gdn_rope(const void *q, int64_t q_row, int64_t q_head, const void *k, int64_t k_row,
+                    int64_t k_head, gdn_dtype dtype, const int32_t *pos, const int32_t *base,
+                    int base_rows, const float *inv_freq, int rot, gdn_rope_layout layout,
+                    float scale, void *q_out, int64_t q_out_row, int64_t q_out_head, void *k_out,
+                    int64_t k_out_row, int64_t k_out_head, int rows, int Hq, int Hk, int d,
+                    void *stream) {
+    return gdn_qk_norm_rope(q, q_row, q_head, k, k_row, k_head, dtype, GDN_NORM_NONE, 0.f, 0.f,
+                            nullptr, 0, nullptr, 0, GDN_DTYPE_F32, pos, base, base_rows, inv_freq,
+                            rot, layout, scale, q_out, q_out_row, q_out_head, k_out, k_out_row,
+                            k_out_head, rows, Hq, Hk, d, stream);
+}
+
+gdn_status gdn_kv_append(void *k_cache, void *v_cache, int64_t page_stride, const int32_t *table,
+                         const int32_t *dst, const int32_t *begin, const int32_t *cu,
+                         const void *q, int64_t q_row, int64_t q_head, const void *k, int64_t k_row,
+                         int64_t k_head, const void *v, int64_t v_row, int64_t v_head,
+                         gdn_dtype dtype, gdn_norm norm, float eps, float offset,
+                         const void *q_weight, int64_t q_weight_head, const void *k_weight,
+                         int64_t k_weight_head, gdn_dtype weight_dtype, const int32_t *pos,
+                         const float *inv_freq, int rot, gdn_rope_layout layout, float scale,
+                         void *q_out, int64_t q_out_row, int64_t q_out_head, void *k_out,
+                         int64_t k_out_row, int64_t k_out_head, int m, int rows, int Hq, int Hkv,
+                         int d, int seqs, int max_pages, int pool, int page, int32_t *status,
+                         void *stream) {
+    const gdn::AppendArgs a{
+        {{q, q_row, q_head, q_out, q_out_row, q_out_head, q_weight, q_weight_head, Hq},
+         {k, k_row, k_head, k_out, k_out_row, k_out_head, k_weight, k_weight_head, Hkv},
+         dtype, weight_dtype == GDN_DTYPE_F32, norm, eps, offset, pos, nullptr, 1, inv_freq, rot,
+         layout, scale, rows, d},
+        v, v_row, v_head, k_cache, v_cache, page_stride, table, dst, begin, cu, m, seqs, max_pages,
+        pool, log2_exact(page), status};
+    if (m < 0 || Hkv < 1 || seqs < 1 || max_pages < 1 || pool < 1 || page < 1)
+        return GDN_ERR_INVALID_ARG;
+    const gdn_status st = heads_status(a.h, weight_dtype, false, false);
+    if (st != GDN_OK) return st;
+    if (!cu && rows != m) return GDN_ERR_INVALID_ARG;
+    if (m == 0) return GDN_OK;
+    if (!k_cache || !v_cache || !table || !dst || !begin || (rows > 0 && !v))
+        return GDN_ERR_INVALID_ARG;
+    if (!aligned16(k_cache) || !aligned16(v_cache) || !all_aligned4(table, dst, begin, cu, status) ||
+        !aligned_to(v, element_bytes(dtype)) || !strides_ok(v_row, v_head))
+        return GDN_ERR_INVALID_ARG;
+    // tokens of a row and pages are counted in 32 bits
+    if (a.page_log < 0 || d % 8 != 0 || (long long)max_pages * page > GDN_MAX_TOKENS ||
+        (long long)Hkv * d > 0xffffffLL || pool > GDN_MAX_PAGES || m > GDN_MAX_REQUESTS)
+        return GDN_ERR_UNSUPPORTED;
+    if (page_stride % 8 != 0 || page_stride < (int64_t)Hkv * page * d) return GDN_ERR_INVALID_ARG;
+    if (!grid_ok((long long)rows * gdn::heads_splits(rows, Hq + 2 * Hkv) + m + 8, 64))
+        return GDN_ERR_UNSUPPORTED;
+    return from_hip(gdn::launch_kv_append(a, static_cast<hipStream_t>(stream)));
+}
+
+gdn_status gdn_count_prompt(int16_t *counts, int64_t stride, const int32_t *slot,
+                            const int32_t *cu, const int32_t *tokens, int m, int rows, int slots,
+                            int vocab, int32_t *status, void *stream) {
+    const gdn::CountArgs a{counts, stride, slot, m, slots, vocab, status};
+    const gdn_status st = count_status(a);
+    if (st != GDN_OK) return st;
+    if (rows < 0) return GDN_ERR_INVALID_ARG;
+    if (m == 0) return GDN_OK;
+    if (!cu || (rows > 0 && !tokens) || !all_aligned4(cu, tokens)) return GDN_ERR_INVALID_ARG;
+    return from_hip(
+        gdn::launch_count_prompt(a, cu, tokens, rows, static_cast<hipStream_t>(stream)));
+}
+
+gdn_status gdn_count_commit(int16_t *counts, int64_t stride, const int32_t *slot,
+                            const int32_t *tokens, const int32_t *path, const int32_t *add, int m,
+                            int n, int max_path, int slots, int vocab, int32_t *status,
+                            void *stream) {
+    const gdn::CountArgs a{counts, stride, slot, m, slots, vocab, status};
+    const gdn_status st = count_status(a);
+    if (st != GDN_OK) return st;
+    if (n < 1 || max_path < 1) return GDN_ERR_INVALID_ARG;
+    if (max_path > GDN_MAX_TOKENS) return GDN_ERR_UNSUPPORTED;
+    if (m == 0) return GDN_OK;
+    if (!tokens || !path || !add || !all_aligned4(tokens, path, add)) return GDN_ERR_INVALID_ARG;
+    return from_hip(gdn::launch_count_commit(a, tokens, path, add, n, max_path,
+                                             static_cast<hipStream_t>(stream)));
+}
+
+int64_t gdn_adjust_logits_workspace(int batch, int n, int vocab) {
+    if (batch < 1 || n < 1 || n > GDN_MAX_NODES || vocab < 1 || vocab > GDN_MAX_VOCAB) return 0;
+    gdn::LogitsArgs a{};
+    a.batch = batch, a.n = n, a.vocab = vocab;
+    return gdn::logits_workspace(a);
+}
+
+gdn_status gdn_adjust_logits(const void *logits, gdn_dtype dtype, int64_t stride,
+                             const int16_t *counts, int64_t counts_stride, const int32_t *slot,
+                             int slots, const int32_t *tokens, const int32_t *parent,
+                             const float *repetition, const float *presence, const float *frequency,
+                             const int32_t *bias_tok, const float *bias, int bias_len,
+                             const int32_t *mask, int mask_rows, void *out, gdn_dtype out_dtype,
+                             int64_t out_stride, int32_t *best, int batch, int n, int vocab,
+                             void *workspace, int64_t workspace_bytes, int32_t *status,
+                             void *stream) {
+    if (!logits || (!out && !best) || !dtype_ok(dtype)) return GDN_ERR_INVALID_ARG;
+    if (out && out_dtype != dtype && out_dtype != GDN_DTYPE_F32) return GDN_ERR_INVALID_ARG;
+    if (batch < 1 || n < 1 || vocab < 1 || bias_len < 0 || stride < 0)
+        return GDN_ERR_INVALID_ARG;
+    if ((tokens != nullptr) != (parent != nullptr) || (bias_len > 0 && (!bias_tok || !bias)))
+        return GDN_ERR_INVALID_ARG;
+    if (counts && (slots < 1 || counts_stride < vocab)) return GDN_ERR_INVALID_ARG;
+    if (mask && mask_rows != 1 && mask_rows != n) return GDN_ERR_INVALID_ARG;
+    if (!aligned_to(logits, element_bytes(dtype)) ||
+        (out && !aligned_to(out, element_bytes(out_dtype))) || !aligned_to(counts, 2) ||
+        !aligned16(workspace) ||
+        !all_aligned4(slot, tokens, parent, repetition, presence, frequency, bias_tok, bias, mask,
+                      best, status))
+        return GDN_ERR_INVALID_ARG;
+    if (n > GDN_MAX_NODES || vocab > GDN_MAX_VOCAB || bias_len > GDN_MAX_BIASES ||
+        (long long)batch * n > 0x3ffffffLL || stride > (1LL << 40) || out_stride > (1LL << 40) ||
+        counts_stride > (1LL << 40))
+        return GDN_ERR_UNSUPPORTED;
+    if (out && (long long)batch * n > 1 && out_stride < vocab) return GDN_ERR_INVALID_ARG;
+    const gdn::LogitsArgs a{logits, dtype,    stride,    counts,     counts_stride, slot,
+                            slots,  tokens,   parent,    repetition, presence,      frequency,
+                            bias_tok, bias,   bias_len,  mask,       mask_rows,     out,
+                            out ? out_dtype : dtype,     out_stride, best,          batch,
+                            n,      vocab,    workspace, status};
+    if (best && (!workspace || workspace_bytes < gdn::logits_workspace(a)))
+        return GDN_ERR_INVALID_ARG;
+    if (!grid_ok(gdn::logits_units(a) + 8, 64)) return GDN_ERR_UNSUPPORTED;
+    return from_hip(gdn::launch_adjust_logits(a, static_cast<hipStream_t>(stream)));
 }
 
 const char *gdn_status_string(int status) {

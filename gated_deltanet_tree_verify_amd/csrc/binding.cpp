@@ -8,6 +8,9 @@
 //       tensor of one of the dtypes and of this shape (None: any); otherwise
 //       whatever the function given to explain() raises for the same arguments
 //   cache(t, dtypes, heads, d)   pages, page size and stride of a paged cache
+//   rows(t, dtypes, tail)   rows, their stride and the sizes and strides of the
+//       last `tail` dimensions of a GPU tensor whose leading ones are one
+//   on_device(index, ...)   whether all tensors given are on that GPU
 //   gdn_*(arguments of the C entry point)   its status; a pointer is an int,
 //       None or a tensor
 #define PY_SSIZE_T_CLEAN
@@ -107,6 +110,70 @@ PyObject *cache(PyObject *, PyObject *const *args, Py_ssize_t n) {
     Py_RETURN_NONE;
 }
 
+// rows(t, dtypes, tail): of a tensor [...][heads][d] (tail 2) or [...][d] (tail 1)
+// on the GPU whose d elements are adjacent and whose leading dimensions can be
+// walked with one stride, the numbers (rows, row stride, heads, head stride, d)
+// or (rows, row stride, d); None otherwise (also where its metadata raises).
+// The stride of a single row or head says nothing: a dense one is given.
+PyObject *rows(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    if (n != 3) {
+        PyErr_SetString(PyExc_TypeError, "rows(t, dtypes, tail)");
+        return nullptr;
+    }
+    const long long tail = PyLong_AsLongLong(args[2]);
+    if (PyErr_Occurred()) return nullptr;
+    if (!THPVariable_Check(args[0]) || !PyTuple_Check(args[1]) || tail < 1 || tail > 2)
+        Py_RETURN_NONE;
+    const at::Tensor &x = THPVariable_Unpack(args[0]);
+    long long count = 1, stride = 0, heads = 1, head = 0, d = 0;
+    const bool ok = guarded(false, [&] {
+        if (!x.is_cuda() || !known_dtype(x, args[1]) || x.dim() < tail) return false;
+        int64_t i = x.dim() - 1;
+        d = x.size(i);
+        if (d > 1 && x.stride(i) != 1) return false;
+        if (tail == 2) {
+            --i;
+            heads = x.size(i);
+            head = heads > 1 ? (long long)x.stride(i) : d;
+        }
+        stride = tail == 2 ? heads * head : d;
+        bool first = true;
+        for (--i; i >= 0; --i) {
+            const long long size = x.size(i);
+            if (size == 1) continue;
+            if (first) stride = x.stride(i);
+            else if (x.stride(i) != stride * count) return false;
+            first = false;
+            count *= size;
+        }
+        return true;
+    });
+    if (!ok) {
+        PyErr_Clear();
+        Py_RETURN_NONE;
+    }
+    return tail == 2 ? Py_BuildValue("LLLLL", count, stride, heads, head, d)
+                     : Py_BuildValue("LLL", count, stride, d);
+}
+
+// on_device(index, t, ...): whether every argument that is a tensor is on it
+PyObject *on_device(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    if (n < 1) {
+        PyErr_SetString(PyExc_TypeError, "on_device(index, ...)");
+        return nullptr;
+    }
+    const long long index = PyLong_AsLongLong(args[0]);
+    if (PyErr_Occurred()) return nullptr;
+    const bool ok = guarded(false, [&] {
+        for (Py_ssize_t i = 1; i < n; ++i)
+            if (THPVariable_Check(args[i]) && THPVariable_Unpack(args[i]).get_device() != index)
+                return false;
+        return true;
+    });
+    if (PyErr_Occurred()) return nullptr;
+    return PyBool_FromLong(ok);
+}
+
 PyObject *need(PyObject *, PyObject *const *args, Py_ssize_t n) {
     if (n < 3 || n > 4) {
         PyErr_SetString(PyExc_TypeError, "need(t, name, dtypes, shape=None)");
@@ -180,6 +247,8 @@ struct Entry<F> {
 PyMethodDef g_methods[] = {
     {"need", (PyCFunction)(void (*)(void))need, METH_FASTCALL, nullptr},
     {"cache", (PyCFunction)(void (*)(void))cache, METH_FASTCALL, nullptr},
+    {"rows", (PyCFunction)(void (*)(void))rows, METH_FASTCALL, nullptr},
+    {"on_device", (PyCFunction)(void (*)(void))on_device, METH_FASTCALL, nullptr},
     {"explain", explain, METH_O, nullptr},
     ENTRY(gdn_prefill),
     ENTRY(gdn_step),
@@ -190,6 +259,12 @@ PyMethodDef g_methods[] = {
     ENTRY(gdn_page_compact),
     ENTRY(gdn_page_copy),
     ENTRY(gdn_kv_commit),
+    ENTRY(gdn_rope),
+    ENTRY(gdn_qk_norm_rope),
+    ENTRY(gdn_kv_append),
+    ENTRY(gdn_count_prompt),
+    ENTRY(gdn_count_commit),
+    ENTRY(gdn_adjust_logits),
     {nullptr, nullptr, 0, nullptr},
 };
 

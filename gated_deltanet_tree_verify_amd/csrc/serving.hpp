@@ -60,6 +60,88 @@ struct KvCommitArgs {
     int32_t *status;
 };
 
+// queries or keys: rows [row][head][d], strides in elements; weights of the
+// norm (null: ones) with a stride of 0 where the heads share them
+struct HeadsPart {
+    const void *in;
+    int64_t in_row, in_head;
+    void *out;
+    int64_t out_row, out_head;
+    const void *weight;
+    int64_t weight_head;
+    int heads;
+};
+
+// norm and rotation of queries and keys; rot = 0: no rotation
+struct HeadsArgs {
+    HeadsPart q, k;
+    gdn_dtype dtype;
+    bool wide_weight;          // weights are fp32, not the heads' type
+    gdn_norm norm;
+    float eps, offset;
+    const int32_t *pos, *base; // base: one for every base_rows rows, or null
+    int base_rows;
+    const float *inv_freq;
+    int rot;
+    gdn_rope_layout layout;
+    float scale;
+    int rows, d;
+};
+
+// the same on the way into a cache; q may have no heads, k's output may be null
+struct AppendArgs {
+    HeadsArgs h;
+    const void *v;
+    int64_t v_row, v_head;
+    void *kc, *vc;
+    int64_t page_stride;
+    const int32_t *table, *dst, *begin, *cu;
+    int m, seqs, width, pool, page_log;
+    int32_t *status;
+};
+
+// waves that share a row's heads: a launch of few rows splits them, until there
+// are as many waves as the chip holds
+constexpr int heads_splits(int rows, int heads) {
+    if (heads < 1) return 1;
+    const int want = rows >= 8192 ? 1 : 8192 / (rows < 1 ? 1 : rows);
+    return want < heads ? want : heads;
+}
+
+// counts of tokens: rows of `vocab` int16 with a stride; low 15 bits the
+// occurrences in the output, the sign bit set where the prompt has the token
+struct CountArgs {
+    int16_t *counts;
+    int64_t stride;
+    const int32_t *slot;
+    int m, slots, vocab;
+    int32_t *status;
+};
+
+struct LogitsArgs {
+    const void *logits;
+    gdn_dtype dtype;
+    int64_t stride;
+    const int16_t *counts;
+    int64_t counts_stride;
+    const int32_t *slot;
+    int slots;
+    const int32_t *tokens, *parent;
+    const float *repetition, *presence, *frequency;
+    const int32_t *bias_tok;
+    const float *bias;
+    int bias_len;
+    const int32_t *mask;
+    int mask_rows;
+    void *out;
+    gdn_dtype out_dtype;
+    int64_t out_stride;
+    int32_t *best;
+    int batch, n, vocab;
+    void *workspace;
+    int32_t *status;
+};
+
 // workgroups of 256 threads: page_copy moves 16 KiB of a page in each (four
 // 16-byte pieces a thread), kv_commit 8 tokens of a request
 constexpr int kCopyThreads = 256, kCopyPieces = 4;
@@ -89,5 +171,14 @@ hipError_t launch_page_compact(const PageArgs &a, int32_t *copies, int32_t *coun
 hipError_t launch_page_copy(void *cache, const int32_t *copies, const int32_t *count, int m,
                             int planes, int pool, int64_t page_bytes, hipStream_t s);
 hipError_t launch_kv_commit(const KvCommitArgs &a, hipStream_t s);
+hipError_t launch_heads(const HeadsArgs &a, hipStream_t s);
+hipError_t launch_kv_append(const AppendArgs &a, hipStream_t s);
+hipError_t launch_count_prompt(const CountArgs &a, const int32_t *cu, const int32_t *tokens,
+                               int rows, hipStream_t s);
+hipError_t launch_count_commit(const CountArgs &a, const int32_t *tokens, const int32_t *path,
+                               const int32_t *add, int n, int max_path, hipStream_t s);
+int64_t logits_units(const LogitsArgs &a);       // waves of the launch
+int64_t logits_workspace(const LogitsArgs &a);
+hipError_t launch_adjust_logits(const LogitsArgs &a, hipStream_t s);
 
 }  // namespace gdn

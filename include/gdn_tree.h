@@ -53,15 +53,18 @@
 extern "C" {
 #endif
 
-#define GDN_TREE_ABI_VERSION 9
+#define GDN_TREE_ABI_VERSION 10
 #define GDN_MAX_NODES 128
 #define GDN_MAX_DIM 128
 #define GDN_MAX_CANDIDATES 32   /* child candidates per node, gdn_tree_build */
-#define GDN_MAX_HEAD_DIM 256    /* head size of gdn_tree_attention */
+#define GDN_MAX_HEAD_DIM 256    /* head size of gdn_tree_attention, gdn_rope, .. */
 #define GDN_MAX_SEQUENCES 512   /* batch and groups of gdn_tree_attention */
-#define GDN_MAX_REQUESTS 4096   /* requests of one page_fork / page_extend call */
+#define GDN_MAX_REQUESTS 4096   /* requests of one page_fork / page_extend /
+                                   kv_append / count call */
 #define GDN_MAX_TOKENS 0x3fffffff /* max_pages * page: tokens of a cache row */
 #define GDN_MAX_PAGES 0x3fffffff  /* pool of the page calls */
+#define GDN_MAX_VOCAB 0x1000000   /* tokens of a row of logits */
+#define GDN_MAX_BIASES 4096       /* biased tokens of a sequence */
 
 typedef enum {
     GDN_OK = 0,
@@ -73,6 +76,19 @@ typedef enum {
 /* element types: q/k/v take F32 or BF16; the pseudo-values of
    gdn_tree_commit_verify take F32 or F16 */
 typedef enum { GDN_DTYPE_F32 = 0, GDN_DTYPE_BF16 = 1, GDN_DTYPE_F16 = 2 } gdn_dtype;
+
+/* norms of queries and keys, and which elements of a head are a rotated pair:
+   (i, i + rot / 2) or (2 i, 2 i + 1) */
+typedef enum { GDN_NORM_NONE = 0, GDN_NORM_RMS = 1, GDN_NORM_L2 = 2 } gdn_norm;
+typedef enum { GDN_ROPE_HALF = 0, GDN_ROPE_INTERLEAVED = 1 } gdn_rope_layout;
+/* how frequencies are scaled for contexts longer than a model was trained for */
+typedef enum {
+    GDN_ROPE_PLAIN = 0,   /* not at all                                       */
+    GDN_ROPE_LINEAR = 1,  /* every frequency divided by the factor            */
+    GDN_ROPE_NTK = 2,     /* a larger base: only the slowest by the factor    */
+    GDN_ROPE_PARTS = 3,   /* slow ones by the factor, fast ones not at all    */
+    GDN_ROPE_YARN = 4     /* GDN_ROPE_PARTS, and a magnitude of 0.1 ln factor + 1 */
+} gdn_rope_scaling;
 
 /* device-detected fault flags (status[b]) */
 #define GDN_FAULT_BAD_PARENT 1 /* some parent[i] outside [-1, i)             */
@@ -439,6 +455,185 @@ gdn_status gdn_kv_commit(void *k_cache, void *v_cache, int64_t page_stride,
                          int max_path, int Hkv, int d, int elem_bytes,
                          int seqs, int max_pages, int pool, int page,
                          int32_t *status, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Between projections and attention, cache and acceptance.  In these entries
+ * a pointer is aligned to its element type (the caches to 16 bytes), rows of
+ * queries, keys and values may have any strides (in elements, >= 0; elements
+ * of a head are adjacent), and an output may be the input of the same shape
+ * and strides; outputs overlap nothing else, themselves included.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * Frequencies of rotary positions, on the HOST: inv_freq [rot / 2] radians a
+ * position and the magnitude that gdn_rope's scale takes.  With
+ * t_i = base^(-2 i / rot):
+ *   PLAIN  t_i          LINEAR  t_i / factor
+ *   NTK    t_i of the base  base factor^(rot / (rot - 2))     (rot > 2)
+ *   PARTS  a pair that turns n = original t_i / (2 pi) times in `original`
+ *          tokens: g t_i + (1 - g) t_i / factor with
+ *          g = (n - low) / (high - low), cut to [0, 1]
+ *   YARN   the same, magnitude 0.1 ln(factor) + 1 (1 elsewhere)
+ * (low = 1 and high = 32 are usual.)  Any other table can be used as well.
+ * Computed in 64 bits, rounded once.  2 <= rot <= GDN_MAX_HEAD_DIM, even;
+ * base > 1; factor >= 1; original, low, high (low < high) are read by PARTS
+ * and YARN only.
+ */
+gdn_status gdn_rope_frequencies(int rot, double base, gdn_rope_scaling scaling,
+                                double factor, double original, double low,
+                                double high, float *inv_freq,
+                                float *magnitude);
+
+/*
+ * Rotary positions.  Row r is at position p = pos[r] (+ base[r / base_rows],
+ * where base is not NULL); the pairs i of the first rot elements of every
+ * head of q and k are turned by the angle p inv_freq[i],
+ *   (x, y) -> scale (x cos - y sin, y cos + x sin),
+ * the other d - rot elements copied.  A negative position turns back.
+ *   q, q_out [rows][Hq][d], k, k_out [rows][Hk][d]  bf16, fp16 or fp32
+ * with strides *_row and *_head; Hq or Hk may be 0 (its pointers are then
+ * ignored).  pos int32 [rows], base int32 [ceil(rows / base_rows)], inv_freq
+ * fp32 [rot / 2] (device memory).  0 <= rot <= d <= GDN_MAX_HEAD_DIM, rot
+ * even, rot = 0: a copy.
+ * Arithmetic: the angle is the product of position and frequency, exact to
+ * 2^-53, reduced in 64 bits: far positions are as good as near ones.  cos, sin
+ * and the turn in fp32, one rounding of the result.
+ */
+gdn_status gdn_rope(const void *q, int64_t q_row, int64_t q_head,
+                    const void *k, int64_t k_row, int64_t k_head,
+                    gdn_dtype dtype, const int32_t *pos, const int32_t *base,
+                    int base_rows, const float *inv_freq, int rot,
+                    gdn_rope_layout layout, float scale, void *q_out,
+                    int64_t q_out_row, int64_t q_out_head, void *k_out,
+                    int64_t k_out_row, int64_t k_out_head, int rows, int Hq,
+                    int Hk, int d, void *stream);
+
+/*
+ * Norms of queries and keys for each head, and gdn_rope of the result in the
+ * same pass:
+ *   RMS  x / sqrt(mean x^2 + eps) (offset + w)
+ *   L2   x / sqrt(sum x^2 + eps) (offset + w)
+ * q_weight, k_weight: [d], or [H][d] with q_weight_head = d (0: one for all
+ * heads), in the heads' type or fp32 (weight_dtype); NULL: the factor
+ * (offset + w) is left out.  rot = 0 (pos and inv_freq are then ignored): the
+ * norm alone.  Squares are summed in fp32: values past 2^60 overflow the sum.
+ * GDN_NORM_NONE: gdn_rope.
+ */
+gdn_status gdn_qk_norm_rope(const void *q, int64_t q_row, int64_t q_head,
+                            const void *k, int64_t k_row, int64_t k_head,
+                            gdn_dtype dtype, gdn_norm norm, float eps,
+                            float offset, const void *q_weight,
+                            int64_t q_weight_head, const void *k_weight,
+                            int64_t k_weight_head, gdn_dtype weight_dtype,
+                            const int32_t *pos, const int32_t *base,
+                            int base_rows, const float *inv_freq, int rot,
+                            gdn_rope_layout layout, float scale, void *q_out,
+                            int64_t q_out_row, int64_t q_out_head, void *k_out,
+                            int64_t k_out_row, int64_t k_out_head, int rows,
+                            int Hq, int Hk, int d, void *stream);
+
+/*
+ * Keys and values appended to a paged cache, norm and rotation of the keys on
+ * the way, and of the queries beside them.  Request r owns the rows
+ * [cu[r], cu[r+1]) of q, k, v (cu int32 [m + 1]; NULL: row r, one token); they
+ * become the tokens begin[r], begin[r] + 1, .. of row dst[r] of the table, at
+ * the positions of the same number, or at pos[row] where pos is not NULL.
+ * Cache, table and begin as for gdn_kv_commit (gdn_page_extend makes the room
+ * and begin); norm, weights and rotation as above.  Keys are written to their
+ * pages and, where k_out is not NULL, to k_out; queries (Hq may be 0) to
+ * q_out.  Requests must not share tokens of a row.  Rows before cu[0] and from
+ * cu[m] on, and the rest of the cache, stay as they are.
+ * Faults, per request: GDN_FAULT_BAD_SLOT, _BAD_LENGTH (begin < -1, or the
+ * tokens pass the table's row), _BAD_PAGE: nothing of it goes to the cache and
+ * its rows of q_out and k_out are NaN; so for begin = -1, which is no fault.
+ * Where cu does not ascend within [0, rows] every request has _BAD_LENGTH and
+ * nothing is written.  m <= GDN_MAX_REQUESTS; d a multiple of 8.
+ */
+gdn_status gdn_kv_append(void *k_cache, void *v_cache, int64_t page_stride,
+                         const int32_t *table, const int32_t *dst,
+                         const int32_t *begin, const int32_t *cu,
+                         const void *q, int64_t q_row, int64_t q_head,
+                         const void *k, int64_t k_row, int64_t k_head,
+                         const void *v, int64_t v_row, int64_t v_head,
+                         gdn_dtype dtype, gdn_norm norm, float eps,
+                         float offset, const void *q_weight,
+                         int64_t q_weight_head, const void *k_weight,
+                         int64_t k_weight_head, gdn_dtype weight_dtype,
+                         const int32_t *pos, const float *inv_freq, int rot,
+                         gdn_rope_layout layout, float scale, void *q_out,
+                         int64_t q_out_row, int64_t q_out_head, void *k_out,
+                         int64_t k_out_row, int64_t k_out_head, int m,
+                         int rows, int Hq, int Hkv, int d, int seqs,
+                         int max_pages, int pool, int page, int32_t *status,
+                         void *stream);
+
+/*
+ * Counts of tokens, the table that gdn_adjust_logits reads: counts int16
+ * [slots][vocab], `stride` elements between rows.  The low 15 bits are a
+ * token's occurrences in a sequence's output (they stay at 32767 once there),
+ * the sign bit is set where its prompt has the token.
+ * gdn_count_prompt: row slot[r] is made anew from the prompt tokens
+ * [cu[r], cu[r+1]) (an empty prompt clears it).
+ * gdn_count_commit: the tokens[r][path[r][j]], j < add[r], of an accepted
+ * branch are counted in row slot[r]; tokens [m][n], path [m][max_path] as for
+ * gdn_kv_commit.
+ * Tokens outside the vocabulary are passed over.  status (optional, [m]):
+ * GDN_FAULT_BAD_SLOT (outside the table, or named by an earlier request of the
+ * call), _BAD_LENGTH (cu), _BAD_PATH; a request with a fault changes nothing.
+ * vocab <= GDN_MAX_VOCAB, m <= GDN_MAX_REQUESTS.
+ */
+gdn_status gdn_count_prompt(int16_t *counts, int64_t stride,
+                            const int32_t *slot, const int32_t *cu,
+                            const int32_t *tokens, int m, int rows, int slots,
+                            int vocab, int32_t *status, void *stream);
+gdn_status gdn_count_commit(int16_t *counts, int64_t stride,
+                            const int32_t *slot, const int32_t *tokens,
+                            const int32_t *path, const int32_t *add, int m,
+                            int n, int max_path, int slots, int vocab,
+                            int32_t *status, void *stream);
+
+/*
+ * Penalties for repeated tokens, biases and grammar masks on the logits of a
+ * draft tree (n = 1: one token), and each node's greedy token.  For sequence
+ * b, node i and token t, in fp32 with every step rounded:
+ *   c  = occurrences of t in the table's row and among tokens[b][j], j on the
+ *        path root .. i
+ *   z1 = z, where c = 0 and t is not in the prompt, else z / rep (z > 0) or
+ *        z rep
+ *   z' = z1 + (bias(t) - (freq c + pres)), the bracket without its second
+ *        term where c = 0
+ *   z' = -inf where the mask has no t
+ *   best[b][i] = the lowest t with the largest z'; -1 where no z' is above
+ *        -inf (a NaN is never the largest)
+ * logits [batch][n][vocab], bf16, fp16 or fp32, `stride` elements between
+ * rows; out (may be NULL) the z' in out_dtype (the logits' or fp32), rows of
+ * out_stride; best (may be NULL, but not both).  Optional, NULL where absent:
+ *   counts  the table above, row slot[b] (slot NULL: row b)
+ *   tokens, parent [batch][n]   the tree; n > 1 without: no paths
+ *   repetition, presence, frequency [batch] fp32
+ *   bias_tok int32, bias fp32 [batch][bias_len]: several entries of a token add
+ *           up in order, entries outside the vocabulary are passed over
+ *   mask [batch][mask_rows][ceil(vocab / 32)] int32, mask_rows 1 or n: bit
+ *           t % 32 of word t / 32 is set where t is allowed
+ * Faults, per sequence (its out rows are NaN, its best -1):
+ * GDN_FAULT_BAD_PARENT, _BAD_SLOT.
+ * workspace: gdn_adjust_logits_workspace(...) bytes, 16-byte aligned, contents
+ * ignored; one call at a time may use it (best = NULL: none).
+ */
+int64_t gdn_adjust_logits_workspace(int batch, int n, int vocab);
+gdn_status gdn_adjust_logits(const void *logits, gdn_dtype dtype,
+                             int64_t stride, const int16_t *counts,
+                             int64_t counts_stride, const int32_t *slot,
+                             int slots, const int32_t *tokens,
+                             const int32_t *parent, const float *repetition,
+                             const float *presence, const float *frequency,
+                             const int32_t *bias_tok, const float *bias,
+                             int bias_len, const int32_t *mask, int mask_rows,
+                             void *out, gdn_dtype out_dtype,
+                             int64_t out_stride, int32_t *best, int batch,
+                             int n, int vocab, void *workspace,
+                             int64_t workspace_bytes, int32_t *status,
+                             void *stream);
 
 /* human-readable text for a gdn_status value (never NULL) */
 const char *gdn_status_string(int status);
