@@ -567,7 +567,7 @@ gdn_status gdn_qk_norm_rope(const void *q, int64_t q_row, int64_t q_head, const 
     const gdn_status st = heads_status(a, weight_dtype, true, true);
     if (st != GDN_OK || rows == 0) return st;
     // a wave a row, or as many as share its heads
-    if (!grid_ok((long long)rows * gdn::heads_splits(rows, Hq + Hk), 64))
+    if (!grid_ok(((long long)rows + 3) * gdn::heads_splits(rows, Hq + Hk), 64))
         return GDN_ERR_UNSUPPORTED;
     return from_hip(gdn::launch_heads(a, static_cast<hipStream_t>(stream)));
 }
@@ -619,7 +619,7 @@ gdn_status gdn_kv_append(void *k_cache, void *v_cache, int64_t page_stride, cons
         (long long)Hkv * d > 0xffffffLL || pool > GDN_MAX_PAGES || m > GDN_MAX_REQUESTS)
         return GDN_ERR_UNSUPPORTED;
     if (page_stride % 8 != 0 || page_stride < (int64_t)Hkv * page * d) return GDN_ERR_INVALID_ARG;
-    if (!grid_ok((long long)rows * gdn::heads_splits(rows, Hq + 2 * Hkv) + m + 8, 64))
+    if (!grid_ok(((long long)rows + 3) * gdn::heads_splits(rows, Hq + 2 * Hkv) + m + 3, 64))
         return GDN_ERR_UNSUPPORTED;
     return from_hip(gdn::launch_kv_append(a, static_cast<hipStream_t>(stream)));
 }

@@ -169,8 +169,315 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int spli
     }
 }
 
+// ---------------------------------------------------------------------------
+// The same in 16-byte pieces: a lane has two pieces of 8 elements of a head, and
+// 64 / lanes(d) heads lie side by side in a wave, so that every load and store
+// of a wave covers whole lines.  In the half layout the two pieces are the two
+// sides of 8 pairs: no lane needs another's elements but for the norm's sum.
+// Angles are a row's, not a head's: each is formed by one lane, once, and
+// handed to the lanes that need it through LDS.
+// ---------------------------------------------------------------------------
+struct Lanes {
+    int log;             // lanes of a head: 1 << log
+    int groups, splits;  // groups of heads that a wave takes at once, and waves that share them
+    int rows;            // rows of a wave, kWaves apart
+    int tiles;           // workgroups of one split: kWaves * rows rows each
+};
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+// 8 adjacent elements as they lie in memory
+template <typename E>
+struct Raw {
+    uint4 x;
+    __device__ __forceinline__ void load(const uint16_t *p) {
+        x = *reinterpret_cast<const uint4 *>(p);
+    }
+    __device__ __forceinline__ void widen(float (&y)[8]) const {
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            y[2 * i] = E::widen((uint16_t)(w[i] & 0xffffu));
+            y[2 * i + 1] = E::widen((uint16_t)(w[i] >> 16));
+        }
+    }
+    __device__ __forceinline__ void narrow(const float (&y)[8]) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = E::bits(y[2 * i]) | (uint32_t)E::bits(y[2 * i + 1]) << 16;
+        x = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ __forceinline__ void store(uint16_t *p) const { *reinterpret_cast<uint4 *>(p) = x; }
+};
+template <>
+struct Raw<F32> {
+    f32x4 x, z;
+    __device__ __forceinline__ void load(const float *p) {
+        x = *reinterpret_cast<const f32x4 *>(p);
+        z = *reinterpret_cast<const f32x4 *>(p + 4);
+    }
+    __device__ __forceinline__ void widen(float (&y)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = x[i], y[4 + i] = z[i];
+    }
+    __device__ __forceinline__ void narrow(const float (&y)[8]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = y[i], z[i] = y[4 + i];
+    }
+    __device__ __forceinline__ void store(float *p) const {
+        *reinterpret_cast<f32x4 *>(p) = x;
+        *reinterpret_cast<f32x4 *>(p + 4) = z;
+    }
+};
+
+template <int kControl>
+__device__ __forceinline__ float lane_move(float x) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), kControl,
+                                                              0xf, 0xf, true));
+}
+
+// the sum over the 1 << log lanes of a head, in each of them
+__device__ __forceinline__ float head_sum(float s, int log) {
+    if (log > 0) s += lane_move<0xb1>(s);        // neighbour
+    if (log > 1) s += lane_move<0x4e>(s);        // the other two of four
+    if (log > 2) s += lane_move<0x141>(s);       // eight, mirrored
+    if (log > 3) s += lane_move<0x140>(s);       // sixteen, mirrored
+    return s;
+}
+
+__device__ __forceinline__ void turn8(float (&x)[8], float (&y)[8], const float2 (&cs)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float a = x[i], b = y[i];
+        x[i] = fmaf(a, cs[i].x, -(b * cs[i].y));
+        y[i] = fmaf(b, cs[i].x, a * cs[i].y);
+    }
+}
+
+__device__ __forceinline__ void turn4(float (&x)[8], const float2 *cs) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float a = x[2 * i], b = x[2 * i + 1];
+        x[2 * i] = fmaf(a, cs[i].x, -(b * cs[i].y));
+        x[2 * i + 1] = fmaf(b, cs[i].x, a * cs[i].y);
+    }
+}
+
+template <typename E>
+__device__ __forceinline__ void weigh(const HeadsArgs &g, float (&x)[8], const void *w, int64_t at,
+                                      float inv) {
+    float y[8];
+    if (g.wide_weight) {
+        Raw<F32> r;
+        r.load(static_cast<const float *>(w) + at);
+        r.widen(y);
+    } else {
+        Raw<E> r;
+        r.load(static_cast<const typename E::type *>(w) + at);
+        r.widen(y);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] *= inv * (g.offset + y[i]);
+}
+
+template <typename E, bool kAppend>
+__global__ __launch_bounds__(kThreads) void pieces_kernel(AppendArgs a, Lanes n) {
+    typedef typename E::type T;
+    __shared__ float2 s_turn[kWaves][GDN_MAX_HEAD_DIM / 2];
+    const HeadsArgs &g = a.h;
+    const int w = threadIdx.x >> 6, l = threadIdx.x & 63;
+    if (kAppend) {
+        const bool bad = a.cu && rows_bad(a);
+        const int r = ((int)blockIdx.x - n.tiles * n.splits) * kWaves + w;
+        if ((int)blockIdx.x >= n.tiles * n.splits) {
+            if (r >= a.m) return;
+            const int fault = bad ? kFaultBadLength
+                                  : request(a, r, a.cu ? a.cu[r + 1] - a.cu[r] : 1).fault;
+            if (l == 0) a.status[r] = fault;
+            return;
+        }
+        if (bad) return;
+    }
+    const int Hq = g.q.heads, Hk = g.k.heads, heads = Hq + (kAppend ? 2 : 1) * Hk;
+    const int half = g.rot >> 1, c = l & ((1 << n.log) - 1), per = 64 >> n.log;
+    // the lane's two pieces, whether they are in the head, and whether they turn
+    int at[2];
+    bool in[2], turns[2];
+    if (g.layout == GDN_ROPE_HALF) {
+        const int p = c - (half >> 3);
+        at[0] = p < 0 ? 8 * c : g.rot + 16 * p;
+        at[1] = p < 0 ? half + 8 * c : g.rot + 16 * p + 8;
+        turns[0] = turns[1] = p < 0;
+    } else {
+        at[0] = 8 * c, at[1] = 8 * (c + (1 << n.log));
+        turns[0] = at[0] < g.rot, turns[1] = at[1] < g.rot;
+    }
+    in[0] = at[0] < g.d, in[1] = at[1] < g.d;
+
+    const int tile = (int)blockIdx.x / n.splits, split = (int)blockIdx.x % n.splits;
+    Request q = {};
+    int r = 0, known = -1;
+    for (int j = 0; j < n.rows; ++j) {
+        const int row = (tile * n.rows + j) * kWaves + w;
+        if (row >= g.rows) break;
+        bool lost = false;
+        size_t cell = 0;
+        int64_t place;
+        if (kAppend) {
+            int t = 0, len = 1;
+            if (a.cu) {
+                if (row < a.cu[0]) continue;
+                if (row >= a.cu[a.m]) break;
+                r = find_request(a, r, row);
+                t = row - a.cu[r], len = a.cu[r + 1] - a.cu[r];
+            } else {
+                r = row;
+            }
+            if (r != known) q = request(a, r, len), known = r;
+            lost = q.fault || q.at < 0;
+            place = q.at + t;
+            if (!lost) {
+                const int p = a.table[(size_t)q.row * a.width + (place >> a.page_log)];
+                cell = (size_t)p * a.page_stride + (size_t)(place & ((1 << a.page_log) - 1)) * g.d;
+            }
+            if (g.pos) place = g.pos[row];
+        } else {
+            place = g.rot > 0 ? g.pos[row] : 0;
+            if (g.base && g.rot > 0) place += g.base[row / g.base_rows];
+        }
+        float2 cs[8] = {};
+        if (g.rot > 0) {
+            for (int i = l; i < half; i += 64) s_turn[w][i] = turn(place, g.inv_freq[i], g.scale);
+            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+            if (g.layout == GDN_ROPE_HALF) {
+                if (turns[0])
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) cs[i] = s_turn[w][8 * c + i];
+            } else {
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (turns[e])
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) cs[4 * e + i] = s_turn[w][at[e] / 2 + i];
+            }
+            __builtin_amdgcn_wave_barrier();
+        }
+        for (int group = split; group < n.groups; group += n.splits) {
+            const int h = group * per + (l >> n.log);
+            if (h >= heads) continue;
+            const bool isq = h < Hq, isv = kAppend && h >= Hq + Hk;
+            const int hx = isq ? h : isv ? h - Hq - Hk : h - Hq;
+            const HeadsPart &part = isq ? g.q : g.k;
+            const T *x = static_cast<const T *>(isv ? a.v : part.in) +
+                         row * (isv ? a.v_row : part.in_row) + hx * (isv ? a.v_head : part.in_head);
+            T *out = static_cast<T *>(isv ? nullptr : part.out);
+            if (out) out += row * part.out_row + hx * part.out_head;
+            T *page = nullptr;
+            if (kAppend && !isq && !lost)
+                page = static_cast<T *>(isv ? a.vc : a.kc) + cell +
+                       ((size_t)hx << a.page_log) * g.d;
+            Raw<E> raw[2] = {};
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (in[e]) raw[e].load(x + at[e]);
+            if (!isv) {
+                float y[2][8];
+                raw[0].widen(y[0]);
+                raw[1].widen(y[1]);
+                if (g.norm != GDN_NORM_NONE) {
+                    float s = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) s = fmaf(y[e][i], y[e][i], s);
+                    const float inv = inverse_norm(g, head_sum(s, n.log));
+                    if (part.weight) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if (in[e])
+                                weigh<E>(g, y[e], part.weight, hx * part.weight_head + at[e], inv);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) y[e][i] *= inv;
+                    }
+                }
+                if (g.layout == GDN_ROPE_HALF) {
+                    if (turns[0]) turn8(y[0], y[1], cs);
+                } else {
+                    if (turns[0]) turn4(y[0], &cs[0]);
+                    if (turns[1]) turn4(y[1], &cs[4]);
+                }
+                if (kAppend && lost)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) y[e][i] = __builtin_nanf("");
+                raw[0].narrow(y[0]);
+                raw[1].narrow(y[1]);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (in[e]) {
+                    if (out) raw[e].store(out + at[e]);
+                    if (page) raw[e].store(page + at[e]);
+                }
+        }
+    }
+}
+
+// whether rows, heads and weights are in 16-byte pieces, and the two sides of
+// the half layout's pairs in pieces of their own
+bool in_pieces(const HeadsArgs &a) {
+    const int step = a.dtype == GDN_DTYPE_F32 ? 4 : 8;
+    if (a.d % 8 != 0 || a.rot % (a.layout == GDN_ROPE_HALF ? 16 : 8) != 0) return false;
+    for (const HeadsPart *x : {&a.q, &a.k}) {
+        if (x->heads == 0) continue;
+        if (((uintptr_t)x->in | (uintptr_t)x->out | (uintptr_t)x->weight) % 16 != 0) return false;
+        if ((x->in_row | x->in_head) % step != 0) return false;
+        if (x->out && (x->out_row | x->out_head) % step != 0) return false;
+    }
+    return true;
+}
+
+bool in_pieces(const AppendArgs &a) {
+    const int step = a.h.dtype == GDN_DTYPE_F32 ? 4 : 8;
+    return in_pieces(a.h) && (uintptr_t)a.v % 16 == 0 && (a.v_row | a.v_head) % step == 0;
+}
+
+Lanes lanes(const HeadsArgs &a, int heads) {
+    const int need = a.layout == GDN_ROPE_HALF ? a.rot / 16 + (a.d - a.rot + 15) / 16
+                                               : (a.d + 15) / 16;
+    Lanes n{};
+    while (1 << n.log < need) ++n.log;
+    n.groups = (heads + (64 >> n.log) - 1) / (64 >> n.log);
+    n.splits = heads_splits(a.rows, n.groups);
+    n.rows = 1;
+    n.tiles = (a.rows + kWaves * n.rows - 1) / (kWaves * n.rows);
+    return n;
+}
+
+template <typename E, bool kAppend>
+void launch_pieces(const AppendArgs &a, hipStream_t s) {
+    const Lanes n = lanes(a.h, a.h.q.heads + (kAppend ? 2 : 1) * a.h.k.heads);
+    const int report = kAppend && a.status ? (a.m + kWaves - 1) / kWaves : 0;
+    const int blocks = n.tiles * n.splits + report;
+    if (blocks > 0)
+        hipLaunchKernelGGL((pieces_kernel<E, kAppend>), dim3((unsigned)blocks), dim3(kThreads), 0,
+                           s, a, n);
+}
+
 template <typename E>
 void launch_heads(const HeadsArgs &a, hipStream_t s) {
+    if (in_pieces(a)) {
+        AppendArgs x{};
+        x.h = a;
+        return launch_pieces<E, false>(x, s);
+    }
     const int splits = heads_splits(a.rows, a.q.heads + a.k.heads);
     const int64_t units = (int64_t)a.rows * splits;
     hipLaunchKernelGGL((heads_kernel<E>), dim3((unsigned)((units + kWaves - 1) / kWaves)),
@@ -179,6 +486,7 @@ void launch_heads(const HeadsArgs &a, hipStream_t s) {
 
 template <typename E>
 void launch_append(const AppendArgs &a, hipStream_t s) {
+    if (in_pieces(a)) return launch_pieces<E, true>(a, s);
     const int splits = heads_splits(a.h.rows, a.h.q.heads + 2 * a.h.k.heads);
     const int64_t units = (int64_t)a.h.rows * splits;
     const int blocks = (int)((units + kWaves - 1) / kWaves);
