@@ -171,17 +171,32 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int spli
 
 // ---------------------------------------------------------------------------
 // The same in 16-byte pieces: a lane has two pieces of 8 elements of a head, and
-// 64 / lanes(d) heads lie side by side in a wave, so that every load and store
-// of a wave covers whole lines.  In the half layout the two pieces are the two
-// sides of 8 pairs: no lane needs another's elements but for the norm's sum.
-// Angles are a row's, not a head's: each is formed by one lane, once, and
-// handed to the lanes that need it through LDS.
+// 64 / lanes(d) heads of queries, keys or values lie side by side in a wave, so
+// that its loads and stores cover whole lines.  In the half layout the two
+// pieces are the two sides of 8 pairs: no lane needs another's elements but for
+// the norm's sum.  Angles are a row's, not a head's: each is formed by one lane,
+// once, and handed to the lanes that need it through LDS.  The next heads are
+// loaded while the present ones are worked on, the first ones before the row's
+// place and angles are known.
 // ---------------------------------------------------------------------------
-struct Lanes {
-    int log;             // lanes of a head: 1 << log
-    int groups, splits;  // groups of heads that a wave takes at once, and waves that share them
+struct Part {
+    const void *in;
+    int64_t in_row, in_head;
+    void *out;           // null: not written
+    int64_t out_row, out_head;
+    const void *weight;  // null: ones
+    int64_t weight_head;
+    void *page;          // the cache that its heads go to, or null
+    int heads, before;   // its heads, and the groups of heads before its own
+};
+
+struct Pieces {
+    Part part[3];        // queries, keys, values (neither normalised nor turned)
+    AppendArgs a;
+    int log, need;       // lanes of a head: 1 << log, of which the first `need` have a part of it
+    int groups, splits;  // groups of heads, and the waves that share a row's
     int rows;            // rows of a wave, kWaves apart
-    int tiles;           // workgroups of one split: kWaves * rows rows each
+    int tiles;           // workgroups of one split, kWaves * rows rows each
 };
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -205,7 +220,7 @@ struct Raw {
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            w[i] = E::bits(y[2 * i]) | (uint32_t)E::bits(y[2 * i + 1]) << 16;
+            w[i] = E::two_bits(y[2 * i], y[2 * i + 1]);
         x = make_uint4(w[0], w[1], w[2], w[3]);
     }
     __device__ __forceinline__ void store(uint16_t *p) const { *reinterpret_cast<uint4 *>(p) = x; }
@@ -264,10 +279,10 @@ __device__ __forceinline__ void turn4(float (&x)[8], const float2 *cs) {
     }
 }
 
+// 8 weights, the offset added
 template <typename E>
-__device__ __forceinline__ void weigh(const HeadsArgs &g, float (&x)[8], const void *w, int64_t at,
-                                      float inv) {
-    float y[8];
+__device__ __forceinline__ void weigh(const HeadsArgs &g, const void *w, int64_t at,
+                                      float (&y)[8]) {
     if (g.wide_weight) {
         Raw<F32> r;
         r.load(static_cast<const float *>(w) + at);
@@ -278,13 +293,77 @@ __device__ __forceinline__ void weigh(const HeadsArgs &g, float (&x)[8], const v
         r.widen(y);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] *= inv * (g.offset + y[i]);
+    for (int i = 0; i < 8; ++i) y[i] += g.offset;
 }
 
-template <typename E, bool kAppend>
-__global__ __launch_bounds__(kThreads) void pieces_kernel(AppendArgs a, Lanes n) {
+// The lane's two pieces of a head.  Lanes past its end repeat its last piece and
+// lanes past the last head that head: they load, compute and store the same
+// bytes as another lane of their wave does, so that no access hides behind a
+// branch and the loads ahead stay in flight.  `own`: whether a piece counts in
+// the head's sum.
+struct Place {
+    int at[2];
+    bool own[2], turns[2];
+};
+
+template <bool kHalf>
+__device__ __forceinline__ Place place_of(const HeadsArgs &g, int lane, int need, int log) {
+    Place p;
+    const int c = min(lane, need - 1);
+    if (kHalf) {
+        const int rest = c - (g.rot >> 4);
+        p.at[0] = rest < 0 ? 8 * c : g.rot + 16 * rest;
+        p.at[1] = p.at[0] + (rest < 0 ? g.rot >> 1 : 8);
+        p.turns[0] = p.turns[1] = rest < 0;
+    } else {
+        p.at[0] = 8 * c, p.at[1] = 8 * (c + need);
+        p.turns[0] = p.at[0] < g.rot, p.turns[1] = p.at[1] < g.rot;
+    }
+    p.own[0] = lane < need, p.own[1] = lane < need && p.at[1] < g.d;
+    if (p.at[1] >= g.d) p.at[1] = p.at[0], p.turns[1] = p.turns[0];
+    return p;
+}
+
+// row's place in its request, and the cell of the cache that it goes to
+struct Row {
+    bool mine, lost;     // a request has it; the request is not served
+    int64_t place;
+    size_t cell;
+};
+
+struct Cursor {
+    Request q;
+    int r, known;
+};
+
+__device__ __forceinline__ Row find_row(const AppendArgs &a, int row, Cursor &c) {
+    Row x = {};
+    int t = 0, len = 1;
+    if (a.cu) {
+        if (row < a.cu[0] || row >= a.cu[a.m]) return x;
+        c.r = find_request(a, c.r, row);
+        t = row - a.cu[c.r], len = a.cu[c.r + 1] - a.cu[c.r];
+    } else {
+        c.r = row;
+    }
+    if (c.r != c.known) c.q = request(a, c.r, len), c.known = c.r;
+    x.mine = true;
+    x.lost = c.q.fault || c.q.at < 0;
+    const int place = c.q.at + t;
+    if (!x.lost) {
+        const int p = a.table[(size_t)c.q.row * a.width + (place >> a.page_log)];
+        x.cell = (size_t)p * a.page_stride + (size_t)(place & ((1 << a.page_log) - 1)) * a.h.d;
+    }
+    x.place = a.h.pos ? a.h.pos[row] : place;
+    return x;
+}
+
+template <typename E, bool kAppend, bool kHalf, bool kNorm>
+__global__ __launch_bounds__(kThreads) void pieces_kernel(Pieces n) {
     typedef typename E::type T;
     __shared__ float2 s_turn[kWaves][GDN_MAX_HEAD_DIM / 2];
+    __shared__ float s_weight[kNorm ? 2 : 1][kNorm ? GDN_MAX_HEAD_DIM : 1];
+    const AppendArgs &a = n.a;
     const HeadsArgs &g = a.h;
     const int w = threadIdx.x >> 6, l = threadIdx.x & 63;
     if (kAppend) {
@@ -299,134 +378,142 @@ __global__ __launch_bounds__(kThreads) void pieces_kernel(AppendArgs a, Lanes n)
         }
         if (bad) return;
     }
-    const int Hq = g.q.heads, Hk = g.k.heads, heads = Hq + (kAppend ? 2 : 1) * Hk;
-    const int half = g.rot >> 1, c = l & ((1 << n.log) - 1), per = 64 >> n.log;
-    // the lane's two pieces, whether they are in the head, and whether they turn
-    int at[2];
-    bool in[2], turns[2];
-    if (g.layout == GDN_ROPE_HALF) {
-        const int p = c - (half >> 3);
-        at[0] = p < 0 ? 8 * c : g.rot + 16 * p;
-        at[1] = p < 0 ? half + 8 * c : g.rot + 16 * p + 8;
-        turns[0] = turns[1] = p < 0;
-    } else {
-        at[0] = 8 * c, at[1] = 8 * (c + (1 << n.log));
-        turns[0] = at[0] < g.rot, turns[1] = at[1] < g.rot;
-    }
-    in[0] = at[0] < g.d, in[1] = at[1] < g.d;
-
+    const Place pl = place_of<kHalf>(g, l & ((1 << n.log) - 1), n.need, n.log);
+    const int mine = l >> n.log, per = 64 >> n.log;      // the lane's head of a group's
     const int tile = (int)blockIdx.x / n.splits, split = (int)blockIdx.x % n.splits;
-    Request q = {};
-    int r = 0, known = -1;
-    for (int j = 0; j < n.rows; ++j) {
-        const int row = (tile * n.rows + j) * kWaves + w;
-        if (row >= g.rows) break;
-        bool lost = false;
-        size_t cell = 0;
-        int64_t place;
-        if (kAppend) {
-            int t = 0, len = 1;
-            if (a.cu) {
-                if (row < a.cu[0]) continue;
-                if (row >= a.cu[a.m]) break;
-                r = find_request(a, r, row);
-                t = row - a.cu[r], len = a.cu[r + 1] - a.cu[r];
-            } else {
-                r = row;
+    const int keys = n.part[1].before, values = n.part[2].before;
+
+    auto head = [&](const Part &p, int group) {
+        return min((group - p.before) * per + mine, p.heads - 1);
+    };
+    // where there is no such group, 16 bytes of the last one: one line for the wave
+    auto load = [&](int row, int group, Raw<E> (&raw)[2]) {
+        const bool more = group < n.groups;
+        group = min(group, n.groups - 1);
+        const Part &p = n.part[group < keys ? 0 : group < values ? 1 : 2];
+        const T *x = static_cast<const T *>(p.in) + row * p.in_row;
+        const int64_t at = more ? head(p, group) * p.in_head + pl.at[0] : 0;
+        raw[0].load(x + at);
+        raw[1].load(x + at + (more ? pl.at[1] - pl.at[0] : 0));
+    };
+    auto store = [&](void *base, int64_t at, const Raw<E> (&raw)[2]) {
+        T *x = static_cast<T *>(base) + at;
+        raw[0].store(x + pl.at[0]);
+        raw[1].store(x + pl.at[1]);
+    };
+    auto position = [&](int row) {
+        if (g.rot == 0) return (int64_t)0;
+        return (int64_t)g.pos[row] + (g.base ? g.base[row / g.base_rows] : 0);
+    };
+
+    int row = tile * n.rows * kWaves + w;
+    Raw<E> next[2];
+    Row x = {true, false, 0, 0};
+    if (row < g.rows) {
+        load(row, split, next);
+        if (!kAppend) x.place = position(row);
+    }
+    if (kNorm) {
+        // weights that the heads share, the offset added; ones where there are none
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const Part &p = n.part[i];
+            for (int j = threadIdx.x; j < g.d; j += kThreads)
+                s_weight[i][j] = p.weight ? g.offset + weight_at<E>(p.weight, g.wide_weight, j) : 1.f;
+        }
+        __syncthreads();
+    }
+    Cursor c = {{}, 0, -1};
+    for (int j = 0; j < n.rows && row < g.rows; ++j, row += kWaves) {
+        if (j > 0) load(row, split, next);
+        if (kAppend) x = find_row(a, row, c);
+        else if (j > 0) x.place = position(row);
+        if (!x.mine) continue;
+        int group = split;
+        if (kAppend && x.lost) {       // the rows of a request that is not served: NaN
+            Raw<E> nan[2];
+            float y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = __builtin_nanf("");
+            nan[0].narrow(y), nan[1].narrow(y);
+            for (; group < values; group += n.splits) {
+                const Part &p = n.part[group < keys ? 0 : 1];
+                if (p.out) store(p.out, row * p.out_row + head(p, group) * p.out_head, nan);
             }
-            if (r != known) q = request(a, r, len), known = r;
-            lost = q.fault || q.at < 0;
-            place = q.at + t;
-            if (!lost) {
-                const int p = a.table[(size_t)q.row * a.width + (place >> a.page_log)];
-                cell = (size_t)p * a.page_stride + (size_t)(place & ((1 << a.page_log) - 1)) * g.d;
-            }
-            if (g.pos) place = g.pos[row];
-        } else {
-            place = g.rot > 0 ? g.pos[row] : 0;
-            if (g.base && g.rot > 0) place += g.base[row / g.base_rows];
+            continue;
         }
         float2 cs[8] = {};
         if (g.rot > 0) {
-            for (int i = l; i < half; i += 64) s_turn[w][i] = turn(place, g.inv_freq[i], g.scale);
+            for (int i = l; i < g.rot >> 1; i += 64)
+                s_turn[w][i] = turn(x.place, g.inv_freq[i], g.scale);
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
             __builtin_amdgcn_wave_barrier();
             __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-            if (g.layout == GDN_ROPE_HALF) {
-                if (turns[0])
+            if (kHalf) {
+                if (pl.turns[0])
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) cs[i] = s_turn[w][8 * c + i];
+                    for (int i = 0; i < 8; ++i) cs[i] = s_turn[w][pl.at[0] + i];
             } else {
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                    if (turns[e])
+                    if (pl.turns[e])
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) cs[4 * e + i] = s_turn[w][at[e] / 2 + i];
+                        for (int i = 0; i < 4; ++i) cs[4 * e + i] = s_turn[w][pl.at[e] / 2 + i];
             }
             __builtin_amdgcn_wave_barrier();
         }
-        for (int group = split; group < n.groups; group += n.splits) {
-            const int h = group * per + (l >> n.log);
-            if (h >= heads) continue;
-            const bool isq = h < Hq, isv = kAppend && h >= Hq + Hk;
-            const int hx = isq ? h : isv ? h - Hq - Hk : h - Hq;
-            const HeadsPart &part = isq ? g.q : g.k;
-            const T *x = static_cast<const T *>(isv ? a.v : part.in) +
-                         row * (isv ? a.v_row : part.in_row) + hx * (isv ? a.v_head : part.in_head);
-            T *out = static_cast<T *>(isv ? nullptr : part.out);
-            if (out) out += row * part.out_row + hx * part.out_head;
-            T *page = nullptr;
-            if (kAppend && !isq && !lost)
-                page = static_cast<T *>(isv ? a.vc : a.kc) + cell +
-                       ((size_t)hx << a.page_log) * g.d;
-            Raw<E> raw[2] = {};
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                if (in[e]) raw[e].load(x + at[e]);
-            if (!isv) {
-                float y[2][8];
-                raw[0].widen(y[0]);
-                raw[1].widen(y[1]);
-                if (g.norm != GDN_NORM_NONE) {
-                    float s = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) s = fmaf(y[e][i], y[e][i], s);
-                    const float inv = inverse_norm(g, head_sum(s, n.log));
-                    if (part.weight) {
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            if (in[e])
-                                weigh<E>(g, y[e], part.weight, hx * part.weight_head + at[e], inv);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) y[e][i] *= inv;
-                    }
-                }
-                if (g.layout == GDN_ROPE_HALF) {
-                    if (turns[0]) turn8(y[0], y[1], cs);
-                } else {
-                    if (turns[0]) turn4(y[0], &cs[0]);
-                    if (turns[1]) turn4(y[1], &cs[4]);
-                }
-                if (kAppend && lost)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) y[e][i] = __builtin_nanf("");
-                raw[0].narrow(y[0]);
-                raw[1].narrow(y[1]);
+        for (; group < values; group += n.splits) {
+            const Part &p = n.part[group < keys ? 0 : 1];
+            const int h = head(p, group);
+            float by[2][8];
+            if (kNorm && p.weight_head != 0) {
+                weigh<E>(g, p.weight, h * p.weight_head + pl.at[0], by[0]);
+                weigh<E>(g, p.weight, h * p.weight_head + pl.at[1], by[1]);
             }
+            const Raw<E> raw[2] = {next[0], next[1]};
+            load(row, group + n.splits, next);
+            float y[2][8];
+            raw[0].widen(y[0]);
+            raw[1].widen(y[1]);
+            if (kNorm) {
+                if (p.weight_head == 0)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
-                if (in[e]) {
-                    if (out) raw[e].store(out + at[e]);
-                    if (page) raw[e].store(page + at[e]);
-                }
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            by[e][i] = s_weight[group < keys ? 0 : 1][pl.at[e] + i];
+                float s = 0.f, z = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s = fmaf(y[0][i], y[0][i], s);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) z = fmaf(y[1][i], y[1][i], z);
+                s = (pl.own[0] ? s : 0.f) + (pl.own[1] ? z : 0.f);
+                const float inv = inverse_norm(g, head_sum(s, n.log));
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[e][i] *= inv * by[e][i];
+            }
+            if (kHalf) {
+                if (pl.turns[0]) turn8(y[0], y[1], cs);
+            } else {
+                if (pl.turns[0]) turn4(y[0], &cs[0]);
+                if (pl.turns[1]) turn4(y[1], &cs[4]);
+            }
+            Raw<E> done[2];
+            done[0].narrow(y[0]);
+            done[1].narrow(y[1]);
+            if (p.out) store(p.out, row * p.out_row + h * p.out_head, done);
+            if (kAppend && group >= keys)
+                store(p.page, x.cell + ((size_t)h << a.page_log) * g.d, done);
         }
+        if (kAppend)
+            for (; group < n.groups; group += n.splits) {
+                const Raw<E> raw[2] = {next[0], next[1]};
+                load(row, group + n.splits, next);
+                const Part &p = n.part[2];
+                store(p.page, x.cell + ((size_t)head(p, group) << a.page_log) * g.d, raw);
+            }
     }
 }
 
@@ -449,26 +536,50 @@ bool in_pieces(const AppendArgs &a) {
     return in_pieces(a.h) && (uintptr_t)a.v % 16 == 0 && (a.v_row | a.v_head) % step == 0;
 }
 
-Lanes lanes(const HeadsArgs &a, int heads) {
-    const int need = a.layout == GDN_ROPE_HALF ? a.rot / 16 + (a.d - a.rot + 15) / 16
-                                               : (a.d + 15) / 16;
-    Lanes n{};
-    while (1 << n.log < need) ++n.log;
-    n.groups = (heads + (64 >> n.log) - 1) / (64 >> n.log);
-    n.splits = heads_splits(a.rows, n.groups);
-    n.rows = 1;
-    n.tiles = (a.rows + kWaves * n.rows - 1) / (kWaves * n.rows);
-    return n;
+// Rows of a wave of kv_append.  Every wave checks its requests' pages, and its
+// workgroup all of cu, before it writes: a row each is best where that is little
+// (131072 rows of 48 heads of 128, 64 requests: 596 us, with eight rows 682), and
+// eight rows where it is more than a row's own bytes (one request in pages of 16:
+// 1235 and 778 us; 4096 requests: 923 and 702 us), as far as the chip stays full.
+int append_rows(const AppendArgs &a) {
+    const int64_t checks = ((int64_t)a.width + (a.cu ? 2 * a.m : 0)) / 1024;
+    const int64_t most = a.h.rows / 4096;
+    const int64_t rows = checks < most ? checks : most;
+    return rows < 1 ? 1 : rows > 16 ? 16 : (int)rows;
 }
 
 template <typename E, bool kAppend>
 void launch_pieces(const AppendArgs &a, hipStream_t s) {
-    const Lanes n = lanes(a.h, a.h.q.heads + (kAppend ? 2 : 1) * a.h.k.heads);
+    const HeadsArgs &g = a.h;
+    Pieces n{};
+    n.need = g.layout == GDN_ROPE_HALF ? g.rot / 16 + (g.d - g.rot + 15) / 16 : (g.d + 15) / 16;
+    while (1 << n.log < n.need) ++n.log;
+    n.a = a;
+    const HeadsPart v{a.v, a.v_row, a.v_head, nullptr, 0, 0, nullptr, 0, kAppend ? g.k.heads : 0};
+    void *const page[3] = {nullptr, a.kc, a.vc};
+    const HeadsPart *const from[3] = {&g.q, &g.k, &v};
+    for (int i = 0; i < 3; ++i) {
+        const HeadsPart &x = *from[i];
+        n.part[i] = {x.in, x.in_row, x.in_head, x.out, x.out_row, x.out_head, x.weight,
+                     x.weight_head, page[i], x.heads, n.groups};
+        n.groups += (x.heads + (64 >> n.log) - 1) / (64 >> n.log);
+    }
+    n.splits = heads_splits(g.rows, n.groups);
+    n.rows = kAppend ? append_rows(a) : 1;
+    n.tiles = (g.rows + kWaves * n.rows - 1) / (kWaves * n.rows);
     const int report = kAppend && a.status ? (a.m + kWaves - 1) / kWaves : 0;
     const int blocks = n.tiles * n.splits + report;
-    if (blocks > 0)
-        hipLaunchKernelGGL((pieces_kernel<E, kAppend>), dim3((unsigned)blocks), dim3(kThreads), 0,
-                           s, a, n);
+    if (blocks == 0) return;
+    const dim3 grid((unsigned)blocks), block(kThreads);
+    const bool half = g.layout == GDN_ROPE_HALF, norm = g.norm != GDN_NORM_NONE;
+    if (half && norm)
+        hipLaunchKernelGGL((pieces_kernel<E, kAppend, true, true>), grid, block, 0, s, n);
+    else if (half)
+        hipLaunchKernelGGL((pieces_kernel<E, kAppend, true, false>), grid, block, 0, s, n);
+    else if (norm)
+        hipLaunchKernelGGL((pieces_kernel<E, kAppend, false, true>), grid, block, 0, s, n);
+    else
+        hipLaunchKernelGGL((pieces_kernel<E, kAppend, false, false>), grid, block, 0, s, n);
 }
 
 template <typename E>

@@ -16,6 +16,11 @@ struct Bf16 {
     static __device__ __forceinline__ uint16_t bits(float x) {
         return __builtin_bit_cast(uint16_t, static_cast<__bf16>(x));
     }
+    static __device__ __forceinline__ uint32_t two_bits(float x, float y) {
+        typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+        return __builtin_bit_cast(uint32_t,
+                                  bf16x2{static_cast<__bf16>(x), static_cast<__bf16>(y)});
+    }
 };
 struct F16 {
     typedef uint16_t type;
@@ -24,6 +29,9 @@ struct F16 {
     }
     static __device__ __forceinline__ uint16_t bits(float x) {
         return __builtin_bit_cast(uint16_t, static_cast<_Float16>(x));
+    }
+    static __device__ __forceinline__ uint32_t two_bits(float x, float y) {
+        return bits(x) | (uint32_t)bits(y) << 16;
     }
 };
 struct F32 {
