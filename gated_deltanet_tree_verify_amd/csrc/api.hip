@@ -692,9 +692,9 @@ gdn_status gdn_adjust_logits(const void *logits, gdn_dtype dtype, int64_t stride
                             bias_tok, bias,   bias_len,  mask,       mask_rows,     out,
                             out ? out_dtype : dtype,     out_stride, best,          batch,
                             n,      vocab,    workspace, status};
-    if (best && (!workspace || workspace_bytes < gdn::logits_workspace(a)))
-        return GDN_ERR_INVALID_ARG;
-    if (!grid_ok(gdn::logits_units(a) + 8, 64)) return GDN_ERR_UNSUPPORTED;
+    const int64_t need = best ? gdn::logits_workspace(a) : 0;
+    if (need > 0 && (!workspace || workspace_bytes < need)) return GDN_ERR_INVALID_ARG;
+    if (!grid_ok(gdn::logits_threads(a), 1)) return GDN_ERR_UNSUPPORTED;
     return from_hip(gdn::launch_adjust_logits(a, static_cast<hipStream_t>(stream)));
 }
 

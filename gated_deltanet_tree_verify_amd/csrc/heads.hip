@@ -365,7 +365,8 @@ __global__ __launch_bounds__(kThreads) void pieces_kernel(Pieces n) {
     __shared__ float s_weight[kNorm ? 2 : 1][kNorm ? GDN_MAX_HEAD_DIM : 1];
     const AppendArgs &a = n.a;
     const HeadsArgs &g = a.h;
-    const int w = threadIdx.x >> 6, l = threadIdx.x & 63;
+    const int l = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);      // the same in all lanes
     if (kAppend) {
         const bool bad = a.cu && rows_bad(a);
         const int r = ((int)blockIdx.x - n.tiles * n.splits) * kWaves + w;

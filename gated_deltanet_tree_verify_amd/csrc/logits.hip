@@ -24,11 +24,71 @@ using heads::F16;
 using heads::F32;
 
 constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / 64;
+constexpr int kMostThreads = 512;              // of a workgroup of the logits
 constexpr int kLane = 8;                       // tokens of a lane
 constexpr int kSlice = 64 * kLane;             // and of a wave
-constexpr int kMarkTokens = 1 << 15;           // of a workgroup of count_prompt
+constexpr int kMarkTokens = 1 << 13;           // of a workgroup of count_prompt
 constexpr int kNone = 0x7fffffff;
+
+// 8 adjacent values as they lie in memory, at any address of their type
+struct __attribute__((packed, aligned(2))) Half8 {
+    uint32_t x[4];
+};
+struct __attribute__((packed, aligned(4))) Full8 {
+    float x[8];
+};
+
+template <typename E>
+struct Eight {
+    Half8 raw;
+    __device__ __forceinline__ void load(const uint16_t *p) {
+        raw = *reinterpret_cast<const Half8 *>(p);
+    }
+    __device__ __forceinline__ void load(const uint16_t *p, int n) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            raw.x[i] = (2 * i < n ? p[2 * i] : 0u) | (2 * i + 1 < n ? (uint32_t)p[2 * i + 1] : 0u)
+                                                        << 16;
+    }
+    __device__ __forceinline__ float at(int i) const {
+        return E::widen((uint16_t)(raw.x[i >> 1] >> (i & 1 ? 16 : 0)));
+    }
+    __device__ __forceinline__ void set(const float (&y)[kLane]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) raw.x[i] = E::two_bits(y[2 * i], y[2 * i + 1]);
+    }
+    __device__ __forceinline__ void store(uint16_t *p) const { *reinterpret_cast<Half8 *>(p) = raw; }
+    __device__ __forceinline__ void store(uint16_t *p, int n) const {
+#pragma unroll
+        for (int i = 0; i < kLane; ++i)
+            if (i < n) p[i] = (uint16_t)(raw.x[i >> 1] >> (i & 1 ? 16 : 0));
+    }
+};
+template <>
+struct Eight<F32> {
+    Full8 raw;
+    __device__ __forceinline__ void load(const float *p) {
+        raw = *reinterpret_cast<const Full8 *>(p);
+    }
+    __device__ __forceinline__ void load(const float *p, int n) {
+#pragma unroll
+        for (int i = 0; i < kLane; ++i) raw.x[i] = i < n ? p[i] : 0.f;
+    }
+    __device__ __forceinline__ float at(int i) const { return raw.x[i]; }
+    __device__ __forceinline__ void set(const float (&y)[kLane]) {
+#pragma unroll
+        for (int i = 0; i < kLane; ++i) raw.x[i] = y[i];
+    }
+    __device__ __forceinline__ void store(float *p) const { *reinterpret_cast<Full8 *>(p) = raw; }
+    __device__ __forceinline__ void store(float *p, int n) const {
+#pragma unroll
+        for (int i = 0; i < kLane; ++i)
+            if (i < n) p[i] = raw.x[i];
+    }
+};
+struct None {            // no output
+    typedef char type;
+};
 
 // ---------------------------------------------------------------------------
 // counts
@@ -43,27 +103,33 @@ __device__ __forceinline__ int slot_fault(const CountArgs &a, int r) {
 }
 
 // A workgroup makes one part of one row: a bit for every token of the part,
-// set by a pass over the prompt, then the row's values.
+// set by a pass over the prompt, then the row's values, 8 tokens a thread.
 __global__ __launch_bounds__(kThreads) void count_prompt_kernel(
     CountArgs a, const int32_t *__restrict__ cu, const int32_t *__restrict__ tokens, int rows) {
     __shared__ uint32_t s_bits[kMarkTokens / 32];
     const int r = blockIdx.x, tid = threadIdx.x;
     const int first = cu[r], end = cu[r + 1];
-    int fault = slot_fault(a, r);
+    for (int i = tid; i < kMarkTokens / 32; i += kThreads) s_bits[i] = 0;
+    int fault = slot_fault(a, r);                // a barrier: the bits are cleared
     if (first < 0 || end < first || end > rows) fault |= kFaultBadLength;
     if (a.status && blockIdx.y == 0 && tid == 0) a.status[r] = fault;
     if (fault) return;
     const int v0 = (int)blockIdx.y * kMarkTokens, n = min(kMarkTokens, a.vocab - v0);
-    for (int i = tid; i < (n + 31) / 32; i += kThreads) s_bits[i] = 0;
-    __syncthreads();
     for (int i = first + tid; i < end; i += kThreads) {
         const uint32_t t = (uint32_t)tokens[i] - (uint32_t)v0;
         if (t < (uint32_t)n) atomicOr(&s_bits[t >> 5], 1u << (t & 31));
     }
     __syncthreads();
-    int16_t *row = a.counts + a.slot[r] * a.stride + v0;
-    for (int i = tid; i < n; i += kThreads)
-        row[i] = (s_bits[i >> 5] >> (i & 31) & 1) ? (int16_t)-32768 : (int16_t)0;
+    uint16_t *row = reinterpret_cast<uint16_t *>(a.counts) + a.slot[r] * a.stride + v0;
+    for (int t = tid * kLane; t < n; t += kThreads * kLane) {
+        const uint32_t bits = s_bits[t >> 5] >> (t & 31);
+        Eight<Bf16> x;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            x.raw.x[k] = (bits >> 2 * k & 1) << 15 | (bits >> (2 * k + 1) & 1) << 31;
+        if (t + kLane <= n) x.store(row + t);
+        else x.store(row + t, n - t);
+    }
 }
 
 // A workgroup for every request; its first wave counts 64 tokens of the path
@@ -105,149 +171,342 @@ struct Best {
     int token;           // kNone: nothing above -inf
 };
 
-__device__ __forceinline__ void better(Best &x, float value, int token) {
-    if (value > x.value || (value == x.value && token < x.token)) x.value = value, x.token = token;
+__device__ __forceinline__ void better(Best &x, const Best &y) {
+    if (y.value > x.value || (y.value == x.value && y.token < x.token)) x = y;
 }
 
-__device__ __forceinline__ Best wave_best(Best x) {
+constexpr Best kNothing = {-__builtin_inff(), kNone};
+
+// How a launch is cut: `parts` workgroups share a node's row, each wave of them
+// takes `per` slices of 512 tokens, one after the other.
+struct Cut {
+    int slices, per, parts;
+    int threads;
+};
+
+// What a wave knows of its node.
+struct Node {
+    float rep, inverse;      // the repetition penalty, and its reciprocal
+    bool plain;              // far from the ends of fp32: a quotient by fused steps is exact
+    float pres, freq;
+    int token[2];            // of the nodes l and 64 + l, if they are on the node's path, or -1
+    int bias_tok;            // the first 64 biases stay in the lanes
+    float bias;
+};
+
+// z / rep for z above 0, z rep otherwise, correctly rounded.  With r the
+// rounded reciprocal and q = z r, the residue z - q rep is exact in a fused
+// step and q + residue r is the rounded quotient (Markstein), as long as
+// nothing leaves the range of normal numbers: 3 instructions instead of 12.
+__device__ __forceinline__ float repeated(const Node &n, float z) {
+    float q = z * n.inverse;
+    q = fmaf(fmaf(-q, n.rep, z), n.inverse, q);
+    // z in [2^-60, 2^60)
+    const bool usual = __float_as_uint(z) - 0x21800000u < 0x5d800000u - 0x21800000u;
+    if (z > 0.f && !(usual && n.plain)) q = z / n.rep;
+    return z > 0.f ? q : z * n.rep;
+}
+
+struct Running {
+    float value;             // the largest of a lane's groups of 8 tokens, the group's
+    int slice;               // slice, and what it is the largest of
+    float of[kLane];
+};
+
+// the bit of a lane's token e: those of a word's halves are 16 apart
+__device__ __forceinline__ constexpr uint32_t touch(int e) {
+    return 1u << ((e >> 1) + 16 * (e & 1));
+}
+
+// The lane's 8 tokens v0 + 8 l .. of a slice; kTail: of which only the first
+// `left` are in the row.
+template <typename E, typename O, bool kTail>
+__device__ __forceinline__ void slice_of(const LogitsArgs &a, const Node &n, int64_t bias0,
+                                         const Eight<E> &z, const Eight<Bf16> &count, uint32_t mask,
+                                         int slice, int left, void *out,
+                                         Running &best) {
+    const int l = threadIdx.x & 63, v0 = slice * kSlice;
+    float y[kLane];
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-        const float v = __shfl_xor(x.value, o);
-        const int t = __shfl_xor(x.token, o);
-        better(x, v, t);
+    for (int e = 0; e < kLane; ++e) y[e] = __builtin_canonicalizef(z.at(e));   // NaNs are quiet
+    auto count_at = [&](int e) { return count.raw.x[e >> 1] >> (e & 1 ? 16 : 0) & 65535u; };
+    auto inside = [&](int t) { return __ballot((uint32_t)t - (uint32_t)v0 < (uint32_t)kSlice); };
+    const uint64_t on_path[2] = {inside(n.token[0]), inside(n.token[1])};
+    const uint64_t biased = inside(n.bias_tok);
+    // tokens that anything is known of, a bit each (touch): those with a count first
+    uint32_t touched = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+        touched |= __builtin_bit_cast(uint32_t, __builtin_elementwise_min(
+                       __builtin_bit_cast(u16x2, count.raw.x[k]), u16x2{1, 1})) << k;
     }
-    return x;
-}
-
-// the table's row of sequence b, -1: none such
-__device__ __forceinline__ int slot_of(const LogitsArgs &a, int b) {
-    if (!a.counts) return 0;
-    const int slot = a.slot ? a.slot[b] : b;
-    return slot < 0 || slot >= a.slots ? -1 : slot;
-}
-
-// A wave for every node and 512 tokens, lane l having tokens l, l + 64, ..
-template <typename E, typename O>
-__global__ __launch_bounds__(kThreads) void logits_kernel(LogitsArgs a, int slices) {
-    const int l = threadIdx.x & 63;
-    const int64_t unit = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
-    const int slice = (int)(unit % slices);
-    const int64_t node = unit / slices;
-    if (node >= (int64_t)a.batch * a.n) return;
-    const int b = (int)(node / a.n), i = (int)(node % a.n);
-    const int v0 = slice * kSlice;
-
-    int fault = 0;
-    const int32_t *parent = a.parent + (size_t)b * a.n;
-    if (a.parent) {
-        bool bad = false;
-        for (int j = l; j < a.n; j += 64) bad |= !parent_ok(parent[j], j);
-        if (__any(bad)) fault |= kFaultBadParent;
-    }
-    const int slot = slot_of(a, b);
-    if (slot < 0) fault |= kFaultBadSlot;
-    if (a.status && slice == 0 && i == 0 && l == 0) a.status[b] = fault;
-
-    const typename E::type *z = static_cast<const typename E::type *>(a.logits) + node * a.stride;
-    typename O::type *out =
-        a.out ? static_cast<typename O::type *>(a.out) + node * a.out_stride : nullptr;
-    const float rep = a.repetition ? a.repetition[b] : 1.f;
-    const float pres = a.presence ? a.presence[b] : 0.f;
-    const float freq = a.frequency ? a.frequency[b] : 0.f;
-
-    int c[kLane] = {}, prompt[kLane] = {};
-    float bias[kLane] = {};
-    if (!fault) {
-        // tokens of the slice are (t - v0) = 64 e + l
-        if (a.counts) {
-            const int16_t *row = a.counts + slot * a.counts_stride;
+    if (__any(touched != 0) || (on_path[0] | on_path[1] | biased) || a.bias_len > 64) {
+        uint64_t more = 0;                       // a byte for each of the lane's tokens
+        const bool any_path = (on_path[0] | on_path[1]) != 0;
 #pragma unroll
-            for (int e = 0; e < kLane; ++e) {
-                const int t = v0 + 64 * e + l, x = t < a.vocab ? row[t] : 0;
-                c[e] = x & 32767, prompt[e] = x < 0;
+        for (int k = 0; k < 2; ++k)
+            for (uint64_t hits = on_path[k]; hits; hits &= hits - 1) {
+                const int to = __builtin_amdgcn_readlane(n.token[k], __builtin_ctzll(hits)) - v0;
+                if (to / kLane == l) more += 1ull << 8 * (to % kLane), touched |= touch(to % kLane);
             }
-        }
-        if (a.tokens) {
-            const int32_t *tok = a.tokens + (size_t)b * a.n;
-            for (int j0 = 0; j0 <= i; j0 += 64) {
-                const int t = j0 + l <= i ? tok[j0 + l] : -1;
-                uint64_t hits = __ballot((uint32_t)t - (uint32_t)v0 < (uint32_t)kSlice);
-                while (hits) {
-                    const int j = __builtin_ctzll(hits);
-                    hits &= hits - 1;
-                    int up = i;
-                    while (up > j0 + j) up = parent[up];
-                    const int at = __shfl(t, j) - v0;
-                    if (up == j0 + j && (at & 63) == l)
-#pragma unroll
-                        for (int e = 0; e < kLane; ++e) c[e] += at >> 6 == e;
-                }
-            }
-        }
-        for (int j0 = 0; j0 < a.bias_len; j0 += 64) {
-            const size_t at0 = (size_t)b * a.bias_len + j0 + l;
-            const bool in = j0 + l < a.bias_len;
-            const int t = in ? a.bias_tok[at0] : -1;
-            const float x = in ? a.bias[at0] : 0.f;
-            uint64_t hits = __ballot((uint32_t)t - (uint32_t)v0 < (uint32_t)kSlice);
-            while (hits) {
+        float bias[kLane] = {};
+        bool any_bias = false;
+        auto add = [&](uint64_t hits, int t, float x) {
+            any_bias |= hits != 0;
+            for (; hits; hits &= hits - 1) {
                 const int j = __builtin_ctzll(hits);
-                hits &= hits - 1;
-                const int at = __shfl(t, j) - v0;
-                const float y = __shfl(x, j);
-                if ((at & 63) == l)
+                const int to = __builtin_amdgcn_readlane(t, j) - v0;
+                const float b = __builtin_bit_cast(
+                    float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), j));
+                if (to / kLane == l) {
+                    touched |= touch(to % kLane);
 #pragma unroll
                     for (int e = 0; e < kLane; ++e)
-                        if (at >> 6 == e) bias[e] += y;
+                        if (to % kLane == e) bias[e] += b;
+                }
+            }
+        };
+        add(biased, n.bias_tok, n.bias);
+        for (int j0 = 64; j0 < a.bias_len; j0 += 64) {
+            const bool in = j0 + l < a.bias_len;
+            const int t = in ? a.bias_tok[bias0 + j0 + l] : -1;
+            add(inside(t), t, in ? a.bias[bias0 + j0 + l] : 0.f);
+        }
+        // z' of a token with z, its entry of the table, its count on the path and its bias
+        auto adjusted = [&](float z0, uint32_t x, uint32_t path, float d) {
+            const int c = (int)((x & 32767u) + path);
+            const float less = n.freq * (float)c + n.pres, r = repeated(n, z0);
+            return (x | path ? r : z0) + (c > 0 ? d - less : d);
+        };
+        if (!__any(__popc(touched) > 2)) {
+            // Few tokens of a slice are touched, seldom more than one of a lane:
+            // the lanes take theirs one after the other.
+            while (__any(touched != 0)) {
+                const uint32_t one = touched & -touched;
+                touched ^= one;
+                bool is[kLane];
+                float z0 = 0.f, d = 0.f;
+                uint32_t x = 0, path = 0;
+#pragma unroll
+                for (int e = 0; e < kLane; ++e) is[e] = one == touch(e), z0 = is[e] ? y[e] : z0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) x = is[2 * k] || is[2 * k + 1] ? count.raw.x[k] : x;
+                x = one >> 16 ? x >> 16 : x & 65535u;
+                if (any_bias)
+#pragma unroll
+                    for (int e = 0; e < kLane; ++e) d = is[e] ? bias[e] : d;
+                if (any_path) {
+                    const int at = __builtin_ctz(one | 1u << 31);
+                    path = (uint32_t)(more >> (8 * ((at & 3) * 2 + (at >> 4 & 1)))) & 255u;
+                }
+                z0 = adjusted(z0, x, path, d);
+#pragma unroll
+                for (int e = 0; e < kLane; ++e) y[e] = is[e] ? z0 : y[e];
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < kLane; ++e) {
+                const float z1 = adjusted(y[e], count_at(e), (uint32_t)(more >> 8 * e) & 255u, bias[e]);
+                y[e] = touched & touch(e) ? z1 : y[e];
             }
         }
     }
-    const int words = (a.vocab + 31) / 32;
-    const int32_t *mask =
-        a.mask ? a.mask + ((size_t)b * a.mask_rows + (a.mask_rows > 1 ? i : 0)) * words : nullptr;
-    Best best = {-__builtin_inff(), kNone};
+    const uint32_t none = __float_as_uint(-__builtin_inff());
 #pragma unroll
     for (int e = 0; e < kLane; ++e) {
-        const int t = v0 + 64 * e + l;
-        if (t >= a.vocab) continue;
-        float y = E::widen(z[t]);
-        if (c[e] > 0 || prompt[e]) y = y > 0.f ? y / rep : y * rep;
-        float less = 0.f;
-        if (c[e] > 0) less = freq * (float)c[e] + pres;
-        y = y + (bias[e] - less);
-        if (mask && !(mask[t >> 5] >> (t & 31) & 1)) y = -__builtin_inff();
-        if (fault) y = __builtin_nanf("");
-        if (out) out[t] = O::bits(y);
-        if (y > best.value) best.value = y, best.token = t;
+        const uint32_t keep = (uint32_t)__builtin_amdgcn_sbfe((int)mask, e, 1);
+        y[e] = __uint_as_float((__float_as_uint(y[e]) & keep) | (none & ~keep));
     }
-    if (!a.best) return;
-    best = wave_best(best);
-    if (l == 0) static_cast<Best *>(a.workspace)[unit] = best;
+    if constexpr (!__is_same(O, None)) {
+        typename O::type *o = static_cast<typename O::type *>(out) + v0 + kLane * l;
+        Eight<O> r;
+        r.set(y);
+        if (kTail) r.store(o, left);
+        else r.store(o);
+    }
+    if (kTail)
+#pragma unroll
+        for (int e = 0; e < kLane; ++e) y[e] = e < left ? y[e] : -__builtin_inff();
+    float top = y[0];
+#pragma unroll
+    for (int e = 1; e < kLane; ++e) top = fmaxf(top, y[e]);
+    // slices ascend: an equal one is not better
+    const bool up = top > best.value;
+    best.value = up ? top : best.value;
+    best.slice = up ? slice : best.slice;
+#pragma unroll
+    for (int e = 0; e < kLane; ++e) best.of[e] = up ? y[e] : best.of[e];
 }
 
-// a wave for every node: the best of its slices
-__global__ __launch_bounds__(64) void logits_join_kernel(LogitsArgs a, int slices) {
+// Loads run two slices ahead of the work.  Which of a lane's 8 tokens is the
+// largest is looked up once, at the end.
+template <typename E, typename O>
+__global__ __launch_bounds__(kMostThreads) void logits_kernel(LogitsArgs a, Cut cut) {
+    typedef typename E::type T;
+    __shared__ Best s_best[kMostThreads / 64];
+    const int l = threadIdx.x & 63;
+    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);      // the same in all lanes
+    const int part = (int)blockIdx.x % cut.parts, node = (int)blockIdx.x / cut.parts;
+    const int b = node / a.n, i = node % a.n, waves = cut.threads / 64;
+    const int first = (part * waves + w) * cut.per, end = min(first + cut.per, cut.slices);
+    const int full = min(end, a.vocab / kSlice);                 // the row may end inside a slice
+
+    int slot = 0, fault = 0;
+    if (a.counts) {
+        slot = a.slot ? a.slot[b] : b;
+        if (slot < 0 || slot >= a.slots) fault = kFaultBadSlot, slot = 0;
+    }
+    const T *z = static_cast<const T *>(a.logits) + node * a.stride;
+    const uint16_t *counts = reinterpret_cast<const uint16_t *>(a.counts) +
+                             (a.counts ? slot * a.counts_stride : 0);
+    // a lane's 8 tokens are a byte of the mask; without one any byte, all bits set
+    const uint8_t *mask = static_cast<const uint8_t *>(a.logits);
+    if (a.mask)
+        mask = reinterpret_cast<const uint8_t *>(
+            a.mask + ((int64_t)b * a.mask_rows + (a.mask_rows > 1 ? i : 0)) * ((a.vocab + 31) / 32));
+    const int mask_lane = a.mask ? l : 0, mask_step = a.mask ? kSlice / 8 : 0;
+    const uint32_t all = a.mask ? 0u : 255u;
+    struct Loaded {
+        Eight<E> z;
+        Eight<Bf16> count;
+        uint32_t mask;
+    };
+    auto load = [&](int s, Loaded &x) {
+        x.z.load(z + (int64_t)s * kSlice + kLane * l);
+        if (a.counts) x.count.load(counts + (int64_t)s * kSlice + kLane * l);
+        x.mask = mask[s * mask_step + mask_lane];
+    };
+    Loaded x0 = {}, x1 = {}, x2 = {};
+    if (first < full) {
+        load(first, x0);
+        load(min(first + 1, full - 1), x1);
+    }
+
+    Node n;
+    n.rep = a.repetition ? a.repetition[b] : 1.f;
+    n.inverse = 1.f / n.rep;
+    n.plain = n.rep >= 0x1p-30f && n.rep <= 0x1p30f;
+    n.pres = a.presence ? a.presence[b] : 0.f;
+    n.freq = a.frequency ? a.frequency[b] : 0.f;
+    const int64_t bias0 = (int64_t)b * a.bias_len;
+    n.bias_tok = l < a.bias_len ? a.bias_tok[bias0 + l] : -1;
+    n.bias = l < a.bias_len ? a.bias[bias0 + l] : 0.f;
+    n.token[0] = n.token[1] = -1;
+    if (a.parent) {
+        int parent[2] = {-1, -1}, token[2] = {-1, -1};
+        bool bad = false;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (64 * k + l < a.n) {
+                parent[k] = a.parent[(int64_t)b * a.n + 64 * k + l];
+                token[k] = a.tokens[(int64_t)b * a.n + 64 * k + l];
+                bad |= !parent_ok(parent[k], 64 * k + l);
+            }
+        if (__any(bad)) fault |= kFaultBadParent;
+        else
+            for (int up = i; up >= 0;
+                 up = __builtin_amdgcn_readlane(up < 64 ? parent[0] : parent[1], up & 63)) {
+                if (l == (up & 63) && up < 64) n.token[0] = token[0];
+                if (l == (up & 63) && up >= 64) n.token[1] = token[1];
+            }
+    }
+    if (a.status && part == 0 && i == 0 && threadIdx.x == 0) a.status[b] = fault;
+
+    typename O::type *out = nullptr;
+    if constexpr (!__is_same(O, None))
+        out = static_cast<typename O::type *>(a.out) + node * a.out_stride;
+    Running best;
+    best.value = -__builtin_inff(), best.slice = 0;
+#pragma unroll
+    for (int e = 0; e < kLane; ++e) best.of[e] = -__builtin_inff();
+    if (fault) {
+        if constexpr (!__is_same(O, None))
+            for (int64_t t = (int64_t)first * kSlice + l; t < min((int64_t)end * kSlice, (int64_t)a.vocab);
+                 t += 64)
+                out[t] = O::bits(__builtin_nanf(""));
+    } else {
+        auto work = [&](const Loaded &x, int s) {
+            slice_of<E, O, false>(a, n, bias0, x.z, x.count, x.mask | all, s, 0, out, best);
+        };
+        for (int s = first; s < full; s += 3) {
+            load(min(s + 2, full - 1), x2);
+            work(x0, s);
+            if (s + 1 >= full) break;
+            load(min(s + 3, full - 1), x0);
+            work(x1, s + 1);
+            if (s + 2 >= full) break;
+            load(min(s + 4, full - 1), x1);
+            work(x2, s + 2);
+        }
+        if (full < end && first < end) {         // the last slice of the row, in part
+            const int left = min(max(a.vocab - full * kSlice - kLane * l, 0), kLane);
+            const int64_t at = (int64_t)full * kSlice + kLane * l;
+            x0.z.load(z + at, left);
+            if (a.counts) x0.count.load(counts + at, left);
+            x0.mask = left > 0 ? mask[full * mask_step + mask_lane] : 0u;
+            slice_of<E, O, true>(a, n, bias0, x0.z, x0.count, x0.mask | all, full, left, out,
+                                 best);
+        }
+    }
+    if (!a.best) return;
+    // the lane's first token with its largest value, then the wave's, then the workgroup's
+    int at = 0;
+#pragma unroll
+    for (int e = kLane - 1; e >= 0; --e) at = best.of[e] == best.value ? e : at;
+    Best mine = kNothing;
+    if (best.value > -__builtin_inff())
+        mine.value = best.value, mine.token = best.slice * kSlice + kLane * l + at;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1)
+        better(mine, {__shfl_xor(mine.value, o), __shfl_xor(mine.token, o)});
+    if (l == 0) s_best[w] = mine;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int k = 1; k < waves; ++k) better(mine, s_best[k]);
+        if (cut.parts == 1) a.best[node] = mine.token == kNone ? -1 : mine.token;
+        else static_cast<Best *>(a.workspace)[(int64_t)node * cut.parts + part] = mine;
+    }
+}
+
+// a wave for every node: the best of its parts
+__global__ __launch_bounds__(64) void logits_join_kernel(LogitsArgs a, int parts) {
     const int l = threadIdx.x;
     const int64_t node = blockIdx.x;
-    const Best *part = static_cast<const Best *>(a.workspace) + node * slices;
-    Best best = {-__builtin_inff(), kNone};
-    for (int i = l; i < slices; i += 64) better(best, part[i].value, part[i].token);
-    best = wave_best(best);
+    const Best *from = static_cast<const Best *>(a.workspace) + node * parts;
+    Best best = kNothing;
+    for (int i = l; i < parts; i += 64) better(best, from[i]);
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1)
+        better(best, {__shfl_xor(best.value, o), __shfl_xor(best.token, o)});
     if (l == 0) a.best[node] = best.token == kNone ? -1 : best.token;
 }
 
-int logits_slices(const LogitsArgs &a) { return (a.vocab + kSlice - 1) / kSlice; }
+// About 4096 waves, 16 a compute unit: enough loads in flight, and no more of
+// what each of them does once.  Up to 8 waves of a node are one workgroup and
+// need no joining; more of them are groups of four.
+Cut cut_of(const LogitsArgs &a) {
+    Cut c;
+    const int64_t nodes = (int64_t)a.batch * a.n;
+    c.slices = (a.vocab + kSlice - 1) / kSlice;
+    int64_t waves = nodes < 4096 ? 4096 / nodes : 1;
+    if (waves > c.slices) waves = c.slices;
+    c.per = (int)((c.slices + waves - 1) / waves);
+    waves = (c.slices + c.per - 1) / c.per;
+    c.parts = waves <= 8 ? 1 : (int)((waves + 3) / 4);
+    c.threads = 64 * (waves <= 8 ? (int)waves : 4);
+    return c;
+}
 
 template <typename E, typename O>
 hipError_t launch(const LogitsArgs &a, hipStream_t s) {
-    const int slices = logits_slices(a);
-    const int64_t units = (int64_t)a.batch * a.n * slices;
-    hipLaunchKernelGGL((logits_kernel<E, O>), dim3((unsigned)((units + kWaves - 1) / kWaves)),
-                       dim3(kThreads), 0, s, a, slices);
+    const Cut c = cut_of(a);
+    hipLaunchKernelGGL((logits_kernel<E, O>), dim3((unsigned)(a.batch * a.n * c.parts)),
+                       dim3((unsigned)c.threads), 0, s, a, c);
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !a.best) return e;
+    if (e != hipSuccess || !a.best || c.parts == 1) return e;
     hipLaunchKernelGGL(logits_join_kernel, dim3((unsigned)(a.batch * a.n)), dim3(64), 0, s, a,
-                       slices);
+                       c.parts);
     return hipGetLastError();
 }
 
@@ -268,15 +527,25 @@ hipError_t launch_count_commit(const CountArgs &a, const int32_t *tokens, const 
     return hipGetLastError();
 }
 
-int64_t logits_units(const LogitsArgs &a) { return (int64_t)a.batch * a.n * logits_slices(a); }
+int64_t logits_threads(const LogitsArgs &a) {
+    const Cut c = cut_of(a);
+    return (int64_t)a.batch * a.n * c.parts * c.threads;
+}
 
-int64_t logits_workspace(const LogitsArgs &a) { return logits_units(a) * (int64_t)sizeof(Best); }
+int64_t logits_workspace(const LogitsArgs &a) {
+    const Cut c = cut_of(a);
+    return c.parts == 1 ? 0 : (int64_t)a.batch * a.n * c.parts * (int64_t)sizeof(Best);
+}
 
 hipError_t launch_adjust_logits(const LogitsArgs &a, hipStream_t s) {
     const bool same = a.out_dtype == a.dtype;
-    if (a.dtype == GDN_DTYPE_BF16) return same ? launch<Bf16, Bf16>(a, s) : launch<Bf16, F32>(a, s);
-    if (a.dtype == GDN_DTYPE_F16) return same ? launch<F16, F16>(a, s) : launch<F16, F32>(a, s);
-    return launch<F32, F32>(a, s);
+    if (a.dtype == GDN_DTYPE_BF16)
+        return !a.out ? launch<Bf16, None>(a, s)
+                      : same ? launch<Bf16, Bf16>(a, s) : launch<Bf16, F32>(a, s);
+    if (a.dtype == GDN_DTYPE_F16)
+        return !a.out ? launch<F16, None>(a, s)
+                      : same ? launch<F16, F16>(a, s) : launch<F16, F32>(a, s);
+    return !a.out ? launch<F32, None>(a, s) : launch<F32, F32>(a, s);
 }
 
 }  // namespace gdn

@@ -177,7 +177,7 @@ hipError_t launch_count_prompt(const CountArgs &a, const int32_t *cu, const int3
                                int rows, hipStream_t s);
 hipError_t launch_count_commit(const CountArgs &a, const int32_t *tokens, const int32_t *path,
                                const int32_t *add, int n, int max_path, hipStream_t s);
-int64_t logits_units(const LogitsArgs &a);       // waves of the launch
+int64_t logits_threads(const LogitsArgs &a);     // of the launch
 int64_t logits_workspace(const LogitsArgs &a);
 hipError_t launch_adjust_logits(const LogitsArgs &a, hipStream_t s);
 

@@ -227,6 +227,21 @@ def test_values_not_finite(gpu_lib):
     same(o, ref, torch.float32)
 
 
+@pytest.mark.parametrize("dtype,bits", [("bf16", 0x7f81), ("bf16", -0x7f), ("fp16", 0x7c01),
+                                        ("fp32", 0x7f800001), ("fp32", -0x7fffff)])
+def test_nan_of_every_kind_is_never_the_largest(gpu_lib, dtype, bits):
+    """signalling ones too, at every place of a lane's eight tokens"""
+    V = 1024
+    z = torch.zeros(1, 8, V, dtype=DT[dtype], device="cuda")
+    raw = z.view(torch.int32 if dtype == "fp32" else torch.int16)
+    for i in range(8):
+        z[0, i, 8 * i + (i + 3) % 8] = 3.0
+        raw[0, i, 8 * i + i] = bits
+        raw[0, i, 512:] = bits
+    assert torch.isnan(z[0, 0, 0])
+    assert gpu_lib.adjust_logits(z)[0].tolist() == [8 * i + (i + 3) % 8 for i in range(8)]
+
+
 def test_masks_that_leave_nothing_or_one(gpu_lib):
     x = make(2, 4, 70, "fp32", 13, mask="node")
     x["mask"][0, 0] = 0
@@ -407,7 +422,7 @@ def test_in_a_graph_and_on_another_stream(gpu_lib):
 
 
 def test_given_workspace_and_prepared(gpu_lib):
-    x = make(2, 3, 3000, "fp16", 23)
+    x = make(2, 3, 150000, "fp16", 23)
     z, kw = upload(x)
     want = gpu_lib.adjust_logits(z, **kw)
     room = torch.full((1 << 16,), 255, dtype=torch.uint8, device="cuda")
@@ -415,5 +430,7 @@ def test_given_workspace_and_prepared(gpu_lib):
     for _ in range(3):
         room.fill_(255)
         assert torch.equal(launch(), want)
+    need = gpu_lib.load().gdn_adjust_logits_workspace(2, 3, 150000)
+    assert 0 < need <= room.numel()
     with pytest.raises(gpu_lib.GdnError):
-        gpu_lib.adjust_logits(z, workspace=room[:16], **kw)
+        gpu_lib.adjust_logits(z, workspace=room[:need - 1], **kw)

@@ -131,8 +131,8 @@ def logits(lib, z=FAKE, dtype=1, stride=100, counts=FAKE, c_stride=100, slot=FAK
     (dict(tokens=None), -1), (dict(parent=None), -1), (dict(bias=None), -1), (dict(bias_tok=None), -1),
     (dict(slots=0), -1), (dict(c_stride=99), -1), (dict(counts=ODD), -1), (dict(slot=ODD), -1),
     (dict(mask_rows=2), -1), (dict(mask_rows=0), -1), (dict(mask=ODD), -1), (dict(out_stride=99), -1),
-    (dict(best=ODD), -1), (dict(status=ODD), -1), (dict(rep=ODD), -1), (dict(ws=None), -1),
-    (dict(ws=0x10004), -1), (dict(size=0), -1), (dict(n=129, mask_rows=1), -2),
+    (dict(best=ODD), -1), (dict(status=ODD), -1), (dict(rep=ODD), -1), (dict(ws=0x10004), -1),
+    (dict(n=129, mask_rows=1), -2),
     (dict(V=(1 << 24) + 1, stride=1 << 25, c_stride=1 << 25, out_stride=1 << 25), -2),
     (dict(biases=4097), -2), (dict(batch=1 << 26), -2), (dict(stride=(1 << 40) + 1), -2),
     (dict(batch=1 << 20, n=64, V=1 << 20, stride=1 << 20, c_stride=1 << 20, out_stride=1 << 20,
@@ -144,9 +144,9 @@ def test_logits_refuse(lib, kw, code):
 
 def test_logits_workspace(lib):
     size = lib.gdn_adjust_logits_workspace
-    need = size(2, 3, 10000)
-    assert need > 0
-    assert logits(lib, V=10000, stride=10000, c_stride=10000, out_stride=10000, size=need - 1) == -1
+    big = dict(V=100000, stride=100000, c_stride=100000, out_stride=100000)
+    need = size(2, 3, 100000)
+    assert need > 0 and logits(lib, size=need - 1, **big) == -1 and logits(lib, ws=None, **big) == -1
     assert size(0, 3, 100) == 0 and size(1, 129, 100) == 0 and size(1, 1, 0) == 0
 
 
