@@ -217,6 +217,7 @@ def _native():
                                f"expects {ABI_VERSION}; rebuild with "
                                "gated_deltanet_tree_verify_amd.build()")
         _binding.explain(_explain)
+        _binding.streams(_torch()._C._cuda_getDevice, _torch()._C._cuda_getCurrentRawStream)
         _native_module = _binding
     return _native_module
 
@@ -1014,6 +1015,13 @@ def rope(q, k, pos, inv_freq, layout="half", scale=1.0, base=None, q_out=None, k
     "interleaved"; scale: the magnitude.  Negative positions turn back.
     Returns (q_out, k_out); q_out may be q, k_out may be k.
     """
+    if q_out is not None and not prepare:
+        code = _native().heads_call(0, q, k, None, None, pos, base, inv_freq, 0.0, 0.0,
+                                    _LAYOUTS.get(layout), scale, q_out, k_out, stream)
+        if code is not None:
+            if code:
+                _check("gdn_rope", code)
+            return q_out, k_out
     return _heads_call("gdn_rope", q, k, 0, 0.0, 0.0, None, None, pos, base, inv_freq, layout,
                        scale, q_out, k_out, stream, prepare)
 
@@ -1028,6 +1036,14 @@ def qk_norm_rope(q, k, q_weight, k_weight, pos=None, inv_freq=None, norm="rms", 
     multiplied as offset + weight, or None; without inv_freq the norm alone.
     Everything else as for rope.  Returns (q_out, k_out).
     """
+    if q_out is not None and not prepare:
+        code = _native().heads_call(_NORMS.get(norm), q, k, q_weight, k_weight, pos, base,
+                                    inv_freq, eps, offset, _LAYOUTS.get(layout), scale, q_out,
+                                    k_out, stream)
+        if code is not None:
+            if code:
+                _check("gdn_qk_norm_rope", code)
+            return q_out, k_out
     return _heads_call("gdn_qk_norm_rope", q, k, _choice(norm, "norm", _NORMS), eps, offset,
                        q_weight, k_weight, pos, base, inv_freq, layout, scale, q_out, k_out, stream,
                        prepare)
@@ -1048,6 +1064,14 @@ def kv_append(k_cache, v_cache, table, dst, begin, k, v, cu=None, inv_freq=None,
     """
     torch = _torch()
     native = _native()
+    if not prepare:
+        code = native.append_call(k_cache, v_cache, table, dst, begin, k, v, cu, inv_freq,
+                                  _LAYOUTS.get(layout), scale, pos, _NORMS.get(norm), eps, offset,
+                                  k_weight, q, q_weight, q_out, k_out, status, stream)
+        if code is not None:
+            if code:
+                _check("gdn_kv_append", code)
+            return q_out, k_out
     kinds = (torch.bfloat16, torch.float16, torch.float32)
     rows, k_row, Hkv, k_head, d = _rows(k, "k", kinds, 2)
     lead = k.shape[:-2]
@@ -1115,6 +1139,12 @@ def count_prompt(counts, slot, cu, tokens, status=None, stream=None, prepare=Fal
     prompt clears its row.  Returns counts."""
     torch = _torch()
     native = _native()
+    if not prepare:
+        code = native.count_prompt_call(counts, slot, cu, tokens, status, stream)
+        if code is not None:
+            if code:
+                _check("gdn_count_prompt", code)
+            return counts
     slots, stride, vocab, m = _need_counts(counts, slot)
     _need(cu, "cu", (torch.int32,), (m + 1,))
     _need(tokens, "tokens", (torch.int32,))
@@ -1133,6 +1163,12 @@ def count_commit(counts, slot, tokens, path, add, status=None, stream=None, prep
     the table counts int16 [slots][vocab].  Returns counts."""
     torch = _torch()
     native = _native()
+    if not prepare:
+        code = native.count_commit_call(counts, slot, tokens, path, add, status, stream)
+        if code is not None:
+            if code:
+                _check("gdn_count_commit", code)
+            return counts
     slots, stride, vocab, m = _need_counts(counts, slot)
     _need(tokens, "tokens", (torch.int32,))
     if tokens.dim() != 2 or tokens.shape[0] != m:
@@ -1148,6 +1184,12 @@ def count_commit(counts, slot, tokens, path, add, status=None, stream=None, prep
             vocab, status, _stream(stream))
     return _issue("gdn_count_commit", native.gdn_count_commit, args,
                   (counts, slot, tokens, path, add, status), counts, prepare)
+
+
+def _logits_room(logits, stream):
+    batch, n, vocab = logits.shape
+    return _empty(_workspace_bytes("gdn_adjust_logits_workspace", batch, n, vocab),
+                  _torch().uint8, logits.device, stream)
 
 
 def adjust_logits(logits, counts=None, slot=None, tokens=None, parent=None, repetition=None,
@@ -1167,6 +1209,18 @@ def adjust_logits(logits, counts=None, slot=None, tokens=None, parent=None, repe
     """
     torch = _torch()
     native = _native()
+    if not prepare and isinstance(best, torch.Tensor) and isinstance(logits, torch.Tensor):
+        room = workspace
+        if room is None and logits.dim() == 3 and logits.is_cuda:
+            room = _logits_room(logits, stream)
+        bias_tok, bias_val = (None, None) if bias is None else bias
+        code = native.logits_call(logits, counts, slot, tokens, parent, repetition, presence,
+                                  frequency, bias_tok, bias_val, mask, out, best, status, stream,
+                                  room)
+        if code is not None:
+            if code:
+                _check("gdn_adjust_logits", code)
+            return best
     kinds = (torch.bfloat16, torch.float16, torch.float32)
     _, row, vocab = _rows(logits, "logits", kinds, 1)
     if logits.dim() != 3:

@@ -539,3 +539,75 @@ def test_in_a_graph(gpu_lib):
         assert st.tolist()[1] == (gpu_lib.FAULT_BAD_PAGE if i == 2 else 0)
         for a, b in zip(outs, eager_o):
             assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+
+
+# ---------------------------------------------------------------------------
+# the two ways to the entry points: with outputs given the native part checks
+# and calls, without, or where it finds something unusual, Python does
+# ---------------------------------------------------------------------------
+def test_both_ways_give_the_same(gpu_lib):
+    (q, k, v), (dq, dk, dv) = projection((2, 7), 6, 2, 64, "bf16", 31, True)
+    f, w = frequencies(32).cuda(), torch.rand(64, device="cuda")
+    pos, base = ints([list(range(7))] * 2), ints([5, 900])
+    out = lambda: (torch.full(dq.shape, NAN, dtype=dq.dtype, device="cuda"),
+                   torch.full(dk.shape, NAN, dtype=dk.dtype, device="cuda"))
+    wq = torch.rand(6, 64, device="cuda")
+    for fn, args, kw in (
+            (gpu_lib.rope, (dq, dk, pos, f), dict(base=base, scale=1.5, layout="interleaved")),
+            (gpu_lib.rope, (dq, dk, pos, f), {}),
+            (gpu_lib.qk_norm_rope, (dq, dk, wq, w, pos, f), dict(base=base, norm="l2", offset=0.5)),
+            (gpu_lib.qk_norm_rope, (dq, dk, w.bfloat16(), None, pos, f), dict(eps=0.1)),
+            (gpu_lib.qk_norm_rope, (dq, dk, None, None), dict(norm="l2"))):
+        a, b = out()
+        got = fn(*args, q_out=a, k_out=b, **kw)
+        assert got[0] is a and got[1] is b
+        want = fn(*args, **kw)
+        assert torch.equal(a, want[0]) and torch.equal(b, want[1])
+        assert torch.equal(fn(args[0], None, *([args[2], None] if fn is gpu_lib.qk_norm_rope else []),
+                              *args[4 if fn is gpu_lib.qk_norm_rope else 2:], q_out=out()[0],
+                              **kw)[0], want[0])
+
+
+def test_native_calls_leave_the_unusual_to_python(gpu_lib):
+    """None, and nothing written, for every argument out of order"""
+    native = gpu_lib._native()
+    q, k = (torch.randn(3, H, 64, device="cuda").bfloat16() for H in (4, 2))
+    qo, ko = torch.zeros_like(q), torch.zeros_like(k)
+    w, pos, f = torch.ones(64, device="cuda").bfloat16(), ints([1, 2, 3]), torch.ones(32, device="cuda")
+    good = [1, q, k, w, w, pos, None, f, 1e-6, 0.0, 0, 1.0, qo, ko, None]
+
+    def refused(call, args, at, value):
+        x = list(args)
+        x[at] = value
+        assert call(*x) is None, (at, value if not torch.is_tensor(value) else value.shape)
+
+    host = torch.zeros(3, dtype=torch.int32)
+    for at, value in (
+            (0, None), (0, 3), (0, -1), (1, None), (1, q.cpu()), (1, q.double()), (1, q[:2]),
+            (1, q[..., ::2]), (2, k.float()), (2, k[:2]), (2, k[..., :32]), (2, None), (3, w.half()),
+            (3, w[:32]), (3, w.float()), (4, torch.ones(4, 64, device="cuda").bfloat16()), (5, None),
+            (5, pos.long()), (5, pos[:2]), (5, host), (5, pos[None]), (6, ints([1])), (7, f.double()),
+            (7, torch.ones(33, device="cuda")), (7, f[None]), (8, "x"), (9, None), (10, None), (10, 2),
+            (11, None), (12, None), (12, ko), (12, qo.float()), (13, None), (13, qo), (14, "s")):
+        refused(native.heads_call, good, at, value)
+    assert not qo.any() and not ko.any()
+    rope = [0, q, k, None, None, pos, None, f, 0.0, 0.0, 0, 1.0, qo, ko, None]
+    refused(native.heads_call, rope, 3, w)
+    refused(native.heads_call, rope, 7, None)
+    assert not qo.any()
+    cache = torch.zeros(2, 4, 2, 16, 64, dtype=torch.bfloat16, device="cuda")
+    table, dst, begin = ints([[0, 1]] * 3), ints([0, 1, 2]), ints([0, 16, 3])
+    good = [cache[0], cache[1], table, dst, begin, k, k, None, f, 0, 1.0, None, 1, 1e-6, 0.0, w, q, w,
+            qo, ko, None, None]
+    for at, value in (
+            (0, cache[0].float()), (0, cache[0][:, :1]), (0, cache[0][:2]), (1, cache[1, :, :, :8]),
+            (0, cache[0].transpose(0, 1)), (2, table[0]), (2, table.long()), (3, dst[:2]),
+            (4, begin.cpu()), (5, k[:2]), (6, k[:2]), (6, k.float()), (7, ints([0, 1])), (7, host),
+            (8, torch.ones(33, device="cuda")), (9, 5), (10, None), (11, ints([1, 2])), (12, 7),
+            (15, w[:9]), (16, None), (16, q[:2]), (17, w.float()), (18, None), (18, ko), (19, qo),
+            (20, ints([0])), (21, "s")):
+        refused(native.append_call, good, at, value)
+    assert not cache.any() and not qo.any() and not ko.any()
+    assert native.append_call(*good) == 0
+    torch.cuda.synchronize()
+    assert cache.any() and qo.any() and ko.any()

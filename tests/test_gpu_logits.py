@@ -158,8 +158,13 @@ def test_adjust_logits(gpu_lib, batch, n, V, dtype, out, mask, bias, pad):
     same(o, ref, DT[out])
     if pad:
         assert (o._base[..., V:] == 3).all() and (z._base[..., V:] == 3).all()
-    # the greedy tokens alone, and in place
+    # the greedy tokens alone, given (checked and called natively) or not, and in place
     assert torch.equal(gpu_lib.adjust_logits(z, **kw), got)
+    mine = torch.full_like(got, -7)
+    assert gpu_lib.adjust_logits(z, best=mine, status=st, **kw) is mine and torch.equal(mine, got)
+    again = torch.full_like(o, NAN)
+    gpu_lib.adjust_logits(z, best=mine, out=again, **kw)
+    same(again, ref, DT[out])
     assert gpu_lib.adjust_logits(z, out=z, best=False, **kw) is None
     same(z, ref, z.dtype)
 
@@ -434,3 +439,50 @@ def test_given_workspace_and_prepared(gpu_lib):
     assert 0 < need <= room.numel()
     with pytest.raises(gpu_lib.GdnError):
         gpu_lib.adjust_logits(z, workspace=room[:need - 1], **kw)
+
+
+def test_native_calls_leave_the_unusual_to_python(gpu_lib):
+    """None, and nothing written, for every argument out of order"""
+    native = gpu_lib._native()
+    z = torch.randn(2, 3, 100, device="cuda").bfloat16()
+    c = torch.zeros(4, 100, dtype=torch.int16, device="cuda")
+    slot, six, one = ints([0, 1]), ints([[1, 2, 3]] * 2), torch.ones(2, device="cuda")
+    parent, mask = ints([[-1, 0, 1]] * 2), ints(np.zeros((2, 1, 4)))
+    best, room = ints([[7] * 3] * 2), torch.empty(64, dtype=torch.uint8, device="cuda")
+    good = [z, c, slot, six, parent, one, one, one, six, torch.ones(2, 3, device="cuda"), mask, None,
+            best, None, None, room]
+
+    def refused(call, args, at, value):
+        x = list(args)
+        x[at] = value
+        assert call(*x) is None, (at, value if not torch.is_tensor(value) else value.shape)
+
+    for at, value in (
+            (0, None), (0, z.cpu()), (0, z[0]), (0, z.double()), (0, z[..., ::2]), (0, z[:1]),
+            (0, z[..., :99]), (1, None), (1, c[:, :99]), (1, c.int()), (1, c[0]), (2, slot[:1]),
+            (2, slot.long()), (3, None), (3, six[:1]), (4, None), (4, parent.cpu()), (5, one[:1]),
+            (6, one.double()), (7, one.cpu()), (8, None), (8, six[0]), (9, six.float()[:1]), (9, six),
+            (10, mask[:, 0]), (10, mask[..., :3]), (10, ints(np.zeros((2, 2, 4)))), (11, z[:1]),
+            (11, z.half()), (11, z.double()), (12, None), (12, best[:1]), (12, best.long()),
+            (13, slot[:1]), (14, "s"), (15, None), (15, room.int())):
+        refused(native.logits_call, good, at, value)
+    torch.cuda.synchronize()
+    assert (best == 7).all()
+    assert native.logits_call(*good) == 0
+    torch.cuda.synchronize()
+    assert (best == -1).all()
+    cu, tok = ints([0, 2, 3]), ints([1, 2, 3])
+    good = [c, slot, cu, tok, None, None]
+    for at, value in ((0, None), (0, c.int()), (0, c[0]), (1, slot[None]), (1, slot.cpu()), (2, cu[:2]),
+                      (3, tok.long()), (3, None), (4, slot[:1]), (5, "s")):
+        refused(native.count_prompt_call, good, at, value)
+    path = ints([[0, 1]] * 2)
+    commit = [c, slot, six, path, slot, None, None]
+    for at, value in ((0, c.int()), (1, slot[None]), (2, six[0]), (2, six[:1]), (3, path[:1]),
+                      (3, path.cpu()), (4, slot[:1]), (5, slot[:1]), (6, "s")):
+        refused(native.count_commit_call, commit, at, value)
+    torch.cuda.synchronize()
+    assert not c.any()
+    assert native.count_prompt_call(*good) == 0 and native.count_commit_call(*commit) == 0
+    torch.cuda.synchronize()
+    assert c.any()
