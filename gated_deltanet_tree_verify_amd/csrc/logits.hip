@@ -192,6 +192,7 @@ struct Node {
     int token[2];            // of the nodes l and 64 + l, if they are on the node's path, or -1
     int bias_tok;            // the first 64 biases stay in the lanes
     float bias;
+    bool any;                // any of these lies in the wave's slices
 };
 
 // z / rep for z above 0, z rep otherwise, correctly rounded.  With r the
@@ -213,11 +214,6 @@ struct Running {
     float of[kLane];
 };
 
-// the bit of a lane's token e: those of a word's halves are 16 apart
-__device__ __forceinline__ constexpr uint32_t touch(int e) {
-    return 1u << ((e >> 1) + 16 * (e & 1));
-}
-
 // The lane's 8 tokens v0 + 8 l .. of a slice; kTail: of which only the first
 // `left` are in the row.
 template <typename E, typename O, bool kTail>
@@ -231,16 +227,21 @@ __device__ __forceinline__ void slice_of(const LogitsArgs &a, const Node &n, int
     for (int e = 0; e < kLane; ++e) y[e] = __builtin_canonicalizef(z.at(e));   // NaNs are quiet
     auto count_at = [&](int e) { return count.raw.x[e >> 1] >> (e & 1 ? 16 : 0) & 65535u; };
     auto inside = [&](int t) { return __ballot((uint32_t)t - (uint32_t)v0 < (uint32_t)kSlice); };
-    const uint64_t on_path[2] = {inside(n.token[0]), inside(n.token[1])};
-    const uint64_t biased = inside(n.bias_tok);
-    // tokens that anything is known of, a bit each (touch): those with a count first
+    uint64_t on_path[2] = {0, 0}, biased = 0;
+    if (n.any) {
+        on_path[0] = inside(n.token[0]), on_path[1] = inside(n.token[1]);
+        biased = inside(n.bias_tok);
+    }
+    // tokens that anything is known of, a bit each: those with a count first, as
+    // far as the mask has them (what it has not is -inf, whatever its count)
     uint32_t touched = 0;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
         touched |= __builtin_bit_cast(uint32_t, __builtin_elementwise_min(
-                       __builtin_bit_cast(u16x2, count.raw.x[k]), u16x2{1, 1})) << k;
+                       __builtin_bit_cast(u16x2, count.raw.x[k]), u16x2{1, 1})) << 2 * k;
     }
+    touched = (touched | touched >> 15) & mask;
     if (__any(touched != 0) || (on_path[0] | on_path[1] | biased) || a.bias_len > 64) {
         uint64_t more = 0;                       // a byte for each of the lane's tokens
         const bool any_path = (on_path[0] | on_path[1]) != 0;
@@ -248,7 +249,7 @@ __device__ __forceinline__ void slice_of(const LogitsArgs &a, const Node &n, int
         for (int k = 0; k < 2; ++k)
             for (uint64_t hits = on_path[k]; hits; hits &= hits - 1) {
                 const int to = __builtin_amdgcn_readlane(n.token[k], __builtin_ctzll(hits)) - v0;
-                if (to / kLane == l) more += 1ull << 8 * (to % kLane), touched |= touch(to % kLane);
+                if (to / kLane == l) more += 1ull << 8 * (to % kLane), touched |= 1u << to % kLane;
             }
         float bias[kLane] = {};
         bool any_bias = false;
@@ -260,7 +261,7 @@ __device__ __forceinline__ void slice_of(const LogitsArgs &a, const Node &n, int
                 const float b = __builtin_bit_cast(
                     float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), j));
                 if (to / kLane == l) {
-                    touched |= touch(to % kLane);
+                    touched |= 1u << to % kLane;
 #pragma unroll
                     for (int e = 0; e < kLane; ++e)
                         if (to % kLane == e) bias[e] += b;
@@ -289,17 +290,14 @@ __device__ __forceinline__ void slice_of(const LogitsArgs &a, const Node &n, int
                 float z0 = 0.f, d = 0.f;
                 uint32_t x = 0, path = 0;
 #pragma unroll
-                for (int e = 0; e < kLane; ++e) is[e] = one == touch(e), z0 = is[e] ? y[e] : z0;
+                for (int e = 0; e < kLane; ++e) is[e] = one == 1u << e, z0 = is[e] ? y[e] : z0;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) x = is[2 * k] || is[2 * k + 1] ? count.raw.x[k] : x;
-                x = one >> 16 ? x >> 16 : x & 65535u;
+                x = one & 0xaau ? x >> 16 : x & 65535u;
                 if (any_bias)
 #pragma unroll
                     for (int e = 0; e < kLane; ++e) d = is[e] ? bias[e] : d;
-                if (any_path) {
-                    const int at = __builtin_ctz(one | 1u << 31);
-                    path = (uint32_t)(more >> (8 * ((at & 3) * 2 + (at >> 4 & 1)))) & 255u;
-                }
+                if (any_path) path = (uint32_t)(more >> 8 * __builtin_ctz(one | 128u)) & 255u;
                 z0 = adjusted(z0, x, path, d);
 #pragma unroll
                 for (int e = 0; e < kLane; ++e) y[e] = is[e] ? z0 : y[e];
@@ -308,7 +306,7 @@ __device__ __forceinline__ void slice_of(const LogitsArgs &a, const Node &n, int
 #pragma unroll
             for (int e = 0; e < kLane; ++e) {
                 const float z1 = adjusted(y[e], count_at(e), (uint32_t)(more >> 8 * e) & 255u, bias[e]);
-                y[e] = touched & touch(e) ? z1 : y[e];
+                y[e] = touched >> e & 1 ? z1 : y[e];
             }
         }
     }
@@ -383,27 +381,33 @@ __global__ __launch_bounds__(kMostThreads) void logits_kernel(LogitsArgs a, Cut 
         load(min(first + 1, full - 1), x1);
     }
 
+    // lanes 0, 1 and 2 fetch the penalties; nothing is used before all loads are out
+    float penalty = l == 0 ? 1.f : 0.f;
+    const float *const from = l == 0 ? a.repetition : l == 1 ? a.presence : a.frequency;
+    if (l < 3 && from) penalty = from[b];
     Node n;
-    n.rep = a.repetition ? a.repetition[b] : 1.f;
-    n.inverse = 1.f / n.rep;
-    n.plain = n.rep >= 0x1p-30f && n.rep <= 0x1p30f;
-    n.pres = a.presence ? a.presence[b] : 0.f;
-    n.freq = a.frequency ? a.frequency[b] : 0.f;
     const int64_t bias0 = (int64_t)b * a.bias_len;
-    n.bias_tok = l < a.bias_len ? a.bias_tok[bias0 + l] : -1;
-    n.bias = l < a.bias_len ? a.bias[bias0 + l] : 0.f;
-    n.token[0] = n.token[1] = -1;
-    if (a.parent) {
-        int parent[2] = {-1, -1}, token[2] = {-1, -1};
-        bool bad = false;
+    n.bias_tok = -1, n.bias = 0.f;
+    if (l < a.bias_len) n.bias_tok = a.bias_tok[bias0 + l], n.bias = a.bias[bias0 + l];
+    int parent[2] = {-1, -1}, token[2] = {-1, -1};
+    if (a.parent)
 #pragma unroll
         for (int k = 0; k < 2; ++k)
             if (64 * k + l < a.n) {
                 parent[k] = a.parent[(int64_t)b * a.n + 64 * k + l];
                 token[k] = a.tokens[(int64_t)b * a.n + 64 * k + l];
-                bad |= !parent_ok(parent[k], 64 * k + l);
             }
-        if (__any(bad)) fault |= kFaultBadParent;
+    auto fetched = [&](int lane) {
+        return __builtin_bit_cast(
+            float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, penalty), lane));
+    };
+    n.rep = fetched(0), n.pres = fetched(1), n.freq = fetched(2);
+    n.inverse = 1.f / n.rep;
+    n.plain = n.rep >= 0x1p-30f && n.rep <= 0x1p30f;
+    n.token[0] = n.token[1] = -1;
+    if (a.parent) {
+        if (__any(!parent_ok(parent[0], l) || !parent_ok(parent[1], 64 + l)))
+            fault |= kFaultBadParent;
         else
             for (int up = i; up >= 0;
                  up = __builtin_amdgcn_readlane(up < 64 ? parent[0] : parent[1], up & 63)) {
@@ -411,6 +415,8 @@ __global__ __launch_bounds__(kMostThreads) void logits_kernel(LogitsArgs a, Cut 
                 if (l == (up & 63) && up >= 64) n.token[1] = token[1];
             }
     }
+    auto ours = [&](int t) { return t >= first * kSlice && t < end * kSlice; };
+    n.any = __any(ours(n.token[0]) || ours(n.token[1]) || ours(n.bias_tok));
     if (a.status && part == 0 && i == 0 && threadIdx.x == 0) a.status[b] = fault;
 
     typename O::type *out = nullptr;
