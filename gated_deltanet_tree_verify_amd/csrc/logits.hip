@@ -24,11 +24,12 @@ using heads::F16;
 using heads::F32;
 
 constexpr int kThreads = 256;
-constexpr int kMostThreads = 512;              // of a workgroup of the logits
+constexpr int kMostThreads = 1024;              // of a workgroup of the logits
 constexpr int kLane = 8;                       // tokens of a lane
 constexpr int kSlice = 64 * kLane;             // and of a wave
 constexpr int kMarkTokens = 1 << 13;           // of a workgroup of count_prompt
 constexpr int kNone = 0x7fffffff;
+constexpr int kAhead = 2;                      // slices on their way, the one in work among them
 
 // 8 adjacent values as they lie in memory, at any address of their type
 struct __attribute__((packed, aligned(2))) Half8 {
@@ -177,6 +178,38 @@ __device__ __forceinline__ void better(Best &x, const Best &y) {
 
 constexpr Best kNothing = {-__builtin_inff(), kNone};
 
+// y of another lane, x where that lane is none
+template <int kControl>
+__device__ __forceinline__ int other_lane(int x) {
+    return __builtin_amdgcn_update_dpp(x, x, kControl, 0xf, 0xf, false);
+}
+
+// f over the values of all lanes: neighbours, the other two of four, the other
+// four of eight, the other eight of sixteen, then from one sixteen to the next
+template <typename F>
+__device__ __forceinline__ int wave_over(int x, F f) {
+    x = f(x, other_lane<0xb1>(x));
+    x = f(x, other_lane<0x4e>(x));
+    x = f(x, other_lane<0x141>(x));
+    x = f(x, other_lane<0x140>(x));
+    x = f(x, other_lane<0x142>(x));
+    x = f(x, other_lane<0x143>(x));
+    return __builtin_amdgcn_readlane(x, 63);
+}
+
+// of values that are no NaN
+__device__ __forceinline__ float wave_largest(float x) {
+    return __builtin_bit_cast(
+        float, wave_over(__builtin_bit_cast(int, x), [](int a, int b) {
+            return __builtin_bit_cast(int, fmaxf(__builtin_bit_cast(float, a),
+                                                 __builtin_bit_cast(float, b)));
+        }));
+}
+
+__device__ __forceinline__ int wave_smallest(int x) {
+    return wave_over(x, [](int a, int b) { return min(a, b); });
+}
+
 // How a launch is cut: `parts` workgroups share a node's row, each wave of them
 // takes `per` slices of 512 tokens, one after the other.
 struct Cut {
@@ -214,13 +247,12 @@ struct Running {
     float of[kLane];
 };
 
-// The lane's 8 tokens v0 + 8 l .. of a slice; kTail: of which only the first
-// `left` are in the row.
-template <typename E, typename O, bool kTail>
+// The lane's 8 tokens v0 + 8 l .. of a slice, of which the first `left` are in
+// the row; the mask has no others.
+template <typename E, typename O>
 __device__ __forceinline__ void slice_of(const LogitsArgs &a, const Node &n, int64_t bias0,
                                          const Eight<E> &z, const Eight<Bf16> &count, uint32_t mask,
-                                         int slice, int left, void *out,
-                                         Running &best) {
+                                         int slice, int left, void *out, Running &best) {
     const int l = threadIdx.x & 63, v0 = slice * kSlice;
     float y[kLane];
 #pragma unroll
@@ -320,12 +352,9 @@ __device__ __forceinline__ void slice_of(const LogitsArgs &a, const Node &n, int
         typename O::type *o = static_cast<typename O::type *>(out) + v0 + kLane * l;
         Eight<O> r;
         r.set(y);
-        if (kTail) r.store(o, left);
+        if ((slice + 1) * kSlice > a.vocab) r.store(o, left);
         else r.store(o);
     }
-    if (kTail)
-#pragma unroll
-        for (int e = 0; e < kLane; ++e) y[e] = e < left ? y[e] : -__builtin_inff();
     float top = y[0];
 #pragma unroll
     for (int e = 1; e < kLane; ++e) top = fmaxf(top, y[e]);
@@ -337,7 +366,7 @@ __device__ __forceinline__ void slice_of(const LogitsArgs &a, const Node &n, int
     for (int e = 0; e < kLane; ++e) best.of[e] = up ? y[e] : best.of[e];
 }
 
-// Loads run two slices ahead of the work.  Which of a lane's 8 tokens is the
+// Loads run a slice ahead of the work.  Which of a lane's 8 tokens is the
 // largest is looked up once, at the end.
 template <typename E, typename O>
 __global__ __launch_bounds__(kMostThreads) void logits_kernel(LogitsArgs a, Cut cut) {
@@ -348,16 +377,17 @@ __global__ __launch_bounds__(kMostThreads) void logits_kernel(LogitsArgs a, Cut 
     const int part = (int)blockIdx.x % cut.parts, node = (int)blockIdx.x / cut.parts;
     const int b = node / a.n, i = node % a.n, waves = cut.threads / 64;
     const int first = (part * waves + w) * cut.per, end = min(first + cut.per, cut.slices);
-    const int full = min(end, a.vocab / kSlice);                 // the row may end inside a slice
-
     int slot = 0, fault = 0;
     if (a.counts) {
         slot = a.slot ? a.slot[b] : b;
         if (slot < 0 || slot >= a.slots) fault = kFaultBadSlot, slot = 0;
     }
     const T *z = static_cast<const T *>(a.logits) + node * a.stride;
-    const uint16_t *counts = reinterpret_cast<const uint16_t *>(a.counts) +
-                             (a.counts ? slot * a.counts_stride : 0);
+    // without a table any bytes, none of them kept: loads have no branch
+    const uint16_t *counts =
+        a.counts ? reinterpret_cast<const uint16_t *>(a.counts) + slot * a.counts_stride
+                 : reinterpret_cast<const uint16_t *>(z);
+    const uint32_t keep = a.counts ? ~0u : 0u;
     // a lane's 8 tokens are a byte of the mask; without one any byte, all bits set
     const uint8_t *mask = static_cast<const uint8_t *>(a.logits);
     if (a.mask)
@@ -365,21 +395,24 @@ __global__ __launch_bounds__(kMostThreads) void logits_kernel(LogitsArgs a, Cut 
             a.mask + ((int64_t)b * a.mask_rows + (a.mask_rows > 1 ? i : 0)) * ((a.vocab + 31) / 32));
     const int mask_lane = a.mask ? l : 0, mask_step = a.mask ? kSlice / 8 : 0;
     const uint32_t all = a.mask ? 0u : 255u;
+    // tokens of a lane in slice s
+    auto left = [&](int s) { return min(max(a.vocab - s * kSlice - kLane * l, 0), kLane); };
     struct Loaded {
         Eight<E> z;
         Eight<Bf16> count;
         uint32_t mask;
     };
-    auto load = [&](int s, Loaded &x) {
+    Loaded x[kAhead] = {};
+    const int full = a.vocab / kSlice;           // the row may end inside a slice
+    auto load = [&](int s, Loaded &x) {          // of the whole ones
+        s = min(s, full - 1);
         x.z.load(z + (int64_t)s * kSlice + kLane * l);
-        if (a.counts) x.count.load(counts + (int64_t)s * kSlice + kLane * l);
+        x.count.load(counts + (int64_t)s * kSlice + kLane * l);
         x.mask = mask[s * mask_step + mask_lane];
     };
-    Loaded x0 = {}, x1 = {}, x2 = {};
-    if (first < full) {
-        load(first, x0);
-        load(min(first + 1, full - 1), x1);
-    }
+    if (first < end && full > 0)
+#pragma unroll
+        for (int k = 0; k + 1 < kAhead; ++k) load(first + k, x[k]);
 
     // lanes 0, 1 and 2 fetch the penalties; nothing is used before all loads are out
     float penalty = l == 0 ? 1.f : 0.f;
@@ -408,12 +441,15 @@ __global__ __launch_bounds__(kMostThreads) void logits_kernel(LogitsArgs a, Cut 
     if (a.parent) {
         if (__any(!parent_ok(parent[0], l) || !parent_ok(parent[1], 64 + l)))
             fault |= kFaultBadParent;
-        else
-            for (int up = i; up >= 0;
-                 up = __builtin_amdgcn_readlane(up < 64 ? parent[0] : parent[1], up & 63)) {
-                if (l == (up & 63) && up < 64) n.token[0] = token[0];
-                if (l == (up & 63) && up >= 64) n.token[1] = token[1];
-            }
+        uint64_t path[2] = {0, 0};
+        for (int up = fault ? -1 : i; up >= 0;) {
+            path[up >> 6] |= 1ull << (up & 63);
+            up = up < 64 ? __builtin_amdgcn_readlane(parent[0], up)
+                         : __builtin_amdgcn_readlane(parent[1], up - 64);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (path[k] >> l & 1) n.token[k] = token[k];
     }
     auto ours = [&](int t) { return t >= first * kSlice && t < end * kSlice; };
     n.any = __any(ours(n.token[0]) || ours(n.token[1]) || ours(n.bias_tok));
@@ -432,40 +468,36 @@ __global__ __launch_bounds__(kMostThreads) void logits_kernel(LogitsArgs a, Cut 
                  t += 64)
                 out[t] = O::bits(__builtin_nanf(""));
     } else {
-        auto work = [&](const Loaded &x, int s) {
-            slice_of<E, O, false>(a, n, bias0, x.z, x.count, x.mask | all, s, 0, out, best);
-        };
-        for (int s = first; s < full; s += 3) {
-            load(min(s + 2, full - 1), x2);
-            work(x0, s);
-            if (s + 1 >= full) break;
-            load(min(s + 3, full - 1), x0);
-            work(x1, s + 1);
-            if (s + 2 >= full) break;
-            load(min(s + 4, full - 1), x1);
-            work(x2, s + 2);
-        }
-        if (full < end && first < end) {         // the last slice of the row, in part
-            const int left = min(max(a.vocab - full * kSlice - kLane * l, 0), kLane);
-            const int64_t at = (int64_t)full * kSlice + kLane * l;
-            x0.z.load(z + at, left);
-            if (a.counts) x0.count.load(counts + at, left);
-            x0.mask = left > 0 ? mask[full * mask_step + mask_lane] : 0u;
-            slice_of<E, O, true>(a, n, bias0, x0.z, x0.count, x0.mask | all, full, left, out,
-                                 best);
-        }
+        for (int s0 = first; s0 < end; s0 += kAhead)
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int s = s0 + k;
+                if (s >= end) break;
+                if (full > 0) load(s + kAhead - 1, x[(k + kAhead - 1) % kAhead]);
+                if (s == full) {
+                    const int64_t at = (int64_t)s * kSlice + kLane * l;
+                    const int n = left(s);
+                    x[k].z.load(z + at, n);
+                    x[k].count.load(counts + at, n);
+                    x[k].mask = n > 0 ? mask[s * mask_step + mask_lane] : 0u;
+                    x[k].mask = (x[k].mask | all) & ((1u << n) - 1);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[k].count.raw.x[j] &= keep;
+                slice_of<E, O>(a, n, bias0, x[k].z, x[k].count, x[k].mask | (s == full ? 0u : all), s,
+                               left(s), out, best);
+            }
     }
     if (!a.best) return;
     // the lane's first token with its largest value, then the wave's, then the workgroup's
     int at = 0;
 #pragma unroll
     for (int e = kLane - 1; e >= 0; --e) at = best.of[e] == best.value ? e : at;
-    Best mine = kNothing;
-    if (best.value > -__builtin_inff())
-        mine.value = best.value, mine.token = best.slice * kSlice + kLane * l + at;
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1)
-        better(mine, {__shfl_xor(mine.value, o), __shfl_xor(mine.token, o)});
+    Best mine;
+    mine.value = wave_largest(best.value);
+    mine.token = wave_smallest(best.value == mine.value && mine.value > -__builtin_inff()
+                                   ? best.slice * kSlice + kLane * l + at
+                                   : kNone);
     if (l == 0) s_best[w] = mine;
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -488,19 +520,25 @@ __global__ __launch_bounds__(64) void logits_join_kernel(LogitsArgs a, int parts
     if (l == 0) a.best[node] = best.token == kNone ? -1 : best.token;
 }
 
-// About 4096 waves, 16 a compute unit: enough loads in flight, and no more of
-// what each of them does once.  Up to 8 waves of a node are one workgroup and
-// need no joining; more of them are groups of four.
+// About 5120 waves, 20 a compute unit: enough loads in flight, and no more of
+// what each of them does once.  Up to 16 waves of a node are one workgroup and
+// need no joining, as many on each of a compute unit's four SIMDs (two
+// workgroups of 8 fit one, of 10 they do not); more are groups of four.
+// 512 nodes of 256 slices: 8 waves each 48 us, 10 59, 16 51, 32 (groups) 58;
+// 64 nodes of 196 slices: 17 groups of three slices a wave 15.4 us, of one
+// slice 18.2, of eight 18.9, one workgroup of 16 waves 25.5;
+// one node of 63 slices: 16 groups 9.1 us, one workgroup of 16 waves 10.2.
 Cut cut_of(const LogitsArgs &a) {
     Cut c;
     const int64_t nodes = (int64_t)a.batch * a.n;
     c.slices = (a.vocab + kSlice - 1) / kSlice;
-    int64_t waves = nodes < 4096 ? 4096 / nodes : 1;
+    int64_t waves = nodes < 5120 ? 5120 / nodes : 1;
+    if (waves <= 16) waves = waves > 11 ? 16 : waves > 4 ? 8 : waves;
     if (waves > c.slices) waves = c.slices;
     c.per = (int)((c.slices + waves - 1) / waves);
     waves = (c.slices + c.per - 1) / c.per;
-    c.parts = waves <= 8 ? 1 : (int)((waves + 3) / 4);
-    c.threads = 64 * (waves <= 8 ? (int)waves : 4);
+    c.parts = waves <= 16 ? 1 : (int)((waves + 3) / 4);
+    c.threads = 64 * (waves > 16 ? 4 : waves > 4 ? ((int)waves + 3) / 4 * 4 : (int)waves);
     return c;
 }
 
