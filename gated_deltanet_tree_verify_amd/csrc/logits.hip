@@ -116,7 +116,7 @@ __global__ __launch_bounds__(kThreads) void count_prompt_kernel(
     if (a.status && blockIdx.y == 0 && tid == 0) a.status[r] = fault;
     if (fault) return;
     const int v0 = (int)blockIdx.y * kMarkTokens, n = min(kMarkTokens, a.vocab - v0);
-    for (int i = first + tid; i < end; i += kThreads) {
+    for (int64_t i = (int64_t)first + tid; i < end; i += kThreads) {
         const uint32_t t = (uint32_t)tokens[i] - (uint32_t)v0;
         if (t < (uint32_t)n) atomicOr(&s_bits[t >> 5], 1u << (t & 31));
     }
@@ -154,8 +154,8 @@ __global__ __launch_bounds__(kThreads) void count_commit_kernel(
     for (int j0 = 0; j0 < m; j0 += 64) {
         const int t = j0 + tid < m ? tokens[(size_t)r * n + p[j0 + tid]] : -1;
         int same = 0, lowest = 64;
-        for (int i = 63; i >= 0; --i)
-            if (__shfl(t, i) == t) ++same, lowest = i;
+        for (int i = min(64, m - j0) - 1; i >= 0; --i)
+            if (__builtin_amdgcn_readlane(t, i) == t) ++same, lowest = i;
         if (t >= 0 && t < a.vocab && lowest == tid) {
             const int16_t c = row[t];
             row[t] = (int16_t)((c & -32768) | min((c & 32767) + same, 32767));
