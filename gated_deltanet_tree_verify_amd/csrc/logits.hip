@@ -223,8 +223,9 @@ struct Node {
     bool plain;              // far from the ends of fp32: a quotient by fused steps is exact
     float pres, freq;
     int token[2];            // of the nodes l and 64 + l, if they are on the node's path, or -1
-    int bias_tok;            // the first 64 biases stay in the lanes
-    float bias;
+    int bias_tok;            // the biases of the wave's slices, in order, up to 64 of them;
+    float bias;              // none here where they are more (many)
+    bool many;
     bool any;                // any of these lies in the wave's slices
 };
 
@@ -274,7 +275,7 @@ __device__ __forceinline__ void slice_of(const LogitsArgs &a, const Node &n, int
                        __builtin_bit_cast(u16x2, count.raw.x[k]), u16x2{1, 1})) << 2 * k;
     }
     touched = (touched | touched >> 15) & mask;
-    if (__any(touched != 0) || (on_path[0] | on_path[1] | biased) || a.bias_len > 64) {
+    if (__any(touched != 0) || (on_path[0] | on_path[1] | biased) || n.many) {
         uint64_t more = 0;                       // a byte for each of the lane's tokens
         const bool any_path = (on_path[0] | on_path[1]) != 0;
 #pragma unroll
@@ -301,7 +302,7 @@ __device__ __forceinline__ void slice_of(const LogitsArgs &a, const Node &n, int
             }
         };
         add(biased, n.bias_tok, n.bias);
-        for (int j0 = 64; j0 < a.bias_len; j0 += 64) {
+        for (int j0 = 0; n.many && j0 < a.bias_len; j0 += 64) {
             const bool in = j0 + l < a.bias_len;
             const int t = in ? a.bias_tok[bias0 + j0 + l] : -1;
             add(inside(t), t, in ? a.bias[bias0 + j0 + l] : 0.f);
@@ -420,8 +421,9 @@ __global__ __launch_bounds__(kMostThreads) void logits_kernel(LogitsArgs a, Cut 
     if (l < 3 && from) penalty = from[b];
     Node n;
     const int64_t bias0 = (int64_t)b * a.bias_len;
-    n.bias_tok = -1, n.bias = 0.f;
-    if (l < a.bias_len) n.bias_tok = a.bias_tok[bias0 + l], n.bias = a.bias[bias0 + l];
+    n.bias_tok = -1, n.bias = 0.f, n.many = false;
+    if (l < a.bias_len && a.bias_len <= 64)
+        n.bias_tok = a.bias_tok[bias0 + l], n.bias = a.bias[bias0 + l];
     int parent[2] = {-1, -1}, token[2] = {-1, -1};
     if (a.parent)
 #pragma unroll
@@ -452,6 +454,23 @@ __global__ __launch_bounds__(kMostThreads) void logits_kernel(LogitsArgs a, Cut 
             if (path[k] >> l & 1) n.token[k] = token[k];
     }
     auto ours = [&](int t) { return t >= first * kSlice && t < end * kSlice; };
+    if (a.bias_len > 64) {
+        int held = 0;
+        for (int j0 = 0; j0 < a.bias_len && !n.many; j0 += 64) {
+            const bool in = j0 + l < a.bias_len;
+            const int t = in ? a.bias_tok[bias0 + j0 + l] : -1;
+            const int x = in ? __float_as_int(a.bias[bias0 + j0 + l]) : 0;
+            for (uint64_t hits = __ballot(ours(t)); hits && !n.many; hits &= hits - 1) {
+                const int j = __builtin_ctzll(hits);
+                const int tok = __builtin_amdgcn_readlane(t, j);
+                const float bias = __int_as_float(__builtin_amdgcn_readlane(x, j));
+                n.many = held == 64;
+                if (l == held) n.bias_tok = tok, n.bias = bias;
+                ++held;
+            }
+        }
+        if (n.many) n.bias_tok = -1;
+    }
     n.any = __any(ours(n.token[0]) || ours(n.token[1]) || ours(n.bias_tok));
     if (a.status && part == 0 && i == 0 && threadIdx.x == 0) a.status[b] = fault;
 

@@ -392,6 +392,25 @@ def test_kv_append(gpu_lib, lens, begin, Hq, Hkv, d, rot, page, dtype, layout, n
     check_append(x, raw, got, append_ref(x))
 
 
+@pytest.mark.parametrize("d,fused", [(8, True), (24, False)])
+def test_kv_append_many_requests(gpu_lib, d, fused):
+    """a thousand requests, several rows a wave, some requests not served"""
+    rng = np.random.default_rng(9)
+    lens = [int(n) for n in rng.integers(0, 17, 1100)]
+    begin = [int(b) if b % 7 else -1 for b in rng.integers(0, 40, 1100)]
+    x = append_case(lens, begin, 1, 1, d, 8, 16, "bf16", "half", "rms", 0, 3, 2, fused=fused)
+    assert sum(lens) > 2 * 4096
+    st = ints([-1] * len(lens))
+    q_out = torch.full((sum(lens) + 5, 1, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    k_out = torch.full_like(q_out, 7.0)
+    raw, got = run_append(gpu_lib, x, status=st, q_out=q_out, k_out=k_out)
+    torch.cuda.synchronize()
+    assert st.tolist() == [0] * len(lens)
+    check_append(x, raw, got, append_ref(x, [b >= 0 for b in begin]), slice(3, 3 + sum(lens)))
+    for y in got:
+        assert (y[:3] == 7).all() and (y[-2:] == 7).all()
+
+
 def test_kv_append_leaves_rows_of_nobody(gpu_lib):
     x = append_case([4, 0, 9], [3, 0, 20], 4, 2, 64, 64, 16, "bf16", "half", "rms", 0, 5, 6)
     q, k, _ = x["dev"]

@@ -140,6 +140,8 @@ CASES = [
     (300, 2, 520, "fp32", "fp32", "one", 9, 0),
     (1, 9, 100003, "bf16", "fp32", "node", 5, 5),
     (2, 17, 65544, "fp32", "fp32", "one", 5, 0),
+    (3, 1, 70000, "bf16", "fp32", "none", 65, 0),
+    (600, 1, 1025, "bf16", "bf16", "node", 3, 0),
 ]
 
 
@@ -210,6 +212,19 @@ def test_arbitrary_values(gpu_lib, dtype):
     slack = 8 * 2.0 ** -24 * size.amax(-1)
     assert (at >= top - slack).all()
     assert torch.equal(got, torch.where(at == top, best, got))
+
+
+@pytest.mark.parametrize("spread", [40, 600, 30000])
+@pytest.mark.parametrize("batch,n", [(1, 1), (3, 40)])
+def test_many_biases(gpu_lib, spread, batch, n):
+    """hundreds of them, on few tokens (which then add up to 20 in order) or on many"""
+    x = make(batch, n, 40000, "fp32", 25, bias=300, mask="none")
+    x["bias"] = (np.random.default_rng(26).integers(-2, spread, (batch, 300)), x["bias"][1])
+    ref, best, _ = reference(x)
+    z, kw = upload(x)
+    o = torch.empty(z.shape, device="cuda")
+    assert torch.equal(gpu_lib.adjust_logits(z, out=o, **kw).cpu().long(), best)
+    same(o, ref, torch.float32)
 
 
 def test_values_not_finite(gpu_lib):
