@@ -178,7 +178,13 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int spli
 // once, and handed to the lanes that need it through LDS.  The next heads are
 // loaded while the present ones are worked on, the first ones before the row's
 // place and angles are known.
+//
+// kSplit: half layout, sides of whole pieces.  kAdjacent: interleaved, whole
+// pieces turn.  kMixed: either, where pieces turn in part; a lane has two of them
+// as they lie, and the other side of its pairs comes through LDS.
 // ---------------------------------------------------------------------------
+enum Mode { kSplit, kAdjacent, kMixed };
+
 struct Part {
     const void *in;
     int64_t in_row, in_head;
@@ -306,11 +312,11 @@ struct Place {
     bool own[2], turns[2];
 };
 
-template <bool kHalf>
+template <Mode kMode>
 __device__ __forceinline__ Place place_of(const HeadsArgs &g, int lane, int need, int log) {
     Place p;
     const int c = min(lane, need - 1);
-    if (kHalf) {
+    if (kMode == kSplit) {
         const int rest = c - (g.rot >> 4);
         p.at[0] = rest < 0 ? 8 * c : g.rot + 16 * rest;
         p.at[1] = p.at[0] + (rest < 0 ? g.rot >> 1 : 8);
@@ -358,11 +364,13 @@ __device__ __forceinline__ Row find_row(const AppendArgs &a, int row, Cursor &c)
     return x;
 }
 
-template <typename E, bool kAppend, bool kHalf, bool kNorm>
+template <typename E, bool kAppend, Mode kMode, bool kNorm>
 __global__ __launch_bounds__(kThreads) void pieces_kernel(Pieces n) {
     typedef typename E::type T;
     __shared__ float2 s_turn[kWaves][GDN_MAX_HEAD_DIM / 2];
     __shared__ float s_weight[kNorm ? 2 : 1][kNorm ? GDN_MAX_HEAD_DIM : 1];
+    // a wave's heads: 64 lanes of 16 elements
+    __shared__ __attribute__((aligned(16))) float s_head[kWaves][kMode == kMixed ? 64 * 16 : 4];
     const AppendArgs &a = n.a;
     const HeadsArgs &g = a.h;
     const int l = threadIdx.x & 63;
@@ -379,7 +387,7 @@ __global__ __launch_bounds__(kThreads) void pieces_kernel(Pieces n) {
         }
         if (bad) return;
     }
-    const Place pl = place_of<kHalf>(g, l & ((1 << n.log) - 1), n.need, n.log);
+    const Place pl = place_of<kMode>(g, l & ((1 << n.log) - 1), n.need, n.log);
     const int mine = l >> n.log, per = 64 >> n.log;      // the lane's head of a group's
     const int tile = (int)blockIdx.x / n.splits, split = (int)blockIdx.x % n.splits;
     const int keys = n.part[1].before, values = n.part[2].before;
@@ -443,14 +451,24 @@ __global__ __launch_bounds__(kThreads) void pieces_kernel(Pieces n) {
             }
             continue;
         }
-        float2 cs[8] = {};
+        float2 cs[kMode == kMixed ? 16 : 8] = {};
+        const int half = g.rot >> 1;
+        const bool adjacent = g.layout == GDN_ROPE_INTERLEAVED;
         if (g.rot > 0) {
-            for (int i = l; i < g.rot >> 1; i += 64)
-                s_turn[w][i] = turn(x.place, g.inv_freq[i], g.scale);
-            __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-            if (kHalf) {
+            for (int i = l; i < half; i += 64) s_turn[w][i] = turn(x.place, g.inv_freq[i], g.scale);
+            exchange();
+            if (kMode == kMixed) {               // (cos, the sine with the other's sign)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int at = pl.at[e] + i;
+                        if (at >= g.rot) continue;
+                        const float2 t = s_turn[w][adjacent ? at >> 1 : at < half ? at : at - half];
+                        const bool first = adjacent ? at % 2 == 0 : at < half;
+                        cs[8 * e + i] = make_float2(t.x, first ? -t.y : t.y);
+                    }
+            } else if (kMode == kSplit) {
                 if (pl.turns[0])
 #pragma unroll
                     for (int i = 0; i < 8; ++i) cs[i] = s_turn[w][pl.at[0] + i];
@@ -459,7 +477,8 @@ __global__ __launch_bounds__(kThreads) void pieces_kernel(Pieces n) {
                 for (int e = 0; e < 2; ++e)
                     if (pl.turns[e])
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) cs[4 * e + i] = s_turn[w][pl.at[e] / 2 + i];
+                        for (int i = 0; i < 4; ++i)
+                            cs[4 * e + i] = s_turn[w][pl.at[e] / 2 + i];
             }
             __builtin_amdgcn_wave_barrier();
         }
@@ -495,11 +514,32 @@ __global__ __launch_bounds__(kThreads) void pieces_kernel(Pieces n) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) y[e][i] *= inv * by[e][i];
             }
-            if (kHalf) {
+            if constexpr (kMode == kSplit) {
                 if (pl.turns[0]) turn8(y[0], y[1], cs);
-            } else {
+            } else if constexpr (kMode == kAdjacent) {
                 if (pl.turns[0]) turn4(y[0], &cs[0]);
                 if (pl.turns[1]) turn4(y[1], &cs[4]);
+            } else {
+                float *mate = &s_head[w][mine * g.d];
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (pl.turns[e]) {
+                        Raw<F32> r;
+                        r.narrow(y[e]);
+                        r.store(mate + pl.at[e]);
+                    }
+                exchange();
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int at = pl.at[e] + i;
+                        if (at >= g.rot) continue;
+                        const float other =
+                            mate[adjacent ? at ^ 1 : at < half ? at + half : at - half];
+                        y[e][i] = fmaf(y[e][i], cs[8 * e + i].x, other * cs[8 * e + i].y);
+                    }
+                exchange();
             }
             Raw<E> done[2];
             done[0].narrow(y[0]);
@@ -518,11 +558,11 @@ __global__ __launch_bounds__(kThreads) void pieces_kernel(Pieces n) {
     }
 }
 
-// whether rows, heads and weights are in 16-byte pieces, and the two sides of
-// the half layout's pairs in pieces of their own
+// whether rows, heads and weights are in 16-byte pieces.  8192 rows of 40 heads
+// with a norm: 41 us (d 80, rot 20) and 40 (96, 24) in pieces, 133 and 156 without.
 bool in_pieces(const HeadsArgs &a) {
     const int step = a.dtype == GDN_DTYPE_F32 ? 4 : 8;
-    if (a.d % 8 != 0 || a.rot % (a.layout == GDN_ROPE_HALF ? 16 : 8) != 0) return false;
+    if (a.d % 8 != 0) return false;
     for (const HeadsPart *x : {&a.q, &a.k}) {
         if (x->heads == 0) continue;
         if (((uintptr_t)x->in | (uintptr_t)x->out | (uintptr_t)x->weight) % 16 != 0) return false;
@@ -553,7 +593,10 @@ template <typename E, bool kAppend>
 void launch_pieces(const AppendArgs &a, hipStream_t s) {
     const HeadsArgs &g = a.h;
     Pieces n{};
-    n.need = g.layout == GDN_ROPE_HALF ? g.rot / 16 + (g.d - g.rot + 15) / 16 : (g.d + 15) / 16;
+    const Mode mode = g.layout == GDN_ROPE_HALF ? g.rot % 16 == 0 ? kSplit : kMixed
+                      : g.rot % 8 == 0          ? kAdjacent
+                                                : kMixed;
+    n.need = mode == kSplit ? g.rot / 16 + (g.d - g.rot + 15) / 16 : (g.d + 15) / 16;
     while (1 << n.log < n.need) ++n.log;
     n.a = a;
     const HeadsPart v{a.v, a.v_row, a.v_head, nullptr, 0, 0, nullptr, 0, kAppend ? g.k.heads : 0};
@@ -572,15 +615,16 @@ void launch_pieces(const AppendArgs &a, hipStream_t s) {
     const int blocks = n.tiles * n.splits + report;
     if (blocks == 0) return;
     const dim3 grid((unsigned)blocks), block(kThreads);
-    const bool half = g.layout == GDN_ROPE_HALF, norm = g.norm != GDN_NORM_NONE;
-    if (half && norm)
-        hipLaunchKernelGGL((pieces_kernel<E, kAppend, true, true>), grid, block, 0, s, n);
-    else if (half)
-        hipLaunchKernelGGL((pieces_kernel<E, kAppend, true, false>), grid, block, 0, s, n);
-    else if (norm)
-        hipLaunchKernelGGL((pieces_kernel<E, kAppend, false, true>), grid, block, 0, s, n);
-    else
-        hipLaunchKernelGGL((pieces_kernel<E, kAppend, false, false>), grid, block, 0, s, n);
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, s, n); };
+    if (g.norm != GDN_NORM_NONE) {
+        if (mode == kSplit) go(pieces_kernel<E, kAppend, kSplit, true>);
+        else if (mode == kAdjacent) go(pieces_kernel<E, kAppend, kAdjacent, true>);
+        else go(pieces_kernel<E, kAppend, kMixed, true>);
+    } else {
+        if (mode == kSplit) go(pieces_kernel<E, kAppend, kSplit, false>);
+        else if (mode == kAdjacent) go(pieces_kernel<E, kAppend, kAdjacent, false>);
+        else go(pieces_kernel<E, kAppend, kMixed, false>);
+    }
 }
 
 template <typename E>

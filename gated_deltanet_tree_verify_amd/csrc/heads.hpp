@@ -58,6 +58,13 @@ __device__ __forceinline__ float2 turn(int64_t p, float f, float scale) {
     return make_float2(c * scale, s * scale);
 }
 
+// what a lane of the wave has written to LDS before is there for the others
+__device__ __forceinline__ void exchange() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 __device__ __forceinline__ float wave_sum(float x) {
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o);

@@ -119,6 +119,15 @@ ROPE = [
     ((6,), 3, 2, 40, 24, "interleaved", "bf16", True, range(6)),
     ((6,), 11, 2, 96, 96, "half", "fp32", True, range(6)),
     ((700,), 6, 2, 64, 32, "half", "bf16", True, range(3, 703)),
+    # pieces that turn in part
+    ((5,), 9, 2, 80, 20, "half", "bf16", True, range(7, 12)),
+    ((5,), 9, 2, 96, 24, "half", "fp32", True, range(7, 12)),
+    ((5,), 3, 2, 256, 250, "half", "fp16", True, range(7, 12)),
+    ((5,), 3, 2, 256, 254, "interleaved", "bf16", True, range(7, 12)),
+    ((5,), 17, 3, 8, 6, "half", "bf16", False, range(7, 12)),
+    ((5,), 17, 3, 8, 2, "interleaved", "bf16", False, range(7, 12)),
+    ((600,), 5, 1, 72, 72, "half", "bf16", True, range(7, 607)),
+    ((600,), 5, 1, 104, 50, "interleaved", "fp32", True, range(7, 607)),
 ]
 
 
@@ -151,6 +160,9 @@ NORM = [
     ((6,), 3, 5, 24, 16, "half", "fp16", True, "rms", "wide", 0.0, 1e-6),
     ((6,), 3, 5, 16, 16, "half", "bf16", True, "l2", "same", 0.0, 1e-6),
     ((600,), 7, 2, 128, 96, "half", "bf16", True, "rms", "same", 0.0, 1e-6),
+    ((600,), 7, 2, 80, 20, "half", "bf16", True, "rms", "heads", 0.0, 1e-6),
+    ((9,), 7, 2, 96, 36, "half", "fp16", True, "l2", "wide", 1.0, 1e-6),
+    ((9,), 7, 2, 88, 44, "interleaved", "bf16", True, "rms", "same", 0.0, 1e-6),
 ]
 
 
@@ -222,6 +234,24 @@ def test_turning_back(gpu_lib):
     back = gpu_lib.rope(there, None, -pos, f)[0].cpu()
     pair = q.double().abs().reshape(50, 4, 2, 64).sum(-2).repeat(1, 1, 2)
     assert ((back.double() - q.double()).abs() <= 4 * F * pair).all()
+
+
+@pytest.mark.parametrize("layout,rot", [("half", 20), ("interleaved", 20), ("half", 64),
+                                        ("interleaved", 48)])
+def test_values_not_finite_do_not_reach_what_is_copied(gpu_lib, layout, rot):
+    """also where a piece turns in part"""
+    q = torch.randn(3, 4, 80, generator=gen(37)).bfloat16()
+    q[1, 2, rot:] = float("inf")
+    q[2, 1, rot + 1] = NAN
+    got = gpu_lib.rope(q.cuda(), None, ints([5, 6, 7]), frequencies(rot).cuda(), layout=layout)[0]
+    got = got.cpu()
+    assert torch.isfinite(got[..., :rot]).all()
+    assert torch.equal(got[..., rot:].view(torch.int16), q[..., rot:].view(torch.int16))
+    q[1, 2, 0] = float("inf")
+    got = gpu_lib.rope(q.cuda(), None, ints([5, 6, 7]), frequencies(rot).cuda(), layout=layout)[0]
+    mate = rot // 2 if layout == "half" else 1
+    bad = ~torch.isfinite(got[1, 2, :rot].cpu())
+    assert bad.tolist() == [i in (0, mate) for i in range(rot)]
 
 
 def test_values_not_finite_stay_in_their_heads(gpu_lib):
@@ -299,6 +329,8 @@ APPEND = [
     ([300], [0], 3, 1, 8, 8, 4, "bf16", "half", "l2", True, False, 0),
     ([5, 6], [7, 0], 2, 1, 16, 0, 1, "fp16", "half", None, True, True, 0),
     ([2, 9] * 100, [1, 31] * 100, 2, 2, 64, 64, 32, "bf16", "half", "rms", True, True, 16),
+    ([2, 9, 31], [1, 31, 0], 5, 2, 80, 20, 16, "bf16", "half", "rms", True, True, 0),
+    ([2, 9, 31], [1, 31, 0], 5, 2, 88, 22, 16, "fp32", "interleaved", None, True, True, 0),
 ]
 
 
