@@ -29,6 +29,8 @@ constexpr int kLane = 8;                       // tokens of a lane
 constexpr int kSlice = 64 * kLane;             // and of a wave
 constexpr int kMarkTokens = 1 << 13;           // of a workgroup of count_prompt
 constexpr int kNone = 0x7fffffff;
+constexpr int kPutOffTokens = 128;             // of a wave
+constexpr int kPutOffSlices = 8;               // of a wave that puts tokens off, at least
 constexpr int kAhead = 2;                      // slices on their way, the one in work among them
 
 // 8 adjacent values as they lie in memory, at any address of their type
@@ -242,11 +244,108 @@ __device__ __forceinline__ float repeated(const Node &n, float z) {
     return z > 0.f ? q : z * n.rep;
 }
 
+// z' of a token with z, its entry x of the table, its count on the path, its bias
+__device__ __forceinline__ float adjusted(const Node &n, float z, uint32_t x, uint32_t path,
+                                          float bias) {
+    const int c = (int)((x & 32767u) + path);
+    const float less = n.freq * (float)c + n.pres, r = repeated(n, z);
+    return (x | path ? r : z) + (c > 0 ? bias - less : bias);
+}
+
+// The lane's tokens with a count, a bit each.  Only those that the mask has are
+// of interest: the others are -inf, whatever their count.
+__device__ __forceinline__ uint32_t counted(const Eight<Bf16> &count) {
+    uint32_t bits = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+        bits |= __builtin_bit_cast(uint32_t, __builtin_elementwise_min(
+                    __builtin_bit_cast(u16x2, count.raw.x[k]), u16x2{1, 1})) << 2 * k;
+    }
+    return (bits | bits >> 15) & 255u;
+}
+
+// y where the lane's mask has token e, -inf elsewhere
+__device__ __forceinline__ float allowed(float y, uint32_t mask, int e) {
+    const uint32_t keep = (uint32_t)__builtin_amdgcn_sbfe((int)mask, e, 1);
+    const uint32_t none = __float_as_uint(-__builtin_inff());
+    return __uint_as_float((__float_as_uint(y) & keep) | (none & ~keep));
+}
+
 struct Running {
     float value;             // the largest of a lane's groups of 8 tokens, the group's
     int slice;               // slice, and what it is the largest of
     float of[kLane];
 };
+
+// Touched tokens of a wave that are put off until there are 64 of them: a slice
+// has few, and each takes its lane as many instructions as 64 take all lanes.
+// A wave of few slices, and one that writes its logits, does them in place.
+struct Later {
+    int *list;               // in LDS, room for kPutOffTokens
+    int held;                // the same in all lanes
+    Best best;               // of those that the lane has done
+};
+
+// the first `count` of them, one a lane; the others move up
+template <typename E>
+__device__ __forceinline__ void settle(const LogitsArgs &a, const Node &n, int64_t bias0,
+                                       const typename E::type *z, const uint16_t *counts,
+                                       uint32_t keep, int count, Later &later) {
+    const int l = threadIdx.x & 63;
+    heads::exchange();
+    const bool in = l < count;
+    const int t = in ? later.list[l] : -1;
+    const int rest = later.held - count, up = l < rest ? later.list[count + l] : 0;
+    heads::exchange();
+    if (l < rest) later.list[l] = up;
+    later.held = rest;
+    const float z0 = in ? __builtin_canonicalizef(E::widen(z[t])) : 0.f;
+    const uint32_t x = in ? counts[t] & keep : 0u;
+    uint32_t path = 0;
+    float bias = 0.f;
+    if (n.any) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            for (uint64_t on = __ballot(n.token[k] >= 0); on; on &= on - 1)
+                path += __builtin_amdgcn_readlane(n.token[k], __builtin_ctzll(on)) == t ? 1u : 0u;
+        auto add = [&](int tok, float y) {
+            for (uint64_t on = __ballot(tok >= 0); on; on &= on - 1) {
+                const int j = __builtin_ctzll(on);
+                const float b = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(y), j));
+                if (__builtin_amdgcn_readlane(tok, j) == t) bias += b;
+            }
+        };
+        add(n.bias_tok, n.bias);
+        for (int j0 = 0; n.many && j0 < a.bias_len; j0 += 64) {
+            const bool one = j0 + l < a.bias_len;
+            add(one ? a.bias_tok[bias0 + j0 + l] : -1, one ? a.bias[bias0 + j0 + l] : 0.f);
+        }
+    }
+    const float y = adjusted(n, z0, x, path, bias);
+    // a lane's tokens ascend: an equal one is not better
+    if (in && y > later.best.value) later.best.value = y, later.best.token = t;
+}
+
+// The same tokens by their bits: those with a count, on the node's path or biased.
+__device__ __forceinline__ uint32_t touched_of(const LogitsArgs &a, const Node &n, int64_t bias0,
+                                               const Eight<Bf16> &count, uint32_t mask, int slice) {
+    const int l = threadIdx.x & 63, v0 = slice * kSlice + kLane * l;
+    uint32_t bits = counted(count);
+    auto add = [&](int t) {
+        for (uint64_t on = __ballot((uint32_t)t - (uint32_t)(slice * kSlice) < (uint32_t)kSlice); on;
+             on &= on - 1) {
+            const int at = __builtin_amdgcn_readlane(t, __builtin_ctzll(on)) - v0;
+            if ((uint32_t)at < (uint32_t)kLane) bits |= 1u << at;
+        }
+    };
+    if (n.any) {
+        add(n.token[0]), add(n.token[1]), add(n.bias_tok);
+        for (int j0 = 0; n.many && j0 < a.bias_len; j0 += 64)
+            add(j0 + l < a.bias_len ? a.bias_tok[bias0 + j0 + l] : -1);
+    }
+    return bits & mask;
+}
 
 // The lane's 8 tokens v0 + 8 l .. of a slice, of which the first `left` are in
 // the row; the mask has no others.
@@ -265,16 +364,7 @@ __device__ __forceinline__ void slice_of(const LogitsArgs &a, const Node &n, int
         on_path[0] = inside(n.token[0]), on_path[1] = inside(n.token[1]);
         biased = inside(n.bias_tok);
     }
-    // tokens that anything is known of, a bit each: those with a count first, as
-    // far as the mask has them (what it has not is -inf, whatever its count)
-    uint32_t touched = 0;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-        touched |= __builtin_bit_cast(uint32_t, __builtin_elementwise_min(
-                       __builtin_bit_cast(u16x2, count.raw.x[k]), u16x2{1, 1})) << 2 * k;
-    }
-    touched = (touched | touched >> 15) & mask;
+    uint32_t touched = counted(count) & mask;
     if (__any(touched != 0) || (on_path[0] | on_path[1] | biased) || n.many) {
         uint64_t more = 0;                       // a byte for each of the lane's tokens
         const bool any_path = (on_path[0] | on_path[1]) != 0;
@@ -307,12 +397,6 @@ __device__ __forceinline__ void slice_of(const LogitsArgs &a, const Node &n, int
             const int t = in ? a.bias_tok[bias0 + j0 + l] : -1;
             add(inside(t), t, in ? a.bias[bias0 + j0 + l] : 0.f);
         }
-        // z' of a token with z, its entry of the table, its count on the path and its bias
-        auto adjusted = [&](float z0, uint32_t x, uint32_t path, float d) {
-            const int c = (int)((x & 32767u) + path);
-            const float less = n.freq * (float)c + n.pres, r = repeated(n, z0);
-            return (x | path ? r : z0) + (c > 0 ? d - less : d);
-        };
         if (!__any(__popc(touched) > 2)) {
             // Few tokens of a slice are touched, seldom more than one of a lane:
             // the lanes take theirs one after the other.
@@ -331,24 +415,21 @@ __device__ __forceinline__ void slice_of(const LogitsArgs &a, const Node &n, int
 #pragma unroll
                     for (int e = 0; e < kLane; ++e) d = is[e] ? bias[e] : d;
                 if (any_path) path = (uint32_t)(more >> 8 * __builtin_ctz(one | 128u)) & 255u;
-                z0 = adjusted(z0, x, path, d);
+                z0 = adjusted(n, z0, x, path, d);
 #pragma unroll
                 for (int e = 0; e < kLane; ++e) y[e] = is[e] ? z0 : y[e];
             }
         } else {
 #pragma unroll
             for (int e = 0; e < kLane; ++e) {
-                const float z1 = adjusted(y[e], count_at(e), (uint32_t)(more >> 8 * e) & 255u, bias[e]);
+                const float z1 = adjusted(n, y[e], count_at(e), (uint32_t)(more >> 8 * e) & 255u,
+                                          bias[e]);
                 y[e] = touched >> e & 1 ? z1 : y[e];
             }
         }
     }
-    const uint32_t none = __float_as_uint(-__builtin_inff());
 #pragma unroll
-    for (int e = 0; e < kLane; ++e) {
-        const uint32_t keep = (uint32_t)__builtin_amdgcn_sbfe((int)mask, e, 1);
-        y[e] = __uint_as_float((__float_as_uint(y[e]) & keep) | (none & ~keep));
-    }
+    for (int e = 0; e < kLane; ++e) y[e] = allowed(y[e], mask, e);
     if constexpr (!__is_same(O, None)) {
         typename O::type *o = static_cast<typename O::type *>(out) + v0 + kLane * l;
         Eight<O> r;
@@ -367,15 +448,24 @@ __device__ __forceinline__ void slice_of(const LogitsArgs &a, const Node &n, int
     for (int e = 0; e < kLane; ++e) best.of[e] = up ? y[e] : best.of[e];
 }
 
+// Workgroups go to the eight XCDs in turn; neighbours in a sequence share its
+// counts, so each XCD gets a run of them (its L2 then has what they share).
+__device__ __forceinline__ int item_of(int block, int blocks) {
+    const int xcd = block & 7, each = blocks >> 3, more = blocks & 7;
+    return xcd * each + min(xcd, more) + (block >> 3);
+}
+
 // Loads run a slice ahead of the work.  Which of a lane's 8 tokens is the
 // largest is looked up once, at the end.
-template <typename E, typename O>
+template <typename E, typename O, bool kPutOff>
 __global__ __launch_bounds__(kMostThreads) void logits_kernel(LogitsArgs a, Cut cut) {
     typedef typename E::type T;
+    __shared__ int s_later[kPutOff ? kMostThreads / 64 : 1][kPutOff ? kPutOffTokens : 1];
     __shared__ Best s_best[kMostThreads / 64];
     const int l = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);      // the same in all lanes
-    const int part = (int)blockIdx.x % cut.parts, node = (int)blockIdx.x / cut.parts;
+    const int item = item_of((int)blockIdx.x, (int)gridDim.x);
+    const int part = item % cut.parts, node = item / cut.parts;
     const int b = node / a.n, i = node % a.n, waves = cut.threads / 64;
     const int first = (part * waves + w) * cut.per, end = min(first + cut.per, cut.slices);
     int slot = 0, fault = 0;
@@ -410,6 +500,21 @@ __global__ __launch_bounds__(kMostThreads) void logits_kernel(LogitsArgs a, Cut 
         x.z.load(z + (int64_t)s * kSlice + kLane * l);
         x.count.load(counts + (int64_t)s * kSlice + kLane * l);
         x.mask = mask[s * mask_step + mask_lane];
+    };
+    auto load_cut = [&](Loaded &x) {             // the one that is not
+        const int64_t at = (int64_t)full * kSlice + kLane * l;
+        const int n = left(full);
+        x.z.load(z + at, n);
+        x.count.load(counts + at, n);
+        x.mask = n > 0 ? (mask[full * mask_step + mask_lane] | all) & ((1u << n) - 1) : 0u;
+    };
+    // the largest of a lane's 8 logits that the mask has
+    auto largest = [&](const Eight<E> &z, uint32_t mask) {
+        float top = -__builtin_inff();
+#pragma unroll
+        for (int e = 0; e < kLane; ++e)
+            top = fmaxf(top, allowed(__builtin_canonicalizef(z.at(e)), mask, e));
+        return top;
     };
     if (first < end && full > 0)
 #pragma unroll
@@ -481,6 +586,8 @@ __global__ __launch_bounds__(kMostThreads) void logits_kernel(LogitsArgs a, Cut 
     best.value = -__builtin_inff(), best.slice = 0;
 #pragma unroll
     for (int e = 0; e < kLane; ++e) best.of[e] = -__builtin_inff();
+    Later later = {s_later[kPutOff ? w : 0], 0, kNothing};
+    auto settle64 = [&] { settle<E>(a, n, bias0, z, counts, keep, 64, later); };
     if (fault) {
         if constexpr (!__is_same(O, None))
             for (int64_t t = (int64_t)first * kSlice + l; t < min((int64_t)end * kSlice, (int64_t)a.vocab);
@@ -493,30 +600,68 @@ __global__ __launch_bounds__(kMostThreads) void logits_kernel(LogitsArgs a, Cut 
                 const int s = s0 + k;
                 if (s >= end) break;
                 if (full > 0) load(s + kAhead - 1, x[(k + kAhead - 1) % kAhead]);
-                if (s == full) {
-                    const int64_t at = (int64_t)s * kSlice + kLane * l;
-                    const int n = left(s);
-                    x[k].z.load(z + at, n);
-                    x[k].count.load(counts + at, n);
-                    x[k].mask = n > 0 ? mask[s * mask_step + mask_lane] : 0u;
-                    x[k].mask = (x[k].mask | all) & ((1u << n) - 1);
-                }
+                if (s == full) load_cut(x[k]);
+                x[k].mask |= s == full ? 0u : all;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) x[k].count.raw.x[j] &= keep;
-                slice_of<E, O>(a, n, bias0, x[k].z, x[k].count, x[k].mask | (s == full ? 0u : all), s,
-                               left(s), out, best);
+                if constexpr (!kPutOff) {
+                    slice_of<E, O>(a, n, bias0, x[k].z, x[k].count, x[k].mask, s, left(s), out, best);
+                    continue;
+                }
+                uint32_t touched = touched_of(a, n, bias0, x[k].count, x[k].mask, s);
+                const float top = largest(x[k].z, x[k].mask & ~touched);
+                // slices ascend: an equal one is not better
+                best.slice = top > best.value ? s : best.slice;
+                best.value = top > best.value ? top : best.value;
+                while (__any(touched != 0)) {
+                    if (later.held > kPutOffTokens - 64) settle64();
+                    const uint64_t have = __ballot(touched != 0);
+                    const int at = later.held + __builtin_amdgcn_mbcnt_hi(
+                                                    (uint32_t)(have >> 32),
+                                                    __builtin_amdgcn_mbcnt_lo((uint32_t)have, 0));
+                    if (touched) later.list[at] = s * kSlice + kLane * l + __builtin_ctz(touched);
+                    later.held += __popcll(have);
+                    touched &= touched - 1;
+                }
             }
+        if constexpr (kPutOff)
+            while (later.held > 0)
+                settle<E>(a, n, bias0, z, counts, keep, min(later.held, 64), later);
     }
     if (!a.best) return;
     // the lane's first token with its largest value, then the wave's, then the workgroup's
-    int at = 0;
+    Best own = kNothing;
+    if constexpr (kPutOff) {
+        // looked up once, in the lowest eight that have it: the logits are as they were
+        own = later.best;
+        const float most = wave_largest(fmaxf(own.value, best.value));
+        const int eight = wave_smallest(best.value == most && most > -__builtin_inff()
+                                            ? best.slice * 64 + l
+                                            : kNone);
+        if (eight != kNone) {
+            const int s = eight >> 6;
+            if (s == full) load_cut(x[0]);
+            else load(s, x[0]);
+            x[0].mask |= s == full ? 0u : all;
 #pragma unroll
-    for (int e = kLane - 1; e >= 0; --e) at = best.of[e] == best.value ? e : at;
+            for (int j = 0; j < 4; ++j) x[0].count.raw.x[j] &= keep;
+            const uint32_t mask = x[0].mask & ~touched_of(a, n, bias0, x[0].count, x[0].mask, s);
+            int at = kLane;
+#pragma unroll
+            for (int e = kLane - 1; e >= 0; --e)
+                at = (mask >> e & 1) && x[0].z.at(e) == most ? e : at;
+            if (l == (eight & 63)) better(own, {most, s * kSlice + kLane * l + at});
+        }
+    } else {
+        int at = 0;
+#pragma unroll
+        for (int e = kLane - 1; e >= 0; --e) at = best.of[e] == best.value ? e : at;
+        if (best.value > -__builtin_inff())
+            own.value = best.value, own.token = best.slice * kSlice + kLane * l + at;
+    }
     Best mine;
-    mine.value = wave_largest(best.value);
-    mine.token = wave_smallest(best.value == mine.value && mine.value > -__builtin_inff()
-                                   ? best.slice * kSlice + kLane * l + at
-                                   : kNone);
+    mine.value = wave_largest(own.value);
+    mine.token = wave_smallest(own.value == mine.value ? own.token : kNone);
     if (l == 0) s_best[w] = mine;
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -539,11 +684,13 @@ __global__ __launch_bounds__(64) void logits_join_kernel(LogitsArgs a, int parts
     if (l == 0) a.best[node] = best.token == kNone ? -1 : best.token;
 }
 
-// About 5120 waves, 20 a compute unit: enough loads in flight, and no more of
+// About 6144 waves, 24 a compute unit: enough loads in flight, and no more of
 // what each of them does once.  Up to 16 waves of a node are one workgroup and
-// need no joining, as many on each of a compute unit's four SIMDs (two
-// workgroups of 8 fit one, of 10 they do not); more are groups of four.
-// 512 nodes of 256 slices: 8 waves each 48 us, 10 59, 16 51, 32 (groups) 58;
+// need no joining, as many on each of a compute unit's four SIMDs and so many
+// that two workgroups fit (12 without, 8 with an output: registers); more are
+// groups of four.
+// 512 nodes of 256 slices: 12 waves each 40 us, 8 44, 16 49, 32 (groups) 58;
+// the same with an output: 8 waves 48, 12 56, 16 52;
 // 64 nodes of 196 slices: 17 groups of three slices a wave 15.4 us, of one
 // slice 18.2, of eight 18.9, one workgroup of 16 waves 25.5;
 // one node of 63 slices: 16 groups 9.1 us, one workgroup of 16 waves 10.2.
@@ -551,8 +698,9 @@ Cut cut_of(const LogitsArgs &a) {
     Cut c;
     const int64_t nodes = (int64_t)a.batch * a.n;
     c.slices = (a.vocab + kSlice - 1) / kSlice;
-    int64_t waves = nodes < 5120 ? 5120 / nodes : 1;
-    if (waves <= 16) waves = waves > 11 ? 16 : waves > 4 ? 8 : waves;
+    int64_t waves = nodes < 6144 ? 6144 / nodes : 1;
+    if (waves <= 16)
+        waves = waves > 13 ? 16 : waves > 8 ? (a.out ? 8 : 12) : waves > 4 ? 8 : waves;
     if (waves > c.slices) waves = c.slices;
     c.per = (int)((c.slices + waves - 1) / waves);
     waves = (c.slices + c.per - 1) / c.per;
@@ -564,8 +712,11 @@ Cut cut_of(const LogitsArgs &a) {
 template <typename E, typename O>
 hipError_t launch(const LogitsArgs &a, hipStream_t s) {
     const Cut c = cut_of(a);
-    hipLaunchKernelGGL((logits_kernel<E, O>), dim3((unsigned)(a.batch * a.n * c.parts)),
-                       dim3((unsigned)c.threads), 0, s, a, c);
+    const dim3 grid((unsigned)(a.batch * a.n * c.parts)), block((unsigned)c.threads);
+    if (__is_same(O, None) && c.per >= kPutOffSlices)
+        hipLaunchKernelGGL((logits_kernel<E, O, __is_same(O, None)>), grid, block, 0, s, a, c);
+    else
+        hipLaunchKernelGGL((logits_kernel<E, O, false>), grid, block, 0, s, a, c);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.best || c.parts == 1) return e;
     hipLaunchKernelGGL(logits_join_kernel, dim3((unsigned)(a.batch * a.n)), dim3(64), 0, s, a,
