@@ -323,8 +323,8 @@ __device__ __forceinline__ void settle(const LogitsArgs &a, const Node &n, int64
         }
     }
     const float y = adjusted(n, z0, x, path, bias);
-    // a lane's tokens ascend: an equal one is not better
-    if (in && y > later.best.value) later.best.value = y, later.best.token = t;
+    // within a slice they do not ascend: the second ones of all lanes follow the first
+    if (in && y > -__builtin_inff()) better(later.best, {y, t});
 }
 
 // The same tokens by their bits: those with a count, on the node's path or biased.

@@ -287,6 +287,47 @@ def test_ties_take_the_lowest_token(gpu_lib):
         assert gpu_lib.adjust_logits(z)[0, 0] == 0
 
 
+@pytest.mark.parametrize("dtype,bias,spread,mask,ties", [
+    ("bf16", 5, 40, "node", False), ("fp16", 300, 30, "node", False), ("fp32", 300, 30000, "one", False),
+    ("bf16", 5, 40, "none", True), ("fp16", 70, 13001, "node", True)])
+def test_many_nodes(gpu_lib, dtype, bias, spread, mask, ties):
+    """so many that a wave goes over many slices of a row, dense counts among them:
+    the greedy tokens alone, and with an output, equal those in 64 bits.  With three
+    values of logits the largest is there dozens of times a slice, with counts and
+    without."""
+    batch, n, V = 16, 128, 13001
+    x = make(batch, n, V, dtype, 31, bias=bias, mask=mask)
+    rng = np.random.default_rng(32)
+    x["bias"] = (rng.integers(-1, spread, (batch, bias)), x["bias"][1])
+    if ties:
+        x["z"] = torch.from_numpy(rng.integers(-1, 2, (batch, n, V)) / 8).to(DT[dtype])
+        x["repetition"][:] = 1
+        x["presence"][:] = x["frequency"][:] = 0
+        x["bias"][1][:] = 0
+    x["z"][:, 3, 9000:] = NAN
+    x["z"][:, 4, 100:] = -INF
+    x["z"][:, 5, :] = -INF
+    ref, best, _ = reference(x)
+    z, kw = upload(x)
+    got = gpu_lib.adjust_logits(z, **kw)
+    assert torch.equal(got.cpu().long(), best)
+    assert (got[:, 5] == -1).all()
+    o = torch.empty(z.shape, dtype=torch.float32, device="cuda")
+    assert torch.equal(gpu_lib.adjust_logits(z, out=o, **kw), got)
+    same(o, ref, torch.float32)
+
+
+def test_many_nodes_with_faults(gpu_lib):
+    x = make(16, 128, 13001, "bf16", 33)
+    x["slot"][2] = 99
+    x["parent"][5, 7] = 7
+    z, kw = upload(x)
+    st = ints([-1] * 16)
+    got = gpu_lib.adjust_logits(z, status=st, **kw)
+    assert [i for i, f in enumerate(st.tolist()) if f] == [2, 5]
+    assert (got[[2, 5]] == -1).all() and (got[[0, 1, 3, 4, 6]] >= 0).all()
+
+
 def test_a_chain_counts_every_node_once(gpu_lib):
     """128 nodes in a row with the same token: its count is the depth + 1"""
     V = 1000
