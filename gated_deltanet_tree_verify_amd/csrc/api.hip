@@ -79,8 +79,8 @@ bool strides_ok(int64_t row, int64_t head) {
 bool apart(int rows, int64_t row, int heads, int64_t head, int d) {
     if (rows <= 1) return heads <= 1 || head >= d;
     if (heads <= 1) return row >= d;
-    return (head >= d && row >= (heads - 1) * head + d) ||
-           (row >= d && head >= (rows - 1) * row + d);
+    return (head >= d && row >= d && (row - d) / head >= heads - 1) ||
+           (row >= d && head >= d && (head - d) / row >= rows - 1);
 }
 
 gdn_status part_status(const gdn::HeadsPart &x, const gdn::HeadsArgs &a, bool out_needed) {

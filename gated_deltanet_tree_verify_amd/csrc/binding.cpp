@@ -134,6 +134,10 @@ bool walk(const at::Tensor &x, int64_t tail, Rows &r) {
     for (--i; i >= 0; --i) {
         const int64_t size = x.size(i);
         if (size == 1) continue;
+        if (size == 0) {             // no rows: their strides say nothing
+            r.count = 0;
+            return true;
+        }
         if (first) r.stride = x.stride(i);
         else if (x.stride(i) != r.stride * r.count) return false;
         first = false;

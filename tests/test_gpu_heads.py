@@ -279,6 +279,12 @@ def test_no_rows(gpu_lib):
     q = torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda")
     a, b = gpu_lib.rope(q, q, ints([]), frequencies(64).cuda())
     assert a.shape == q.shape and b.shape == q.shape
+    for lead in ((2, 0), (0, 2)):
+        q, f = torch.empty(*lead, 4, 64, dtype=torch.float16, device="cuda"), frequencies(64).cuda()
+        pos, base = torch.empty(lead, dtype=torch.int32, device="cuda"), ints([3] * lead[0])
+        for given in (None, q):
+            a, b = gpu_lib.qk_norm_rope(q, q, None, None, pos, f, base=base, q_out=given, k_out=given)
+            assert a.shape == q.shape and b.shape == q.shape
 
 
 # ---------------------------------------------------------------------------

@@ -45,6 +45,15 @@ def test_norm_refuses(lib, kw, code):
     assert norm(lib, **kw) == code
 
 
+def test_strides_beyond_64_bits_are_weighed(lib):
+    """rows times a row's stride would not fit: heads inside such rows are fine, rows
+    between such heads are not"""
+    far = 1 << 40
+    assert norm(lib, rows=(1 << 25), out_row=far, out_head=far, k_row=far, Hk=0) == -1
+    assert norm(lib, rows=(1 << 30), out_row=far, out_head=far, Hk=0) == -1
+    assert norm(lib, rows=(1 << 25), out_row=64, out_head=(1 << 30), Hq=2, Hk=0) == -1
+
+
 def test_nothing_to_do_is_no_error(lib):
     assert norm(lib, rows=0) == 0
     assert norm(lib, rows=0, q=None, k=None) == 0
@@ -271,6 +280,9 @@ def test_rows_of_strided_tensors():
         assert rows(big, (torch.float32,), 2) is None
         assert rows(torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda"), bf16,
                     2) == (0, 256, 4, 64, 64)
+        for lead in ((2, 0), (0, 2), (3, 0, 2)):
+            none = torch.empty(*lead, 4, 64, dtype=torch.bfloat16, device="cuda")
+            assert rows(none, bf16, 2)[0] == 0
         assert g._native().on_device(0, big, None, 3) and not g._native().on_device(1, big)
     assert rows(torch.empty(3, 4, 64, dtype=torch.bfloat16), bf16, 2) is None
     with pytest.raises(TypeError):
