@@ -31,6 +31,7 @@ constexpr int kMarkTokens = 1 << 13;           // of a workgroup of count_prompt
 constexpr int kNone = 0x7fffffff;
 constexpr int kPutOffTokens = 128;             // of a wave
 constexpr int kPutOffSlices = 8;               // of a wave that puts tokens off, at least
+constexpr int kInPlaceLanes = 24;              // with touched tokens: a slice that puts none off
 constexpr int kAhead = 2;                      // slices on their way, the one in work among them
 
 // 8 adjacent values as they lie in memory, at any address of their type
@@ -226,9 +227,11 @@ struct Node {
     float pres, freq;
     int token[2];            // of the nodes l and 64 + l, if they are on the node's path, or -1
     int bias_tok;            // the biases of the wave's slices, in order, up to 64 of them;
-    float bias;              // none here where they are more (many)
-    bool many;
+    float bias;              // none here where they are more
+    uint64_t many;           // then: the slices, counted from the wave's first, modulo 64, that have some
+    int first;
     bool any;                // any of these lies in the wave's slices
+    __device__ __forceinline__ bool many_in(int slice) const { return many >> (slice - first & 63) & 1; }
 };
 
 // z / rep for z above 0, z rep otherwise, correctly rounded.  With r the
@@ -278,6 +281,19 @@ struct Running {
     float of[kLane];
 };
 
+constexpr float kLeast = -__builtin_inff();
+constexpr Running kNoneYet = {kLeast, 0, {kLeast, kLeast, kLeast, kLeast, kLeast, kLeast, kLeast,
+                                          kLeast}};
+
+// the lane's first token with its largest value
+__device__ __forceinline__ Best best_of(const Running &x) {
+    int at = 0;
+#pragma unroll
+    for (int e = kLane - 1; e >= 0; --e) at = x.of[e] == x.value ? e : at;
+    if (!(x.value > kLeast)) return kNothing;
+    return {x.value, x.slice * kSlice + kLane * (int)(threadIdx.x & 63) + at};
+}
+
 // Touched tokens of a wave that are put off until there are 64 of them: a slice
 // has few, and each takes its lane as many instructions as 64 take all lanes.
 // A wave of few slices, and one that writes its logits, does them in place.
@@ -287,7 +303,38 @@ struct Later {
     Best best;               // of those that the lane has done
 };
 
-// the first `count` of them, one a lane; the others move up
+// token t of each lane, with logit z0 and entry x of the table; of the node's path
+// and biases only the lanes in path0, path1 and biased can have it
+__device__ __forceinline__ void settle_one(const LogitsArgs &a, const Node &n, int64_t bias0, bool in,
+                                           int t, float z0, uint32_t x, uint64_t path0,
+                                           uint64_t path1, uint64_t biased, bool many,
+                                           Later &later) {
+    const int l = threadIdx.x & 63;
+    uint32_t path = 0;
+    float bias = 0.f;
+    for (; path0; path0 &= path0 - 1)
+        path += __builtin_amdgcn_readlane(n.token[0], __builtin_ctzll(path0)) == t ? 1u : 0u;
+    for (; path1; path1 &= path1 - 1)
+        path += __builtin_amdgcn_readlane(n.token[1], __builtin_ctzll(path1)) == t ? 1u : 0u;
+    auto add = [&](uint64_t on, int tok, float y) {
+        for (; on; on &= on - 1) {
+            const int j = __builtin_ctzll(on);
+            const float b = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(y), j));
+            if (__builtin_amdgcn_readlane(tok, j) == t) bias += b;
+        }
+    };
+    add(biased, n.bias_tok, n.bias);
+    for (int j0 = 0; many && j0 < a.bias_len; j0 += 64) {
+        const bool one = j0 + l < a.bias_len;
+        const int tok = one ? a.bias_tok[bias0 + j0 + l] : -1;
+        add(__ballot(tok >= 0), tok, one ? a.bias[bias0 + j0 + l] : 0.f);
+    }
+    const float y = adjusted(n, z0, x, path, bias);
+    // the tokens of a lane do not ascend: the second ones of all follow the first
+    if (in && y > kLeast) better(later.best, {y, t});
+}
+
+// the first `count` of those put off, one a lane; the others move up
 template <typename E>
 __device__ __forceinline__ void settle(const LogitsArgs &a, const Node &n, int64_t bias0,
                                        const typename E::type *z, const uint16_t *counts,
@@ -302,29 +349,35 @@ __device__ __forceinline__ void settle(const LogitsArgs &a, const Node &n, int64
     later.held = rest;
     const float z0 = in ? __builtin_canonicalizef(E::widen(z[t])) : 0.f;
     const uint32_t x = in ? counts[t] & keep : 0u;
-    uint32_t path = 0;
-    float bias = 0.f;
-    if (n.any) {
+    settle_one(a, n, bias0, in, t, z0, x, n.any ? __ballot(n.token[0] >= 0) : 0,
+               n.any ? __ballot(n.token[1] >= 0) : 0, n.any ? __ballot(n.bias_tok >= 0) : 0,
+               n.many != 0, later);
+}
+
+// all touched tokens of a slice at once, each lane its own one after the other
+template <typename E>
+__device__ __forceinline__ void settle_slice(const LogitsArgs &a, const Node &n, int64_t bias0,
+                                             const Eight<E> &z, const Eight<Bf16> &count,
+                                             uint32_t touched, int slice, Later &later) {
+    const int v0 = slice * kSlice + kLane * (int)(threadIdx.x & 63);
+    auto inside = [&](int t) {
+        return n.any ? __ballot((uint32_t)t - (uint32_t)(slice * kSlice) < (uint32_t)kSlice) : 0;
+    };
+    const uint64_t path0 = inside(n.token[0]), path1 = inside(n.token[1]);
+    const uint64_t biased = inside(n.bias_tok);
+    while (__any(touched != 0)) {
+        const uint32_t one = touched & -touched;
+        touched ^= one;
+        float z0 = 0.f;
+        uint32_t x = 0;
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-            for (uint64_t on = __ballot(n.token[k] >= 0); on; on &= on - 1)
-                path += __builtin_amdgcn_readlane(n.token[k], __builtin_ctzll(on)) == t ? 1u : 0u;
-        auto add = [&](int tok, float y) {
-            for (uint64_t on = __ballot(tok >= 0); on; on &= on - 1) {
-                const int j = __builtin_ctzll(on);
-                const float b = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(y), j));
-                if (__builtin_amdgcn_readlane(tok, j) == t) bias += b;
-            }
-        };
-        add(n.bias_tok, n.bias);
-        for (int j0 = 0; n.many && j0 < a.bias_len; j0 += 64) {
-            const bool one = j0 + l < a.bias_len;
-            add(one ? a.bias_tok[bias0 + j0 + l] : -1, one ? a.bias[bias0 + j0 + l] : 0.f);
-        }
+        for (int e = 0; e < kLane; ++e) z0 = one == 1u << e ? z.at(e) : z0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x = one >> 2 * k & 3 ? count.raw.x[k] : x;
+        x = one & 0xaau ? x >> 16 : x & 65535u;
+        settle_one(a, n, bias0, one != 0, v0 + __builtin_ctz(one | 128u), __builtin_canonicalizef(z0),
+                   x, path0, path1, biased, n.many_in(slice), later);
     }
-    const float y = adjusted(n, z0, x, path, bias);
-    // within a slice they do not ascend: the second ones of all lanes follow the first
-    if (in && y > -__builtin_inff()) better(later.best, {y, t});
 }
 
 // The same tokens by their bits: those with a count, on the node's path or biased.
@@ -341,7 +394,7 @@ __device__ __forceinline__ uint32_t touched_of(const LogitsArgs &a, const Node &
     };
     if (n.any) {
         add(n.token[0]), add(n.token[1]), add(n.bias_tok);
-        for (int j0 = 0; n.many && j0 < a.bias_len; j0 += 64)
+        for (int j0 = 0; n.many_in(slice) && j0 < a.bias_len; j0 += 64)
             add(j0 + l < a.bias_len ? a.bias_tok[bias0 + j0 + l] : -1);
     }
     return bits & mask;
@@ -365,7 +418,8 @@ __device__ __forceinline__ void slice_of(const LogitsArgs &a, const Node &n, int
         biased = inside(n.bias_tok);
     }
     uint32_t touched = counted(count) & mask;
-    if (__any(touched != 0) || (on_path[0] | on_path[1] | biased) || n.many) {
+    const bool many = n.many_in(slice);
+    if (__any(touched != 0) || (on_path[0] | on_path[1] | biased) || many) {
         uint64_t more = 0;                       // a byte for each of the lane's tokens
         const bool any_path = (on_path[0] | on_path[1]) != 0;
 #pragma unroll
@@ -392,7 +446,7 @@ __device__ __forceinline__ void slice_of(const LogitsArgs &a, const Node &n, int
             }
         };
         add(biased, n.bias_tok, n.bias);
-        for (int j0 = 0; n.many && j0 < a.bias_len; j0 += 64) {
+        for (int j0 = 0; many && j0 < a.bias_len; j0 += 64) {
             const bool in = j0 + l < a.bias_len;
             const int t = in ? a.bias_tok[bias0 + j0 + l] : -1;
             add(inside(t), t, in ? a.bias[bias0 + j0 + l] : 0.f);
@@ -526,7 +580,7 @@ __global__ __launch_bounds__(kMostThreads) void logits_kernel(LogitsArgs a, Cut 
     if (l < 3 && from) penalty = from[b];
     Node n;
     const int64_t bias0 = (int64_t)b * a.bias_len;
-    n.bias_tok = -1, n.bias = 0.f, n.many = false;
+    n.bias_tok = -1, n.bias = 0.f, n.many = 0, n.first = first;
     if (l < a.bias_len && a.bias_len <= 64)
         n.bias_tok = a.bias_tok[bias0 + l], n.bias = a.bias[bias0 + l];
     int parent[2] = {-1, -1}, token[2] = {-1, -1};
@@ -561,31 +615,29 @@ __global__ __launch_bounds__(kMostThreads) void logits_kernel(LogitsArgs a, Cut 
     auto ours = [&](int t) { return t >= first * kSlice && t < end * kSlice; };
     if (a.bias_len > 64) {
         int held = 0;
-        for (int j0 = 0; j0 < a.bias_len && !n.many; j0 += 64) {
+        uint64_t at = 0;
+        for (int j0 = 0; j0 < a.bias_len; j0 += 64) {
             const bool in = j0 + l < a.bias_len;
             const int t = in ? a.bias_tok[bias0 + j0 + l] : -1;
             const int x = in ? __float_as_int(a.bias[bias0 + j0 + l]) : 0;
-            for (uint64_t hits = __ballot(ours(t)); hits && !n.many; hits &= hits - 1) {
+            for (uint64_t hits = __ballot(ours(t)); hits; hits &= hits - 1) {
                 const int j = __builtin_ctzll(hits);
                 const int tok = __builtin_amdgcn_readlane(t, j);
                 const float bias = __int_as_float(__builtin_amdgcn_readlane(x, j));
-                n.many = held == 64;
+                at |= 1ull << (tok / kSlice - first & 63);
                 if (l == held) n.bias_tok = tok, n.bias = bias;
                 ++held;
             }
         }
-        if (n.many) n.bias_tok = -1;
+        if (held > 64) n.many = at, n.bias_tok = -1;
     }
-    n.any = __any(ours(n.token[0]) || ours(n.token[1]) || ours(n.bias_tok));
+    n.any = n.many != 0 || __any(ours(n.token[0]) || ours(n.token[1]) || ours(n.bias_tok));
     if (a.status && part == 0 && i == 0 && threadIdx.x == 0) a.status[b] = fault;
 
     typename O::type *out = nullptr;
     if constexpr (!__is_same(O, None))
         out = static_cast<typename O::type *>(a.out) + node * a.out_stride;
-    Running best;
-    best.value = -__builtin_inff(), best.slice = 0;
-#pragma unroll
-    for (int e = 0; e < kLane; ++e) best.of[e] = -__builtin_inff();
+    Running best = kNoneYet;
     Later later = {s_later[kPutOff ? w : 0], 0, kNothing};
     auto settle64 = [&] { settle<E>(a, n, bias0, z, counts, keep, 64, later); };
     if (fault) {
@@ -613,6 +665,10 @@ __global__ __launch_bounds__(kMostThreads) void logits_kernel(LogitsArgs a, Cut 
                 // slices ascend: an equal one is not better
                 best.slice = top > best.value ? s : best.slice;
                 best.value = top > best.value ? top : best.value;
+                if (__popcll(__ballot(touched != 0)) > kInPlaceLanes) {
+                    settle_slice<E>(a, n, bias0, x[k].z, x[k].count, touched, s, later);
+                    continue;
+                }
                 while (__any(touched != 0)) {
                     if (later.held > kPutOffTokens - 64) settle64();
                     const uint64_t have = __ballot(touched != 0);
@@ -653,11 +709,7 @@ __global__ __launch_bounds__(kMostThreads) void logits_kernel(LogitsArgs a, Cut 
             if (l == (eight & 63)) better(own, {most, s * kSlice + kLane * l + at});
         }
     } else {
-        int at = 0;
-#pragma unroll
-        for (int e = kLane - 1; e >= 0; --e) at = best.of[e] == best.value ? e : at;
-        if (best.value > -__builtin_inff())
-            own.value = best.value, own.token = best.slice * kSlice + kLane * l + at;
+        own = best_of(best);
     }
     Best mine;
     mine.value = wave_largest(own.value);

@@ -317,6 +317,22 @@ def test_many_nodes(gpu_lib, dtype, bias, spread, mask, ties):
     same(o, ref, torch.float32)
 
 
+@pytest.mark.parametrize("density", [0.02, 0.06, 0.3, 1.0])
+@pytest.mark.parametrize("spread", [40, 13001])
+def test_many_nodes_by_density(gpu_lib, density, spread):
+    """few or all tokens of a slice counted, hundreds of biases, with a path and without"""
+    batch, n, V = 16, 128, 13001
+    x = make(batch, n, V, "bf16", 41, bias=300, mask="one")
+    rng = np.random.default_rng(42)
+    x["counts"] = np.where(rng.random(x["counts"].shape) < density,
+                           rng.choice([1, 2, 7, -32768, -32765], x["counts"].shape), 0).astype(np.int16)
+    x["bias"] = (rng.integers(-1, spread, (batch, 300)), x["bias"][1])
+    for skip in ([], ["tokens"], ["counts"], ["counts", "tokens"]):
+        _, best, _ = reference(x, skip)
+        z, kw = upload(x, skip)
+        assert torch.equal(gpu_lib.adjust_logits(z, **kw).cpu().long(), best), skip
+
+
 def test_many_nodes_with_faults(gpu_lib):
     x = make(16, 128, 13001, "bf16", 33)
     x["slot"][2] = 99
