@@ -218,7 +218,15 @@ __device__ __forceinline__ int wave_smallest(int x) {
 struct Cut {
     int slices, per, parts;
     int threads;
+    int listed;              // biases of a wave that its list in LDS has room for
 };
+
+struct Biased {
+    int token;
+    float bias;
+};
+
+constexpr int kListed = 432;     // the lists of 16 waves and the rest stay below 64 KiB
 
 // What a wave knows of its node.
 struct Node {
@@ -228,11 +236,29 @@ struct Node {
     int token[2];            // of the nodes l and 64 + l, if they are on the node's path, or -1
     int bias_tok;            // the biases of the wave's slices, in order, up to 64 of them;
     float bias;              // none here where they are more
-    uint64_t many;           // then: the slices, counted from the wave's first, modulo 64, that have some
+    uint64_t many;           // then: the slices, counted from the wave's first, modulo 64, that have some,
+    const Biased *list;      // and the list of them in LDS,
+    int listed;              // so many; -1: more than it has room for, the sequence's are gone over
     int first;
     bool any;                // any of these lies in the wave's slices
     __device__ __forceinline__ bool many_in(int slice) const { return many >> (slice - first & 63) & 1; }
 };
+
+// f(token, bias) of 64 biases of the wave at a time, in order (token -1: none)
+template <typename F>
+__device__ __forceinline__ void each_bias(const LogitsArgs &a, const Node &n, int64_t bias0, F f) {
+    const int l = threadIdx.x & 63;
+    if (n.listed >= 0)
+        for (int j = l; j - l < n.listed; j += 64) {
+            const Biased x = j < n.listed ? n.list[j] : Biased{-1, 0.f};
+            f(x.token, x.bias);
+        }
+    else
+        for (int j = l; j - l < a.bias_len; j += 64) {
+            const bool in = j < a.bias_len;
+            f(in ? a.bias_tok[bias0 + j] : -1, in ? a.bias[bias0 + j] : 0.f);
+        }
+}
 
 // z / rep for z above 0, z rep otherwise, correctly rounded.  With r the
 // rounded reciprocal and q = z r, the residue z - q rep is exact in a fused
@@ -309,7 +335,6 @@ __device__ __forceinline__ void settle_one(const LogitsArgs &a, const Node &n, i
                                            int t, float z0, uint32_t x, uint64_t path0,
                                            uint64_t path1, uint64_t biased, bool many,
                                            Later &later) {
-    const int l = threadIdx.x & 63;
     uint32_t path = 0;
     float bias = 0.f;
     for (; path0; path0 &= path0 - 1)
@@ -324,11 +349,8 @@ __device__ __forceinline__ void settle_one(const LogitsArgs &a, const Node &n, i
         }
     };
     add(biased, n.bias_tok, n.bias);
-    for (int j0 = 0; many && j0 < a.bias_len; j0 += 64) {
-        const bool one = j0 + l < a.bias_len;
-        const int tok = one ? a.bias_tok[bias0 + j0 + l] : -1;
-        add(__ballot(tok >= 0), tok, one ? a.bias[bias0 + j0 + l] : 0.f);
-    }
+    if (many)
+        each_bias(a, n, bias0, [&](int tok, float y) { add(__ballot(tok >= 0), tok, y); });
     const float y = adjusted(n, z0, x, path, bias);
     // the tokens of a lane do not ascend: the second ones of all follow the first
     if (in && y > kLeast) better(later.best, {y, t});
@@ -394,8 +416,7 @@ __device__ __forceinline__ uint32_t touched_of(const LogitsArgs &a, const Node &
     };
     if (n.any) {
         add(n.token[0]), add(n.token[1]), add(n.bias_tok);
-        for (int j0 = 0; n.many_in(slice) && j0 < a.bias_len; j0 += 64)
-            add(j0 + l < a.bias_len ? a.bias_tok[bias0 + j0 + l] : -1);
+        if (n.many_in(slice)) each_bias(a, n, bias0, [&](int t, float) { add(t); });
     }
     return bits & mask;
 }
@@ -446,11 +467,7 @@ __device__ __forceinline__ void slice_of(const LogitsArgs &a, const Node &n, int
             }
         };
         add(biased, n.bias_tok, n.bias);
-        for (int j0 = 0; many && j0 < a.bias_len; j0 += 64) {
-            const bool in = j0 + l < a.bias_len;
-            const int t = in ? a.bias_tok[bias0 + j0 + l] : -1;
-            add(inside(t), t, in ? a.bias[bias0 + j0 + l] : 0.f);
-        }
+        if (many) each_bias(a, n, bias0, [&](int t, float x) { add(inside(t), t, x); });
         if (!__any(__popc(touched) > 2)) {
             // Few tokens of a slice are touched, seldom more than one of a lane:
             // the lanes take theirs one after the other.
@@ -512,10 +529,11 @@ __device__ __forceinline__ int item_of(int block, int blocks) {
 // Loads run a slice ahead of the work.  Which of a lane's 8 tokens is the
 // largest is looked up once, at the end.
 template <typename E, typename O, bool kPutOff>
-__global__ __launch_bounds__(kMostThreads) void logits_kernel(LogitsArgs a, Cut cut) {
+__global__ __launch_bounds__(kMostThreads, kPutOff ? 6 : 4) void logits_kernel(LogitsArgs a, Cut cut) {
     typedef typename E::type T;
     __shared__ int s_later[kPutOff ? kMostThreads / 64 : 1][kPutOff ? kPutOffTokens : 1];
     __shared__ Best s_best[kMostThreads / 64];
+    extern __shared__ Biased s_biased[];
     const int l = threadIdx.x & 63;
     const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);      // the same in all lanes
     const int item = item_of((int)blockIdx.x, (int)gridDim.x);
@@ -581,6 +599,7 @@ __global__ __launch_bounds__(kMostThreads) void logits_kernel(LogitsArgs a, Cut 
     Node n;
     const int64_t bias0 = (int64_t)b * a.bias_len;
     n.bias_tok = -1, n.bias = 0.f, n.many = 0, n.first = first;
+    n.list = nullptr, n.listed = 0;
     if (l < a.bias_len && a.bias_len <= 64)
         n.bias_tok = a.bias_tok[bias0 + l], n.bias = a.bias[bias0 + l];
     int parent[2] = {-1, -1}, token[2] = {-1, -1};
@@ -614,22 +633,32 @@ __global__ __launch_bounds__(kMostThreads) void logits_kernel(LogitsArgs a, Cut 
     }
     auto ours = [&](int t) { return t >= first * kSlice && t < end * kSlice; };
     if (a.bias_len > 64) {
+        Biased *list = s_biased + w * cut.listed;
         int held = 0;
-        uint64_t at = 0;
-        for (int j0 = 0; j0 < a.bias_len; j0 += 64) {
-            const bool in = j0 + l < a.bias_len;
-            const int t = in ? a.bias_tok[bias0 + j0 + l] : -1;
-            const int x = in ? __float_as_int(a.bias[bias0 + j0 + l]) : 0;
-            for (uint64_t hits = __ballot(ours(t)); hits; hits &= hits - 1) {
-                const int j = __builtin_ctzll(hits);
-                const int tok = __builtin_amdgcn_readlane(t, j);
-                const float bias = __int_as_float(__builtin_amdgcn_readlane(x, j));
-                at |= 1ull << (tok / kSlice - first & 63);
-                if (l == held) n.bias_tok = tok, n.bias = bias;
-                ++held;
+        uint64_t in_slices = 0;
+#pragma unroll 1
+        for (int j = l; j - l < a.bias_len; j += 64) {
+            const bool in = j < a.bias_len;
+            const Biased x = {in ? a.bias_tok[bias0 + j] : -1, in ? a.bias[bias0 + j] : 0.f};
+            const uint64_t hits = __ballot(ours(x.token));
+            const int at = held + __builtin_amdgcn_mbcnt_hi(
+                                      (uint32_t)(hits >> 32),
+                                      __builtin_amdgcn_mbcnt_lo((uint32_t)hits, 0));
+            if (ours(x.token)) {
+                if (at < cut.listed) list[at] = x;
+                in_slices |= 1ull << (x.token / kSlice - first & 63);
             }
+            held += __popcll(hits);
         }
-        if (held > 64) n.many = at, n.bias_tok = -1;
+        heads::exchange();
+        if (held > 64) {
+            auto either = [](int x, int y) { return x | y; };
+            n.many = (uint64_t)(uint32_t)wave_over((int)(in_slices >> 32), either) << 32 |
+                     (uint32_t)wave_over((int)in_slices, either);
+            n.list = list, n.listed = held <= cut.listed ? held : -1;
+        } else if (l < held) {
+            n.bias_tok = list[l].token, n.bias = list[l].bias;
+        }
     }
     n.any = n.many != 0 || __any(ours(n.token[0]) || ours(n.token[1]) || ours(n.bias_tok));
     if (a.status && part == 0 && i == 0 && threadIdx.x == 0) a.status[b] = fault;
@@ -758,6 +787,7 @@ Cut cut_of(const LogitsArgs &a) {
     waves = (c.slices + c.per - 1) / c.per;
     c.parts = waves <= 16 ? 1 : (int)((waves + 3) / 4);
     c.threads = 64 * (waves > 16 ? 4 : waves > 4 ? ((int)waves + 3) / 4 * 4 : (int)waves);
+    c.listed = a.bias_len <= 64 ? 0 : a.bias_len < kListed ? a.bias_len : kListed;
     return c;
 }
 
@@ -765,10 +795,11 @@ template <typename E, typename O>
 hipError_t launch(const LogitsArgs &a, hipStream_t s) {
     const Cut c = cut_of(a);
     const dim3 grid((unsigned)(a.batch * a.n * c.parts)), block((unsigned)c.threads);
+    const unsigned lds = (unsigned)(c.threads / 64 * c.listed * (int)sizeof(Biased));
     if (__is_same(O, None) && c.per >= kPutOffSlices)
-        hipLaunchKernelGGL((logits_kernel<E, O, __is_same(O, None)>), grid, block, 0, s, a, c);
+        hipLaunchKernelGGL((logits_kernel<E, O, __is_same(O, None)>), grid, block, lds, s, a, c);
     else
-        hipLaunchKernelGGL((logits_kernel<E, O, false>), grid, block, 0, s, a, c);
+        hipLaunchKernelGGL((logits_kernel<E, O, false>), grid, block, lds, s, a, c);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !a.best || c.parts == 1) return e;
     hipLaunchKernelGGL(logits_join_kernel, dim3((unsigned)(a.batch * a.n)), dim3(64), 0, s, a,
