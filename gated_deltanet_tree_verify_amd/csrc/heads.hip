@@ -8,7 +8,13 @@
 //            (y_{2i}, y_{2i+1}), by the angle p f_i:
 //            (y, y') -> scale (y cos - y' sin, y' cos + y sin)
 // Every element is read once and written once (a key that also goes to its
-// page: twice); 3 flops a rotated element and 4 a normed one.
+// page: twice); 3 flops a rotated element and 4 a normed one: memory bounds long
+// calls, the chain of dependent loads (place, page, angle, head) short ones.
+//   8192 rows of 40 heads of 128, bf16: rotation (half of each, 27 us in a loop over
+//     one input set) and norm with rotation (29 us): 36 and 40 us among other
+//     passes, 4.6 and 4.2 TB/s; a copy of the same bytes 33 us
+//   the same into pages of 64, 8 more heads of values, ragged: 59 us, a copy 46
+//   one row: 3.4 us, with a norm 4.2, into its page 5.3
 #include "heads.hpp"
 
 namespace gdn {

@@ -617,8 +617,9 @@ gdn_status gdn_count_commit(int16_t *counts, int64_t stride,
  *           t % 32 of word t / 32 is set where t is allowed
  * Faults, per sequence (its out rows are NaN, its best -1):
  * GDN_FAULT_BAD_PARENT, _BAD_SLOT.
- * workspace: gdn_adjust_logits_workspace(...) bytes, 16-byte aligned, contents
- * ignored; one call at a time may use it (best = NULL: none).
+ * workspace: gdn_adjust_logits_workspace(...) bytes (0 for some sizes: NULL is
+ * then enough), 16-byte aligned, contents ignored; one call at a time may use it
+ * (best = NULL: none).
  */
 int64_t gdn_adjust_logits_workspace(int batch, int n, int vocab);
 gdn_status gdn_adjust_logits(const void *logits, gdn_dtype dtype,
