@@ -235,7 +235,13 @@ struct Raw {
             w[i] = E::two_bits(y[2 * i], y[2 * i + 1]);
         x = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    __device__ __forceinline__ void store(uint16_t *p) const { *reinterpret_cast<uint4 *>(p) = x; }
+    // Written once, past the lines of the L2 that are still to be read: 8192 rows of
+    // 40 heads, rotation 35.9 -> 29.6 us, with a norm 39.9 -> 33.4, ragged into pages
+    // 59.2 -> 53.4 (loads that pass it too: 32.2, 35.0, 52.9)
+    __device__ __forceinline__ void store(uint16_t *p) const {
+        typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+        __builtin_nontemporal_store(u32x4{x.x, x.y, x.z, x.w}, reinterpret_cast<u32x4 *>(p));
+    }
 };
 template <>
 struct Raw<F32> {
@@ -253,6 +259,10 @@ struct Raw<F32> {
         for (int i = 0; i < 4; ++i) x[i] = y[i], z[i] = y[4 + i];
     }
     __device__ __forceinline__ void store(float *p) const {
+        __builtin_nontemporal_store(x, reinterpret_cast<f32x4 *>(p));
+        __builtin_nontemporal_store(z, reinterpret_cast<f32x4 *>(p + 4));
+    }
+    __device__ __forceinline__ void put(float *p) const {         // to LDS
         *reinterpret_cast<f32x4 *>(p) = x;
         *reinterpret_cast<f32x4 *>(p + 4) = z;
     }
@@ -532,7 +542,7 @@ __global__ __launch_bounds__(kThreads) void pieces_kernel(Pieces n) {
                     if (pl.turns[e]) {
                         Raw<F32> r;
                         r.narrow(y[e]);
-                        r.store(mate + pl.at[e]);
+                        r.put(mate + pl.at[e]);
                     }
                 exchange();
 #pragma unroll
