@@ -56,6 +56,9 @@ struct __attribute__((packed, aligned(4))) Full8 {
     float x[8];
 };
 
+typedef uint32_t Half8Vector __attribute__((ext_vector_type(4), aligned(2)));
+typedef float Full4Vector __attribute__((ext_vector_type(4), aligned(4)));
+
 template <typename E>
 struct Eight {
     Half8 raw;
@@ -76,6 +79,10 @@ struct Eight {
         for (int i = 0; i < 4; ++i) raw.x[i] = E::two_bits(y[2 * i], y[2 * i + 1]);
     }
     __device__ __forceinline__ void store(uint16_t *p) const { *reinterpret_cast<Half8 *>(p) = raw; }
+    __device__ __forceinline__ void store_once(uint16_t *p) const {
+        const Half8Vector x = {raw.x[0], raw.x[1], raw.x[2], raw.x[3]};
+        __builtin_nontemporal_store(x, reinterpret_cast<Half8Vector *>(p));
+    }
     __device__ __forceinline__ void store(uint16_t *p, int n) const {
 #pragma unroll
         for (int i = 0; i < kLane; ++i)
@@ -97,7 +104,13 @@ struct Eight<F32> {
 #pragma unroll
         for (int i = 0; i < kLane; ++i) raw.x[i] = y[i];
     }
-    __device__ __forceinline__ void store(float *p) const { *reinterpret_cast<Full8 *>(p) = raw; }
+    __device__ __forceinline__ void store_once(float *p) const {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const Full4Vector x = {raw.x[4 * k], raw.x[4 * k + 1], raw.x[4 * k + 2], raw.x[4 * k + 3]};
+            __builtin_nontemporal_store(x, reinterpret_cast<Full4Vector *>(p) + k);
+        }
+    }
     __device__ __forceinline__ void store(float *p, int n) const {
 #pragma unroll
         for (int i = 0; i < kLane; ++i)
@@ -520,7 +533,7 @@ __device__ __forceinline__ void slice_of(const LogitsArgs &a, const Node &n, int
         Eight<O> r;
         r.set(y);
         if ((slice + 1) * kSlice > a.vocab) r.store(o, left);
-        else r.store(o);
+        else r.store_once(o);
     }
     float top = y[0];
 #pragma unroll
