@@ -11,9 +11,9 @@
 // page: twice); 3 flops a rotated element and 4 a normed one: memory bounds long
 // calls, the chain of dependent loads (place, page, angle, head) short ones.
 //   8192 rows of 40 heads of 128, bf16: rotation (half of each, 27 us in a loop over
-//     one input set) and norm with rotation (29 us): 36 and 40 us among other
-//     passes, 4.6 and 4.2 TB/s; a copy of the same bytes 33 us
-//   the same into pages of 64, 8 more heads of values, ragged: 59 us, a copy 46
+//     one input set) and norm with rotation (29 us): 29 and 32 us among other
+//     passes, 5.7 and 5.3 TB/s; a copy of the same bytes 33 us
+//   the same into pages of 64, 8 more heads of values, ragged: 53 us, a copy 46
 //   one row: 3.4 us, with a norm 4.2, into its page 5.3
 #include "heads.hpp"
 
@@ -575,7 +575,7 @@ __global__ __launch_bounds__(kThreads) void pieces_kernel(Pieces n) {
 }
 
 // whether rows, heads and weights are in 16-byte pieces.  8192 rows of 40 heads
-// with a norm: 41 us (d 80, rot 20) and 40 (96, 24) in pieces, 133 and 156 without.
+// with a norm: 33 us (d 80, rot 20; 96, 24) in pieces, 133 and 156 without.
 bool in_pieces(const HeadsArgs &a) {
     const int step = a.dtype == GDN_DTYPE_F32 ? 4 : 8;
     if (a.d % 8 != 0) return false;

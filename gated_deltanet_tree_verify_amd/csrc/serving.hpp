@@ -102,8 +102,8 @@ struct AppendArgs {
 
 // waves that share a row's heads: a launch of few rows splits them, until there
 // are as many waves as the chip holds (one row of 18 heads of 256: 4.3 us split,
-// 6.6 in one wave; 1024 rows of 40 heads of 128: 8.0 and 9.2; 8192 rows: 36 us in
-// one wave, the same in two, 42 and more in four)
+// 6.6 in one wave; 1024 rows of 40 heads of 128: 8.0 and 9.2; before results passed
+// the L2's other lines, 8192 rows: 36 us in one wave, the same in two, 42 in four)
 constexpr int heads_splits(int rows, int heads) {
     if (heads < 1) return 1;
     const int want = rows >= 8192 ? 1 : 8192 / (rows < 1 ? 1 : rows);
