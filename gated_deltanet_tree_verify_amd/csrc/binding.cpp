@@ -407,12 +407,16 @@ PyObject *whole_call(PyObject *const *args, Py_ssize_t n, Py_ssize_t expected, F
     Py_RETURN_NONE;
 }
 
-#define LAUNCH(call)                 \
-    do {                             \
-        Py_BEGIN_ALLOW_THREADS       \
-        status = (call);             \
-        Py_END_ALLOW_THREADS         \
-    } while (0)
+// fn(x...) while other threads may have the interpreter.  The arguments are
+// formed before that: a tensor without storage raises for its address.
+template <typename... P, typename... A>
+int unlocked(gdn_status (*fn)(P...), A... x) {
+    gdn_status status;
+    Py_BEGIN_ALLOW_THREADS
+    status = fn(x...);
+    Py_END_ALLOW_THREADS
+    return status;
+}
 
 // (norm, q, k, q_weight, k_weight, pos, base, inv_freq, eps, offset, layout,
 // scale, q_out, k_out, stream); norm 0: gdn_rope
@@ -460,12 +464,12 @@ bool run_heads(PyObject *const *o, int &status) {
         !narrow(rq.heads) || !narrow(rk.heads) || !narrow(rq.d) || layout > 1 || norm > 2)
         return false;
     const bool wide = wq ? wq->scalar_type() == at::kFloat : wk && wk->scalar_type() == at::kFloat;
-    LAUNCH(gdn_qk_norm_rope(
-        data(q), rq.stride, rq.head, data(k), rk.stride, rk.head, dtype, static_cast<gdn_norm>(norm),
-        eps, offset, data(wq), wq_head, data(wk), wk_head, wide ? GDN_DTYPE_F32 : dtype,
+    status = unlocked(
+        gdn_qk_norm_rope, data(q), rq.stride, rq.head, data(k), rk.stride, rk.head, dtype,
+        static_cast<gdn_norm>(norm), eps, offset, data(wq), wq_head, data(wk), wk_head, wide ? GDN_DTYPE_F32 : dtype,
         data<int32_t>(pos), data<int32_t>(base), (int)base_rows, data<float>(f), (int)rot,
         static_cast<gdn_rope_layout>(layout), scale, data(q_out), oq.stride, oq.head, data(k_out),
-        ok.stride, ok.head, (int)rq.count, (int)rq.heads, (int)rk.heads, (int)rq.d, in.stream));
+        ok.stride, ok.head, (int)rq.count, (int)rq.heads, (int)rk.heads, (int)rq.d, in.stream);
     return true;
 }
 
@@ -534,15 +538,15 @@ bool run_append(PyObject *const *o, int &status) {
                       page[1]})
         if (!narrow(x)) return false;
     const bool wide = wq ? wq->scalar_type() == at::kFloat : wk && wk->scalar_type() == at::kFloat;
-    LAUNCH(gdn_kv_append(
-        data(kc), data(vc), page[2], data<int32_t>(table), data<int32_t>(dst), data<int32_t>(begin),
-        data<int32_t>(cu), data(q), rq.stride, rq.head, data(k), rk.stride, rk.head, data(v),
+    status = unlocked(
+        gdn_kv_append, data(kc), data(vc), page[2], data<int32_t>(table), data<int32_t>(dst),
+        data<int32_t>(begin), data<int32_t>(cu), data(q), rq.stride, rq.head, data(k), rk.stride, rk.head, data(v),
         rv.stride, rv.head, dtype, static_cast<gdn_norm>(norm), eps, offset, data(wq), wq_head,
         data(wk), wk_head, wide ? GDN_DTYPE_F32 : dtype, data<int32_t>(pos), data<float>(f), (int)rot,
         static_cast<gdn_rope_layout>(layout), scale, data(q_out), oq.stride, oq.head, data(k_out),
         ok.stride, ok.head, (int)m, (int)rk.count, (int)rq.heads, (int)rk.heads, (int)rk.d,
         (int)table->size(0), (int)table->size(1), (int)page[0], (int)page[1], data<int32_t>(st),
-        in.stream));
+        in.stream);
     return true;
 }
 
@@ -558,9 +562,10 @@ bool run_count_prompt(PyObject *const *o, int &status) {
     const at::Tensor *st = in.plain_or_none(o[4], at::kInt, {m});
     if (!in.ok || !narrow(m) || !narrow(tokens->numel()) || !narrow(r.count) || !narrow(r.d))
         return false;
-    LAUNCH(gdn_count_prompt(data<int16_t>(counts), r.stride, data<int32_t>(slot), data<int32_t>(cu),
-                            data<int32_t>(tokens), (int)m, (int)tokens->numel(), (int)r.count,
-                            (int)r.d, data<int32_t>(st), in.stream));
+    status = unlocked(
+        gdn_count_prompt, data<int16_t>(counts), r.stride, data<int32_t>(slot), data<int32_t>(cu),
+        data<int32_t>(tokens), (int)m, (int)tokens->numel(), (int)r.count, (int)r.d,
+        data<int32_t>(st), in.stream);
     return true;
 }
 
@@ -579,10 +584,11 @@ bool run_count_commit(PyObject *const *o, int &status) {
         path->size(0) != m || !narrow(m) || !narrow(tokens->size(1)) || !narrow(path->size(1)) ||
         !narrow(r.count) || !narrow(r.d))
         return false;
-    LAUNCH(gdn_count_commit(data<int16_t>(counts), r.stride, data<int32_t>(slot),
-                            data<int32_t>(tokens), data<int32_t>(path), data<int32_t>(add), (int)m,
-                            (int)tokens->size(1), (int)path->size(1), (int)r.count, (int)r.d,
-                            data<int32_t>(st), in.stream));
+    status = unlocked(
+        gdn_count_commit, data<int16_t>(counts), r.stride, data<int32_t>(slot),
+        data<int32_t>(tokens), data<int32_t>(path), data<int32_t>(add), (int)m,
+        (int)tokens->size(1), (int)path->size(1), (int)r.count, (int)r.d, data<int32_t>(st),
+        in.stream);
     return true;
 }
 
@@ -640,13 +646,13 @@ bool run_logits(PyObject *const *o, int &status) {
     if (!in.ok) return false;
     for (int64_t x : {batch, n, rz.d, rc.count, biases})
         if (!narrow(x)) return false;
-    LAUNCH(gdn_adjust_logits(
-        data(z), dtype, rz.stride, data<int16_t>(counts), rc.stride, data<int32_t>(slot),
-        (int)rc.count, data<int32_t>(tokens), data<int32_t>(parent), data<float>(penalty[0]),
+    status = unlocked(
+        gdn_adjust_logits, data(z), dtype, rz.stride, data<int16_t>(counts), rc.stride,
+        data<int32_t>(slot), (int)rc.count, data<int32_t>(tokens), data<int32_t>(parent), data<float>(penalty[0]),
         data<float>(penalty[1]), data<float>(penalty[2]), data<int32_t>(bias_tok), data<float>(bias),
         (int)biases, data<int32_t>(mask), (int)mask_rows, data(out), out_dtype, ro.stride,
         data<int32_t>(best), (int)batch, (int)n, (int)rz.d, data(room), room->numel(),
-        data<int32_t>(st), in.stream));
+        data<int32_t>(st), in.stream);
     return true;
 }
 
