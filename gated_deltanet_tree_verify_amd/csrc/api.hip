@@ -83,6 +83,14 @@ bool apart(int rows, int64_t row, int heads, int64_t head, int d) {
            (row >= d && head >= d && (head - d) / row >= rows - 1);
 }
 
+// What a call does not use may be anything: it goes before the checks, so that no
+// kernel sees it.
+gdn::HeadsArgs used(gdn::HeadsArgs a) {
+    for (gdn::HeadsPart *x : {&a.q, &a.k})
+        if (x->heads == 0) x->weight = nullptr;
+    return a;
+}
+
 gdn_status part_status(const gdn::HeadsPart &x, const gdn::HeadsArgs &a, bool out_needed) {
     if (x.heads == 0) return GDN_OK;
     if (!x.in || (out_needed && !x.out)) return GDN_ERR_INVALID_ARG;
@@ -559,11 +567,11 @@ gdn_status gdn_qk_norm_rope(const void *q, int64_t q_row, int64_t q_head, const 
                             void *q_out, int64_t q_out_row, int64_t q_out_head, void *k_out,
                             int64_t k_out_row, int64_t k_out_head, int rows, int Hq, int Hk, int d,
                             void *stream) {
-    const gdn::HeadsArgs a{
-        {q, q_row, q_head, q_out, q_out_row, q_out_head, q_weight, q_weight_head, Hq},
-        {k, k_row, k_head, k_out, k_out_row, k_out_head, k_weight, k_weight_head, Hk},
-        dtype, weight_dtype == GDN_DTYPE_F32, norm, eps, offset, pos, base, base_rows, inv_freq,
-        rot, layout, scale, rows, d};
+    const gdn::HeadsArgs a = used(
+        {{q, q_row, q_head, q_out, q_out_row, q_out_head, q_weight, q_weight_head, Hq},
+         {k, k_row, k_head, k_out, k_out_row, k_out_head, k_weight, k_weight_head, Hk},
+         dtype, weight_dtype == GDN_DTYPE_F32, norm, eps, offset, pos, base, base_rows, inv_freq,
+         rot, layout, scale, rows, d});
     const gdn_status st = heads_status(a, weight_dtype, true, true);
     if (st != GDN_OK || rows == 0) return st;
     // a wave a row, or as many as share its heads
@@ -597,10 +605,10 @@ gdn_status gdn_kv_append(void *k_cache, void *v_cache, int64_t page_stride, cons
                          int d, int seqs, int max_pages, int pool, int page, int32_t *status,
                          void *stream) {
     const gdn::AppendArgs a{
-        {{q, q_row, q_head, q_out, q_out_row, q_out_head, q_weight, q_weight_head, Hq},
-         {k, k_row, k_head, k_out, k_out_row, k_out_head, k_weight, k_weight_head, Hkv},
-         dtype, weight_dtype == GDN_DTYPE_F32, norm, eps, offset, pos, nullptr, 1, inv_freq, rot,
-         layout, scale, rows, d},
+        used({{q, q_row, q_head, q_out, q_out_row, q_out_head, q_weight, q_weight_head, Hq},
+              {k, k_row, k_head, k_out, k_out_row, k_out_head, k_weight, k_weight_head, Hkv},
+              dtype, weight_dtype == GDN_DTYPE_F32, norm, eps, offset, pos, nullptr, 1, inv_freq,
+              rot, layout, scale, rows, d}),
         v, v_row, v_head, k_cache, v_cache, page_stride, table, dst, begin, cu, m, seqs, max_pages,
         pool, log2_exact(page), status};
     if (m < 0 || Hkv < 1 || seqs < 1 || max_pages < 1 || pool < 1 || page < 1)

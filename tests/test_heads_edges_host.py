@@ -75,3 +75,49 @@ def test_a_tensor_without_an_address_raises(case):
                           capture_output=True, timeout=300)
     assert done.returncode == 0 and done.stdout.strip() == "raised", (done.returncode, done.stdout,
                                                                       done.stderr[-2000:])
+
+
+# ---------------------------------------------------------------------------
+# What a call does not use is not looked at.  So many rows that the launch is
+# refused (-2), after all arguments have been accepted: nothing runs.
+# ---------------------------------------------------------------------------
+FAKE = 0x10000          # an aligned address that is never dereferenced
+ODD = 0x10001
+ROWS = 1 << 30
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(g.lib_path()):
+        g.build()
+    return g.load()
+
+
+def norm(lib, kind=1, Hq=4, Hk=2, wq=FAKE, wq_head=0, wk=FAKE, wk_head=0, w_dtype=1, pos=FAKE, base=None,
+         base_rows=1, f=FAKE, rot=64, rows=ROWS):
+    return lib.gdn_qk_norm_rope(FAKE, 384, 64, FAKE, 384, 64, 1, kind, 1e-6, 0.0, wq, wq_head, wk,
+                                wk_head, w_dtype, pos, base, base_rows, f, rot, 0, 1.0, FAKE, 256, 64,
+                                FAKE, 128, 64, rows, Hq, Hk, 64, None)
+
+
+def append(lib, kind=1, Hq=4, wq=FAKE, wq_head=0, wk=FAKE, wk_head=0, w_dtype=1, pos=FAKE, f=FAKE,
+           rot=64, rows=ROWS):
+    return lib.gdn_kv_append(FAKE, FAKE, 2 * 16 * 64, FAKE, FAKE, FAKE, FAKE, FAKE, 512, 64, FAKE, 512,
+                             64, FAKE, 512, 64, 1, kind, 1e-6, 0.0, wq, wq_head, wk, wk_head, w_dtype,
+                             pos, f, rot, 0, 1.0, FAKE, 256, 64, None, 0, 0, 3, rows, Hq, 2, 64, 4, 4, 8,
+                             16, None, None)
+
+
+def test_all_in_order_but_the_rows(lib):
+    assert norm(lib) == -2 and append(lib) == -2
+    assert norm(lib, wq=ODD) == -1 and append(lib, wk=ODD) == -1
+
+
+def test_weights_of_a_part_without_heads_are_not_looked_at(lib):
+    """its pointers are ignored, and so is the type that only they would have"""
+    stale = dict(w_dtype=2, wq_head=7)
+    assert norm(lib, wk=None, **stale) == -1                  # queries have heads: another type
+    for q in (FAKE, ODD):
+        assert norm(lib, Hq=0, wq=q, wk=None, **stale) == -2
+        assert append(lib, Hq=0, wq=q, wk=None, **stale) == -2
+        assert norm(lib, Hk=0, wk=q, wq=None, w_dtype=2, wk_head=7) == -2
