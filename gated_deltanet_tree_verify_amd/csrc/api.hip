@@ -88,6 +88,7 @@ bool apart(int rows, int64_t row, int heads, int64_t head, int d) {
 gdn::HeadsArgs used(gdn::HeadsArgs a) {
     for (gdn::HeadsPart *x : {&a.q, &a.k})
         if (x->heads == 0) x->weight = nullptr;
+    if (a.rot == 0) a.pos = a.base = nullptr, a.inv_freq = nullptr;
     return a;
 }
 

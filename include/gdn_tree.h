@@ -515,8 +515,8 @@ gdn_status gdn_rope(const void *q, int64_t q_row, int64_t q_head,
  *   L2   x / sqrt(sum x^2 + eps) (offset + w)
  * q_weight, k_weight: [d], or [H][d] with q_weight_head = d (0: one for all
  * heads), in the heads' type or fp32 (weight_dtype); NULL: the factor
- * (offset + w) is left out.  rot = 0 (pos and inv_freq are then ignored): the
- * norm alone.  Squares are summed in fp32: values past 2^60 overflow the sum.
+ * (offset + w) is left out.  rot = 0 (pos, base and inv_freq are then ignored):
+ * the norm alone.  Squares are summed in fp32: values past 2^60 overflow the sum.
  * GDN_NORM_NONE: gdn_rope.
  */
 gdn_status gdn_qk_norm_rope(const void *q, int64_t q_row, int64_t q_head,

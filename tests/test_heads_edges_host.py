@@ -121,3 +121,13 @@ def test_weights_of_a_part_without_heads_are_not_looked_at(lib):
         assert norm(lib, Hq=0, wq=q, wk=None, **stale) == -2
         assert append(lib, Hq=0, wq=q, wk=None, **stale) == -2
         assert norm(lib, Hk=0, wk=q, wq=None, w_dtype=2, wk_head=7) == -2
+
+
+def test_positions_without_a_rotation_are_not_looked_at(lib):
+    for fn in (norm, append):
+        for kw in (dict(pos=ODD), dict(f=ODD)):
+            assert fn(lib, **kw) == -1
+            assert fn(lib, rot=0, **kw) == -2
+        assert fn(lib, rot=0, pos=None, f=None) == -2
+    assert norm(lib, base=ODD) == -1 and norm(lib, base=FAKE, base_rows=0) == -1
+    assert norm(lib, rot=0, base=ODD) == -2 and norm(lib, rot=0, base=FAKE, base_rows=0) == -2
