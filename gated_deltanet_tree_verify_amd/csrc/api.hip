@@ -86,8 +86,10 @@ bool apart(int rows, int64_t row, int heads, int64_t head, int d) {
 // What a call does not use may be anything: it goes before the checks, so that no
 // kernel sees it.
 gdn::HeadsArgs used(gdn::HeadsArgs a) {
-    for (gdn::HeadsPart *x : {&a.q, &a.k})
+    for (gdn::HeadsPart *x : {&a.q, &a.k}) {
         if (x->heads == 0) x->weight = nullptr;
+        if (!x->weight) x->weight_head = 0;
+    }
     if (a.rot == 0) a.pos = a.base = nullptr, a.inv_freq = nullptr;
     return a;
 }
