@@ -87,7 +87,7 @@ bool apart(int rows, int64_t row, int heads, int64_t head, int d) {
 // kernel sees it.
 gdn::HeadsArgs used(gdn::HeadsArgs a) {
     for (gdn::HeadsPart *x : {&a.q, &a.k}) {
-        if (x->heads == 0) x->weight = nullptr;
+        if (x->heads == 0 || a.norm == GDN_NORM_NONE) x->weight = nullptr;
         if (!x->weight) x->weight_head = 0;
     }
     if (a.rot == 0) a.pos = a.base = nullptr, a.inv_freq = nullptr;

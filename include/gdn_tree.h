@@ -517,7 +517,7 @@ gdn_status gdn_rope(const void *q, int64_t q_row, int64_t q_head,
  * heads), in the heads' type or fp32 (weight_dtype); NULL: the factor
  * (offset + w) is left out.  rot = 0 (pos, base and inv_freq are then ignored):
  * the norm alone.  Squares are summed in fp32: values past 2^60 overflow the sum.
- * GDN_NORM_NONE: gdn_rope.
+ * GDN_NORM_NONE: gdn_rope, weights are ignored.
  */
 gdn_status gdn_qk_norm_rope(const void *q, int64_t q_row, int64_t q_head,
                             const void *k, int64_t k_row, int64_t k_head,

@@ -131,3 +131,11 @@ def test_positions_without_a_rotation_are_not_looked_at(lib):
         assert fn(lib, rot=0, pos=None, f=None) == -2
     assert norm(lib, base=ODD) == -1 and norm(lib, base=FAKE, base_rows=0) == -1
     assert norm(lib, rot=0, base=ODD) == -2 and norm(lib, rot=0, base=FAKE, base_rows=0) == -2
+
+
+def test_weights_without_a_norm_are_not_looked_at(lib):
+    """GDN_NORM_NONE is gdn_rope, which has none"""
+    for fn in (norm, append):
+        for kw in (dict(wq=ODD), dict(wk=ODD), dict(wq_head=7), dict(wk_head=7)):
+            assert fn(lib, **kw) == -1
+            assert fn(lib, kind=0, **kw) == -2
