@@ -495,9 +495,9 @@ gdn_status gdn_rope_frequencies(int rot, double base, gdn_rope_scaling scaling,
  * ignored).  pos int32 [rows], base int32 [ceil(rows / base_rows)], inv_freq
  * fp32 [rot / 2] (device memory).  0 <= rot <= d <= GDN_MAX_HEAD_DIM, rot
  * even, rot = 0: a copy.
- * Arithmetic: the angle is the product of position and frequency, exact to
- * 2^-53, reduced in 64 bits: far positions are as good as near ones.  cos, sin
- * and the turn in fp32, one rounding of the result.
+ * Arithmetic: position times frequency, whole turns taken off, is exact to
+ * 2^-50 of a turn: far positions are as good as near ones.  cos, sin and the
+ * turn in fp32, one rounding of the result.
  */
 gdn_status gdn_rope(const void *q, int64_t q_row, int64_t q_head,
                     const void *k, int64_t k_row, int64_t k_head,
