@@ -75,6 +75,7 @@ DTYPE_F16 = 2     # pseudo-values of commit_verify, tree_attention, rope and aft
 MAX_NODES = 128
 MAX_DIM = 128
 MAX_CANDIDATES = 32
+MAX_HEAD_DIM = 256
 # GDN_TREE_ABI_VERSION of include/gdn_tree.h that the signatures below follow
 ABI_VERSION = 10
 
@@ -873,10 +874,12 @@ def rope_frequencies(rot, base=10000.0, scaling=None, factor=1.0, original=0, lo
     less.  Computed on the host: made once, kept by the program."""
     torch = _torch()
     kind = _choice(scaling, "scaling", _SCALINGS)
-    host = torch.empty(max(1, int(rot) // 2), dtype=torch.float32)
+    # ctypes would cut a larger number to its low 32 bits
+    rot = min(max(int(rot), 0), MAX_HEAD_DIM + 2)
+    host = torch.empty(max(1, rot // 2), dtype=torch.float32)
     magnitude = ctypes.c_float()
     _check("gdn_rope_frequencies", load().gdn_rope_frequencies(
-        int(rot), float(base), kind, float(factor), float(original), float(low), float(high),
+        rot, float(base), kind, float(factor), float(original), float(low), float(high),
         host.data_ptr(), ctypes.addressof(magnitude)))
     return host.to(device), magnitude.value
 

@@ -139,3 +139,11 @@ def test_weights_without_a_norm_are_not_looked_at(lib):
         for kw in (dict(wq=ODD), dict(wk=ODD), dict(wq_head=7), dict(wk_head=7)):
             assert fn(lib, **kw) == -1
             assert fn(lib, kind=0, **kw) == -2
+
+
+@pytest.mark.parametrize("rot", [2 ** 32 + 64, 2 ** 31, 2 ** 40 + 2, 258, -2 ** 32 + 64, -2, 0, 63])
+def test_frequencies_of_sizes_that_no_head_has(rot):
+    """refused, whatever their low 32 bits are"""
+    pytest.importorskip("torch")
+    with pytest.raises(g.GdnError):
+        g.rope_frequencies(rot, device="cpu")
