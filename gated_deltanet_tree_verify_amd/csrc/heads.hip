@@ -77,7 +77,6 @@ struct Head {
     }
 };
 
-template <typename E>
 __device__ __forceinline__ void angles(const HeadsArgs &g, int64_t p, float2 (&cs)[kPairs]) {
     const int l = threadIdx.x & 63;
 #pragma unroll
@@ -104,7 +103,7 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadsArgs a, int splits
     if (row >= a.rows) return;
     float2 cs[kPairs] = {};
     if (a.rot > 0)
-        angles<E>(a, (int64_t)a.pos[row] + (a.base ? a.base[row / a.base_rows] : 0), cs);
+        angles(a, (int64_t)a.pos[row] + (a.base ? a.base[row / a.base_rows] : 0), cs);
     for (int h = (int)(unit % splits); h < a.q.heads + a.k.heads; h += splits) {
         const bool k = h >= a.q.heads;
         const HeadsPart &x = k ? a.k : a.q;
@@ -144,7 +143,7 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs a, int spli
     const HeadsArgs &g = a.h;
     const int place = q.at + t;
     float2 cs[kPairs] = {};
-    if (g.rot > 0 && !lost) angles<E>(g, g.pos ? g.pos[row] : place, cs);
+    if (g.rot > 0 && !lost) angles(g, g.pos ? g.pos[row] : place, cs);
     size_t cell = 0;
     if (!lost) {
         const int p = a.table[(size_t)q.row * a.width + (place >> a.page_log)];
@@ -329,7 +328,7 @@ struct Place {
 };
 
 template <Mode kMode>
-__device__ __forceinline__ Place place_of(const HeadsArgs &g, int lane, int need, int log) {
+__device__ __forceinline__ Place place_of(const HeadsArgs &g, int lane, int need) {
     Place p;
     const int c = min(lane, need - 1);
     if (kMode == kSplit) {
@@ -403,7 +402,7 @@ __global__ __launch_bounds__(kThreads) void pieces_kernel(Pieces n) {
         }
         if (bad) return;
     }
-    const Place pl = place_of<kMode>(g, l & ((1 << n.log) - 1), n.need, n.log);
+    const Place pl = place_of<kMode>(g, l & ((1 << n.log) - 1), n.need);
     const int mine = l >> n.log, per = 64 >> n.log;      // the lane's head of a group's
     const int tile = (int)blockIdx.x / n.splits, split = (int)blockIdx.x % n.splits;
     const int keys = n.part[1].before, values = n.part[2].before;
