@@ -871,7 +871,10 @@ def rope_frequencies(rot, base=10000.0, scaling=None, factor=1.0, original=0, lo
     that rope's scale takes.  scaling: None, "linear", "ntk", "parts" or "yarn",
     by `factor`; the last two leave pairs alone that turn `high` times or more
     within the `original` context, and divide those that turn `low` times or
-    less.  Computed on the host: made once, kept by the program."""
+    less, with a share that is linear in the turns between.  (Some models called
+    "yarn" were run with a share that is linear in the pairs' indices: they need
+    their own table, which rope takes as well.)  Computed on the host: made once,
+    kept by the program."""
     torch = _torch()
     kind = _choice(scaling, "scaling", _SCALINGS)
     # ctypes would cut a larger number to its low 32 bits

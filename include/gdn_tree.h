@@ -475,6 +475,10 @@ gdn_status gdn_kv_commit(void *k_cache, void *v_cache, int64_t page_stride,
  *          g = (n - low) / (high - low), cut to [0, 1]
  *   YARN   the same, magnitude 0.1 ln(factor) + 1 (1 elsewhere)
  * (low = 1 and high = 32 are usual.)  Any other table can be used as well.
+ * YARN's g runs over the turns n, as published for it.  Some models that go by
+ * that name were run with a g that runs over the pairs' indices, between two
+ * rounded ones: their middle frequencies are others, and such a model needs its
+ * own table.
  * Computed in 64 bits, rounded once.  2 <= rot <= GDN_MAX_HEAD_DIM, even;
  * base > 1; factor >= 1; original, low, high (low < high) are read by PARTS
  * and YARN only.
