@@ -18,7 +18,8 @@
 // token.  So the loop takes maxima of eight tokens a lane, looks up at the end
 // which of the eight it was, and gives the touched ones the long way.
 //   16 trees of 32 nodes, 131072 tokens, bf16, masks, counts of 1200 tokens:
-//     41 us, 3.6 TB/s (touched tokens in their slices: 48); without counts and masks 30
+//     41 us, 3.6 TB/s (touched tokens in their slices: 48), vector units active 79 % of
+//     the time; without counts and masks 30
 //   64 rows of 100003 tokens, bf16 read and written, counts of 1500: 13 us and
 //     4 us of joining the parts; one row of 32000: 5 and 2 us
 //   the trees with a hundredth, a tenth, all of the vocabulary counted: 47, 87,
@@ -255,7 +256,10 @@ struct Biased {
     float bias;
 };
 
-constexpr int kListed = 432;     // the lists of 16 waves and the rest stay below 64 KiB
+// Biases of a wave's list: the lists of 16 waves and the rest stay below 64 KiB.  With
+// more of them the sequence's are gone over in memory for every slice (one wave a node,
+// 32000 tokens, 8192 nodes: 432 biases 0.9 ms, 1000 3.6, 4096 154).
+constexpr int kListed = 432;
 
 // What a wave knows of its node.
 struct Node {
